@@ -483,6 +483,118 @@ ssdq_status ssdq_frontend_step(void* conv_state, const void* xbc, const float* c
                                int32_t batch, int32_t nheads, int32_t headdim, int32_t dstate, int32_t ngroups,
                                hipStream_t stream);
 
+/* Element types of the gated scan and of activation checkpoints. */
+typedef enum {
+  SSDQ_DTYPE_F32 = 0,   /* binary32 */
+  SSDQ_DTYPE_F16 = 1,   /* IEEE binary16 */
+  SSDQ_DTYPE_BF16 = 2   /* bfloat16 */
+} ssdq_dtype;
+
+/* Channels that share one scale of an 8-bit activation checkpoint. */
+#define SSDQ_CHECKPOINT_BLOCK 64
+
+/*
+ * 8-bit activation checkpoint: an activation kept between the forward and the backward pass as one
+ * signed code per element and one binary32 scale per 64 consecutive channels of a row (1.0625
+ * bytes per element), by the max/127 rule of the 8-bit decode state.
+ *
+ *   m[r,k]     = max over i in block k of |x[r,i]|
+ *   scale[r,k] = m * (1/127), one product of binary32 numbers, 1/127 rounded to binary32 (within
+ *                2^-23 of m / 127); 0, with zero codes, when m < 127 * 2^-126
+ *   codes[r,i] = the integer nearest to the exact quotient x[r,i] / scale[r,k], ties to even
+ *                (within [-127, 127]; -128 is never produced)
+ * A block that holds a NaN or an infinity gets the scale NaN and zero codes, so that it reads back
+ * as NaN and the fault is not hidden.
+ *   dtype : ssdq_dtype of x          x : (rows, channels)
+ *   codes : (rows, channels) int8, written     scale : (rows, ceil(channels / 64)) fp32, written
+ * Any rows >= 0 (0 = no-op) and channels >= 1 (the last block of a row may be partial) with
+ * rows * ceil(channels / 64) < 2^36; else SSDQ_ERROR_UNSUPPORTED.  No output overlaps x.
+ */
+ssdq_status ssdq_checkpoint_save(int32_t dtype, const void* x, int8_t* codes, float* scale, int64_t rows,
+                                 int32_t channels, hipStream_t stream);
+
+/*
+ * The values of an 8-bit checkpoint: x[r,i] = codes[r,i] * scale[r,k], formed in binary32 and rounded
+ * once to dtype.  Arguments and limits as ssdq_checkpoint_save; codes of -128 read as such.
+ */
+ssdq_status ssdq_checkpoint_load(int32_t dtype, const int8_t* codes, const float* scale, void* x, int64_t rows,
+                                 int32_t channels, hipStream_t stream);
+
+/* What the gate tensor of the gated scan holds. */
+typedef enum {
+  SSDQ_GATE_LOG = 0,    /* log a:      a = exp(gate),                b = u   (-inf: a = 0) */
+  SSDQ_GATE_LOGIT = 1   /* logit of a: a = 1 / (1 + exp(-gate)),     b = (1 - a) u              */
+} ssdq_gate_kind;
+
+/* Bytes of workspace that ssdq_gated_scan and ssdq_gated_scan_backward need (host; the same for
+ * both, any dtype; packed is nonzero for calls with offsets; 0 on invalid or unsupported sizes,
+ * else at least 256). */
+size_t ssdq_gated_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t channels, int32_t packed);
+
+/*
+ * Gated linear recurrence: the recurrence h_t = Abar_t h_{t-1} + Bbar_t x_t (Ternary Mamba,
+ * Section 1) with a gate of its own for every channel,
+ *
+ *   h_t[c] = a_t[c] h_{t-1}[c] + b_t[c],   h_{-1} = h0 (or 0),   a and b from gate and u by gate_kind,
+ *
+ * over every token of every sequence, in binary32 whatever the types.
+ *   dtype   : ssdq_dtype of gate, u and h         gate, u, h : (tokens, channels); h is written
+ *   offsets : NULL: tokens = sequences * L, sequence s holds rows s*L .. s*L + L - 1 (dense).
+ *             Otherwise (sequences + 1) int32, device, nondecreasing, within [0, tokens]: sequence s
+ *             holds rows offsets[s] .. offsets[s+1] - 1 (packed; none, one or many each).  Rows in no
+ *             sequence are neither read nor written.  Offsets out of range or out of order give
+ *             unspecified results but no access outside the tensors.
+ *   h0      : (sequences, channels) fp32 or NULL (= 0)
+ *   h_final : (sequences, channels) fp32 or NULL: the state after each sequence's last token (the
+ *             unrounded one; h0 for a sequence without tokens); may alias h0
+ *   codes, scale : both NULL, or the 8-bit checkpoint of the written h (that of
+ *             ssdq_checkpoint_save(dtype, h, ...), bit for bit): (tokens, channels) int8 and
+ *             (tokens, ceil(channels / 64)) fp32
+ *   workspace : device scratch of at least ssdq_gated_scan_workspace_size() bytes, owned by the
+ *             caller, not shared with a concurrent call; it need not start at any value
+ * Any sequences >= 1, tokens >= 0, channels >= 1 with tokens < 2^31 - 2^16, tokens * channels
+ * < 2^40 and sequences * channels < 2^36 (else SSDQ_ERROR_UNSUPPORTED); dense tokens must be a
+ * multiple of sequences.  With tokens == 0 the (tokens, ...) pointers are not looked at.
+ * A NaN or infinity in gate, u or h0 makes the rows after it in its sequence and channel non-finite
+ * or NaN (a = 0 does not clear it: 0 times infinity is NaN), and nothing else.  The result does not
+ * depend on timing: calls with the same arguments give the same bits.
+ */
+ssdq_status ssdq_gated_scan(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const float* h0,
+                            const int32_t* offsets, void* h, float* h_final, int8_t* codes, float* scale,
+                            int32_t sequences, int64_t tokens, int32_t channels, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of ssdq_gated_scan.  With dh the gradient of every h_t and dh_final that of h_final,
+ *
+ *   d_t = dh_t + k_{t+1},  k_t = a_t d_t   (k after a sequence's last token: dh_final or 0)
+ *   SSDQ_GATE_LOG   : dgate_t = k_t h_{t-1}                        du_t = d_t
+ *   SSDQ_GATE_LOGIT : dgate_t = k_t (1 - a_t) (h_{t-1} - u_t)      du_t = (1 - a_t) d_t
+ *   dh0 = k of the first token (dh_final, or 0, for a sequence without tokens)
+ *
+ * where h_{t-1} is read from the saved h of the forward pass, or from its 8-bit checkpoint (codes *
+ * scale), and is h0 (or 0) for a first token.
+ *   gate, dh, dgate, du : (tokens, channels) of dtype; dgate and du are written
+ *   u       : (tokens, channels) of dtype; needed with SSDQ_GATE_LOGIT, not looked at otherwise
+ *   h       : (tokens, channels) of dtype, or NULL with codes and scale given (exactly one of them)
+ *   dh_final, dh0 : (sequences, channels) fp32 or NULL each; dh0 is written and may alias dh_final
+ * Everything else as ssdq_gated_scan.
+ */
+ssdq_status ssdq_gated_scan_backward(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const void* h,
+                                     const int8_t* codes, const float* scale, const float* h0, const void* dh,
+                                     const float* dh_final, const int32_t* offsets, void* dgate, void* du, float* dh0,
+                                     int32_t sequences, int64_t tokens, int32_t channels, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of ssdq_gated_scan for every sequence of a decode batch, the state updated in place:
+ *   state <- a state + b;   h = the updated state rounded to dtype
+ *   state : (batch, channels) fp32, read and written     gate, u, h : (batch, channels) of dtype
+ * batch, channels >= 1 with batch * channels < 2^36; no workspace.
+ */
+ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, const void* gate, const void* u, void* h,
+                            int32_t batch, int32_t channels, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

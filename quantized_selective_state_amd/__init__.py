@@ -89,6 +89,18 @@ lib.ssdq_chunk_scan_state_fused.argtypes = [_i32, _i32]
 lib.ssdq_chunk_scan_state_fused.restype = _i32
 lib.ssdq_chunk_scan_plan.argtypes = [_i32, _i32, ctypes.c_uint32]
 lib.ssdq_chunk_scan_plan.restype = _i32
+lib.ssdq_checkpoint_save.argtypes = [_i32, _P, _P, _P, _i64, _i32, _P]
+lib.ssdq_checkpoint_save.restype = ctypes.c_int
+lib.ssdq_checkpoint_load.argtypes = [_i32, _P, _P, _P, _i64, _i32, _P]
+lib.ssdq_checkpoint_load.restype = ctypes.c_int
+lib.ssdq_gated_scan_workspace_size.argtypes = [_i32, _i64, _i32, _i32]
+lib.ssdq_gated_scan_workspace_size.restype = _sz
+lib.ssdq_gated_scan.argtypes = [_i32, _i32] + [_P] * 8 + [_i32, _i64, _i32, _P, _sz, _P]
+lib.ssdq_gated_scan.restype = ctypes.c_int
+lib.ssdq_gated_scan_backward.argtypes = [_i32, _i32] + [_P] * 12 + [_i32, _i64, _i32, _P, _sz, _P]
+lib.ssdq_gated_scan_backward.restype = ctypes.c_int
+lib.ssdq_gated_step.argtypes = [_i32, _i32, _P, _P, _P, _P, _i32, _i32, _P]
+lib.ssdq_gated_step.restype = ctypes.c_int
 
 
 # scale layouts of ssdq_chunk_scan_scaled / ssdq_state_update_scaled (bit flags)
@@ -512,3 +524,201 @@ def state_update(state, x, x_scale, B, B_scale, C, C_scale, dt, A, D=None, y=Non
     else:
         _check(lib.ssdq_state_update(_ptr(state), *rest), "ssdq_state_update")
     return y
+
+
+# ---------------------------------------------------------------------------------------------
+# gated linear recurrence and 8-bit activation checkpoints
+
+CHECKPOINT_BLOCK = 64                      # channels that share one scale
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_GATE_KINDS = {"log": 0, "logit": 1}       # ssdq_gate_kind
+
+
+def _element_type(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _kind(gate_kind: str) -> int:
+    code = _GATE_KINDS.get(gate_kind)
+    if code is None:
+        raise ValueError(f"gate_kind must be one of {sorted(_GATE_KINDS)}, got {gate_kind!r}")
+    return code
+
+
+def _call(function, where: str, device: torch.device, *args) -> None:
+    """One library call on the current stream of `device`, with that device current."""
+    if device.index == torch.cuda.current_device():
+        _check(function(*args, _stream(device)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(function(*args, _stream(device)), where)
+
+
+def checkpoint_empty(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Buffers for the 8-bit checkpoint of x (..., C): codes like x, int8, and scale (..., ceil(C/64)) fp32."""
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have a last axis of at least one channel")
+    blocks = -(-x.shape[-1] // CHECKPOINT_BLOCK)
+    return (torch.empty(x.shape, dtype=torch.int8, device=x.device),
+            torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=x.device))
+
+
+def _need_checkpoint(codes, scale, shape, device):
+    _need(codes, "codes", torch.int8, shape, device)
+    _need(scale, "scale", torch.float32, (*shape[:-1], -(-shape[-1] // CHECKPOINT_BLOCK)), device)
+
+
+def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """The 8-bit checkpoint of an activation x (..., C), fp32, fp16 or bf16: codes (..., C) int8 and one
+    fp32 scale per 64 channels (..., ceil(C/64)) (ssdq_checkpoint_save).  Returns (codes, scale);
+    `out` may give the two tensors."""
+    dtype = _element_type(x, "x")
+    codes, scale = checkpoint_empty(x) if out is None else out
+    _need(x, "x", x.dtype, None, None)
+    _need_checkpoint(codes, scale, tuple(x.shape), x.device)
+    channels = x.shape[-1]
+    _call(lib.ssdq_checkpoint_save, "ssdq_checkpoint_save", x.device, dtype, _ptr(x), _ptr(codes), _ptr(scale),
+          x.numel() // channels, channels)
+    return codes, scale
+
+
+def checkpoint_load(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype, out: torch.Tensor | None = None):
+    """The values codes * scale of an 8-bit checkpoint as a tensor of `dtype` (ssdq_checkpoint_load)."""
+    if codes.dim() < 1 or codes.shape[-1] == 0:
+        raise ValueError("codes must have a last axis of at least one channel")
+    _need_checkpoint(codes, scale, tuple(codes.shape), None)
+    if out is None:
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    _need(scale, "scale", torch.float32, None, codes.device)
+    _need(out, "out", dtype, tuple(codes.shape), codes.device)
+    channels = codes.shape[-1]
+    _call(lib.ssdq_checkpoint_load, "ssdq_checkpoint_load", codes.device, _element_type(out, "out"), _ptr(codes),
+          _ptr(scale), _ptr(out), codes.numel() // channels, channels)
+    return out
+
+
+def gated_scan_workspace_size(sequences: int, tokens: int, channels: int, packed: bool = False) -> int:
+    """Workspace bytes of gated_scan and gated_scan_backward (0: sizes that they do not take)."""
+    return int(lib.ssdq_gated_scan_workspace_size(sequences, tokens, channels, int(packed)))
+
+
+def _gated_sizes(gate: torch.Tensor, offsets: torch.Tensor | None) -> tuple[int, int, int]:
+    """(sequences, tokens, channels) of a dense (batch, seqlen, channels) or, with offsets, a packed
+    (tokens, channels) tensor."""
+    if offsets is None:
+        if gate.dim() != 3:
+            raise ValueError("gate must be (batch, seqlen, channels), or (tokens, channels) with offsets")
+        return gate.shape[0], gate.shape[0] * gate.shape[1], gate.shape[2]
+    if gate.dim() != 2:
+        raise ValueError("gate must be (tokens, channels) with offsets")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must hold sequences + 1 >= 2 values")
+    _need(offsets, "offsets", torch.int32, None, gate.device)
+    return offsets.numel() - 1, gate.shape[0], gate.shape[1]
+
+
+def _gated_workspace(workspace, sequences, tokens, channels, packed, device, where):
+    need = lib.ssdq_gated_scan_workspace_size(sequences, tokens, channels, packed)
+    if need == 0:
+        raise SSDQError(SSDQ_ERROR_UNSUPPORTED, where)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8, None, device)
+    return workspace
+
+
+def gated_scan(gate: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None = None,
+               offsets: torch.Tensor | None = None, gate_kind: str = "log", checkpoint=None, h=None, h_final=None,
+               workspace=None, want_final_state: bool = True):
+    """The gated linear recurrence h_t = a_t h_{t-1} + b_t per channel (ssdq_gated_scan); returns
+    (h, h_final or None).  gate and u are (batch, seqlen, channels), or packed (tokens, channels) with
+    offsets (sequences + 1) int32 on the device, in fp32, fp16 or bf16; h0 and h_final (batch,
+    channels) fp32.  gate_kind "log": a = exp(gate), b = u; "logit": a = sigmoid(gate), b = (1 - a) u.
+    checkpoint: (codes, scale) as of checkpoint_empty(u), which then receive the 8-bit checkpoint
+    of h.  h, h_final and workspace may give those tensors."""
+    sequences, tokens, channels = _gated_sizes(gate, offsets)
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, tuple(gate.shape)
+    _need(gate, "gate", gate.dtype, None, None)
+    _need(u, "u", gate.dtype, shape, dev)
+    _need(h0, "h0", torch.float32, (sequences, channels), dev, optional=True)
+    if h is None:
+        h = torch.empty_like(gate)
+    else:
+        _need(h, "h", gate.dtype, shape, dev)
+    if h_final is not None:
+        _need(h_final, "h_final", torch.float32, (sequences, channels), dev)
+    elif want_final_state:
+        h_final = torch.empty((sequences, channels), dtype=torch.float32, device=dev)
+    codes, scale = (None, None) if checkpoint is None else checkpoint
+    if checkpoint is not None:
+        _need_checkpoint(codes, scale, shape, dev)
+    workspace = _gated_workspace(workspace, sequences, tokens, channels, offsets is not None, dev, "ssdq_gated_scan")
+    _call(lib.ssdq_gated_scan, "ssdq_gated_scan", dev, dtype, kind, _ptr(gate), _ptr(u), _ptr(h0), _ptr(offsets),
+          _ptr(h), _ptr(h_final), _ptr(codes), _ptr(scale), sequences, tokens, channels, _ptr(workspace),
+          workspace.numel())
+    return h, h_final
+
+
+def gated_scan_backward(gate: torch.Tensor, dh: torch.Tensor, u: torch.Tensor | None = None,
+                        h: torch.Tensor | None = None, checkpoint=None, h0=None, dh_final=None,
+                        offsets: torch.Tensor | None = None, gate_kind: str = "log", dgate=None, du=None, dh0=None,
+                        workspace=None):
+    """The gradients (dgate, du, dh0) of gated_scan from dh, that of h, and dh_final, that of h_final
+    (None: zero), with the states of the forward pass given either as the saved h or as its 8-bit
+    checkpoint (codes, scale) (ssdq_gated_scan_backward).  u is needed with gate_kind "logit" only;
+    gate, offsets and h0 are those of the forward call.  dgate, du, dh0 and workspace may give those
+    tensors."""
+    sequences, tokens, channels = _gated_sizes(gate, offsets)
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, tuple(gate.shape)
+    states = (sequences, channels)
+    _need(gate, "gate", gate.dtype, None, None)
+    _need(dh, "dh", gate.dtype, shape, dev)
+    _need(u, "u", gate.dtype, shape, dev, optional=gate_kind == "log")
+    if (h is None) == (checkpoint is None):
+        raise ValueError("give the states of the forward pass as h or as checkpoint, one of them")
+    codes, scale = (None, None) if checkpoint is None else checkpoint
+    if checkpoint is None:
+        _need(h, "h", gate.dtype, shape, dev)
+    else:
+        _need_checkpoint(codes, scale, shape, dev)
+    _need(h0, "h0", torch.float32, states, dev, optional=True)
+    _need(dh_final, "dh_final", torch.float32, states, dev, optional=True)
+    if dgate is None:
+        dgate = torch.empty_like(gate)
+    else:
+        _need(dgate, "dgate", gate.dtype, shape, dev)
+    if du is None:
+        du = torch.empty_like(gate)
+    else:
+        _need(du, "du", gate.dtype, shape, dev)
+    if dh0 is None:
+        dh0 = torch.empty(states, dtype=torch.float32, device=dev)
+    else:
+        _need(dh0, "dh0", torch.float32, states, dev)
+    workspace = _gated_workspace(workspace, sequences, tokens, channels, offsets is not None, dev,
+                                 "ssdq_gated_scan_backward")
+    _call(lib.ssdq_gated_scan_backward, "ssdq_gated_scan_backward", dev, dtype, kind, _ptr(gate), _ptr(u), _ptr(h),
+          _ptr(codes), _ptr(scale), _ptr(h0), _ptr(dh), _ptr(dh_final), _ptr(offsets), _ptr(dgate), _ptr(du),
+          _ptr(dh0), sequences, tokens, channels, _ptr(workspace), workspace.numel())
+    return dgate, du, dh0
+
+
+def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_kind: str = "log",
+               h: torch.Tensor | None = None) -> torch.Tensor:
+    """One decode token of gated_scan (ssdq_gated_step): state (batch, channels) fp32 is updated in
+    place; gate and u (batch, channels); returns h, the updated state in their type."""
+    if state.dim() != 2:
+        raise ValueError("state must be (batch, channels)")
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), state.device, tuple(state.shape)
+    _need(state, "state", torch.float32, None, None)
+    _need(gate, "gate", gate.dtype, shape, dev)
+    _need(u, "u", gate.dtype, shape, dev)
+    if h is None:
+        h = torch.empty_like(gate)
+    else:
+        _need(h, "h", gate.dtype, shape, dev)
+    _call(lib.ssdq_gated_step, "ssdq_gated_step", dev, dtype, kind, _ptr(state), _ptr(gate), _ptr(u), _ptr(h), *shape)
+    return h

@@ -520,4 +520,139 @@ ssdq_status ssdq_frontend_step(void* conv_state, const void* xbc, const float* c
   return e == hipSuccess ? SSDQ_SUCCESS : SSDQ_ERROR_LAUNCH;
 }
 
+
+namespace {
+
+constexpr int64_t kMostElements = int64_t(1) << 40;   // byte offsets of 4-byte elements stay far inside 64 bits
+constexpr int64_t kMostStates = int64_t(1) << 36;
+
+bool ok_dtype(int32_t d) { return d == SSDQ_DTYPE_F32 || d == SSDQ_DTYPE_F16 || d == SSDQ_DTYPE_BF16; }
+bool ok_gate(int32_t g) { return g == SSDQ_GATE_LOG || g == SSDQ_GATE_LOGIT; }
+
+ssdq_status check_gated_shape(int32_t sequences, int64_t tokens, int32_t channels, bool packed) {
+  if (sequences <= 0 || tokens < 0 || channels <= 0) return SSDQ_ERROR_INVALID_VALUE;
+  if (!packed && tokens % sequences != 0) return SSDQ_ERROR_INVALID_VALUE;
+  if (tokens >= (int64_t(1) << 31) - (int64_t(1) << 16)) return SSDQ_ERROR_UNSUPPORTED;   // rows in 32 bits
+  if (tokens * channels >= kMostElements || int64_t(sequences) * channels >= kMostStates)
+    return SSDQ_ERROR_UNSUPPORTED;
+  if (gated_workspace_bytes(sequences, tokens, channels, packed) == 0) return SSDQ_ERROR_UNSUPPORTED;
+  return SSDQ_SUCCESS;
+}
+
+ssdq_status check_checkpoint(int32_t dtype, const void* x, const void* codes, const void* scale, int64_t rows,
+                             int32_t channels) {
+  if (!ok_dtype(dtype) || rows < 0 || channels <= 0) return SSDQ_ERROR_INVALID_VALUE;
+  const int64_t blocks = (int64_t(channels) + SSDQ_CHECKPOINT_BLOCK - 1) / SSDQ_CHECKPOINT_BLOCK;
+  if (rows >= kMostStates / blocks) return SSDQ_ERROR_UNSUPPORTED;
+  if (rows > 0 && (!ok_ptr(x) || !ok_ptr(codes) || !ok_ptr(scale))) return SSDQ_ERROR_INVALID_VALUE;
+  return SSDQ_SUCCESS;
+}
+
+}  // namespace
+
+ssdq_status ssdq_checkpoint_save(int32_t dtype, const void* x, int8_t* codes, float* scale, int64_t rows,
+                                 int32_t channels, hipStream_t stream) {
+  const ssdq_status st = check_checkpoint(dtype, x, codes, scale, rows, channels);
+  if (st != SSDQ_SUCCESS || rows == 0) return st;
+  return launch_checkpoint_save(dtype, x, codes, scale, rows, channels, stream) == hipSuccess ? SSDQ_SUCCESS
+                                                                                              : SSDQ_ERROR_LAUNCH;
+}
+
+ssdq_status ssdq_checkpoint_load(int32_t dtype, const int8_t* codes, const float* scale, void* x, int64_t rows,
+                                 int32_t channels, hipStream_t stream) {
+  const ssdq_status st = check_checkpoint(dtype, x, codes, scale, rows, channels);
+  if (st != SSDQ_SUCCESS || rows == 0) return st;
+  return launch_checkpoint_load(dtype, codes, scale, x, rows, channels, stream) == hipSuccess ? SSDQ_SUCCESS
+                                                                                              : SSDQ_ERROR_LAUNCH;
+}
+
+size_t ssdq_gated_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t channels, int32_t packed) {
+  if (check_gated_shape(sequences, tokens, channels, packed != 0) != SSDQ_SUCCESS) return 0;
+  return gated_workspace_bytes(sequences, tokens, channels, packed != 0);
+}
+
+ssdq_status ssdq_gated_scan(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const float* h0,
+                            const int32_t* offsets, void* h, float* h_final, int8_t* codes, float* scale,
+                            int32_t sequences, int64_t tokens, int32_t channels, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+  if (!ok_dtype(dtype) || !ok_gate(gate_kind)) return SSDQ_ERROR_INVALID_VALUE;
+  const ssdq_status st = check_gated_shape(sequences, tokens, channels, offsets != nullptr);
+  if (st != SSDQ_SUCCESS) return st;
+  if (!ok_opt(h0) || !ok_opt(h_final) || !ok_opt(offsets) || !ok_ptr(workspace)) return SSDQ_ERROR_INVALID_VALUE;
+  if (tokens > 0) {
+    if (!ok_ptr(gate) || !ok_ptr(u) || !ok_ptr(h) || !ok_opt(codes) || !ok_opt(scale)) return SSDQ_ERROR_INVALID_VALUE;
+    if ((codes == nullptr) != (scale == nullptr)) return SSDQ_ERROR_INVALID_VALUE;
+  }
+  if (workspace_bytes < gated_workspace_bytes(sequences, tokens, channels, offsets != nullptr))
+    return SSDQ_ERROR_WORKSPACE_TOO_SMALL;
+  GatedArgs a = {};
+  a.dtype = dtype;
+  a.gate_kind = gate_kind;
+  a.gate = gate;
+  a.u = u;
+  a.h0 = h0;
+  a.offsets = offsets;
+  a.h = h;
+  a.h_final = h_final;
+  a.codes = codes;
+  a.scale = scale;
+  a.sequences = sequences;
+  a.tokens = tokens;
+  a.channels = channels;
+  a.workspace = workspace;
+  return launch_gated_scan(a, stream) == hipSuccess ? SSDQ_SUCCESS : SSDQ_ERROR_LAUNCH;
+}
+
+ssdq_status ssdq_gated_scan_backward(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const void* h,
+                                     const int8_t* codes, const float* scale, const float* h0, const void* dh,
+                                     const float* dh_final, const int32_t* offsets, void* dgate, void* du, float* dh0,
+                                     int32_t sequences, int64_t tokens, int32_t channels, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  if (!ok_dtype(dtype) || !ok_gate(gate_kind)) return SSDQ_ERROR_INVALID_VALUE;
+  const ssdq_status st = check_gated_shape(sequences, tokens, channels, offsets != nullptr);
+  if (st != SSDQ_SUCCESS) return st;
+  if (!ok_opt(h0) || !ok_opt(dh_final) || !ok_opt(dh0) || !ok_opt(offsets) || !ok_ptr(workspace))
+    return SSDQ_ERROR_INVALID_VALUE;
+  if (tokens > 0) {
+    if (!ok_ptr(gate) || !ok_ptr(dh) || !ok_ptr(dgate) || !ok_ptr(du) || !ok_opt(h) || !ok_opt(codes) ||
+        !ok_opt(scale))
+      return SSDQ_ERROR_INVALID_VALUE;
+    if (gate_kind == SSDQ_GATE_LOGIT && !ok_ptr(u)) return SSDQ_ERROR_INVALID_VALUE;
+    if ((codes == nullptr) != (scale == nullptr) || (h == nullptr) == (codes == nullptr))
+      return SSDQ_ERROR_INVALID_VALUE;
+  }
+  if (workspace_bytes < gated_workspace_bytes(sequences, tokens, channels, offsets != nullptr))
+    return SSDQ_ERROR_WORKSPACE_TOO_SMALL;
+  GatedArgs a = {};
+  a.dtype = dtype;
+  a.gate_kind = gate_kind;
+  a.gate = gate;
+  a.u = u;
+  a.h0 = h0;
+  a.offsets = offsets;
+  a.h = const_cast<void*>(h);
+  a.codes = const_cast<int8_t*>(codes);
+  a.scale = const_cast<float*>(scale);
+  a.dh = dh;
+  a.dh_final = dh_final;
+  a.dgate = dgate;
+  a.du = du;
+  a.dh0 = dh0;
+  a.sequences = sequences;
+  a.tokens = tokens;
+  a.channels = channels;
+  a.workspace = workspace;
+  return launch_gated_backward(a, stream) == hipSuccess ? SSDQ_SUCCESS : SSDQ_ERROR_LAUNCH;
+}
+
+ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, const void* gate, const void* u, void* h,
+                            int32_t batch, int32_t channels, hipStream_t stream) {
+  if (!ok_dtype(dtype) || !ok_gate(gate_kind) || batch <= 0 || channels <= 0) return SSDQ_ERROR_INVALID_VALUE;
+  if (!ok_ptr(state) || !ok_ptr(gate) || !ok_ptr(u) || !ok_ptr(h)) return SSDQ_ERROR_INVALID_VALUE;
+  const int64_t n = int64_t(batch) * channels;
+  if (n >= kMostStates) return SSDQ_ERROR_UNSUPPORTED;
+  return launch_gated_step(dtype, gate_kind, state, gate, u, h, n, stream) == hipSuccess ? SSDQ_SUCCESS
+                                                                                         : SSDQ_ERROR_LAUNCH;
+}
+
 }  // extern "C"

@@ -1,0 +1,96 @@
+"""Refusals of the gated-scan and checkpoint calls that need no GPU: every call below has at least one
+invalid argument, so validation returns before the library touches the HIP runtime or any memory (the
+pointers are fake), and the binding's checks on tensors."""
+import ctypes
+
+import pytest
+import torch
+
+ssdq = pytest.importorskip("quantized_selective_state_amd")
+
+OK, INVALID, UNSUPPORTED, WS_SMALL = 0, 1, 2, 3
+A = 0x100000          # 16-byte aligned, never dereferenced
+ODD = A + 8
+BIG = 1 << 62
+
+
+def scan(**over):
+    a = dict(dtype=1, kind=0, gate=A, u=A, h0=A, offsets=None, h=A, h_final=A, codes=None, scale=None, sequences=2,
+             tokens=8, channels=64, ws=A, ws_bytes=BIG)
+    a.update(over)
+    return ssdq.lib.ssdq_gated_scan(*a.values(), None)
+
+
+def backward(**over):
+    a = dict(dtype=1, kind=0, gate=A, u=A, h=A, codes=None, scale=None, h0=A, dh=A, dh_final=A, offsets=None, dgate=A,
+             du=A, dh0=A, sequences=2, tokens=8, channels=64, ws=A, ws_bytes=BIG)
+    a.update(over)
+    return ssdq.lib.ssdq_gated_scan_backward(*a.values(), None)
+
+
+SHAPES = [(dict(dtype=3), INVALID), (dict(dtype=-1), INVALID), (dict(kind=2), INVALID), (dict(sequences=0), INVALID),
+          (dict(tokens=-1), INVALID), (dict(channels=0), INVALID), (dict(sequences=3), INVALID),
+          (dict(tokens=1 << 31, sequences=1), UNSUPPORTED), (dict(channels=1 << 30, tokens=1 << 20), UNSUPPORTED),
+          (dict(gate=None), INVALID), (dict(gate=ODD), INVALID), (dict(h0=ODD), INVALID), (dict(ws=None), INVALID),
+          (dict(ws=ODD), INVALID), (dict(offsets=ODD), INVALID), (dict(ws_bytes=255), WS_SMALL)]
+
+
+@pytest.mark.parametrize("over,status", SHAPES + [
+    (dict(u=None), INVALID), (dict(h=None), INVALID), (dict(h=ODD), INVALID), (dict(h_final=ODD), INVALID),
+    (dict(codes=A), INVALID), (dict(scale=A), INVALID), (dict(codes=ODD, scale=A), INVALID)])
+def test_scan_refusals(over, status):
+    assert scan(**over) == status
+
+
+@pytest.mark.parametrize("over,status", SHAPES + [
+    (dict(dh=None), INVALID), (dict(dgate=None), INVALID), (dict(du=ODD), INVALID), (dict(dh0=ODD), INVALID),
+    (dict(dh_final=ODD), INVALID), (dict(h=None), INVALID), (dict(codes=A, scale=A), INVALID),
+    (dict(h=None, codes=A), INVALID), (dict(h=None, scale=A), INVALID), (dict(kind=1, u=None), INVALID),
+    (dict(kind=1, u=ODD), INVALID)])
+def test_backward_refusals(over, status):
+    assert backward(**over) == status
+
+
+def test_step_refusals():
+    call = lambda d=0, k=0, s=A, g=A, u=A, h=A, b=2, c=64: ssdq.lib.ssdq_gated_step(d, k, s, g, u, h, b, c, None)
+    for over in (dict(d=3), dict(k=-1), dict(s=None), dict(g=ODD), dict(u=None), dict(h=None), dict(b=0), dict(c=0)):
+        assert call(**over) == INVALID, over
+    assert call(b=1 << 30, c=1 << 30) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["ssdq_checkpoint_save", "ssdq_checkpoint_load"])
+def test_checkpoint_refusals(name):
+    f = getattr(ssdq.lib, name)
+    for args, status in (((3, A, A, A, 2, 64), INVALID), ((0, A, A, A, -1, 64), INVALID), ((0, A, A, A, 2, 0), INVALID),
+                         ((0, None, A, A, 2, 64), INVALID), ((0, A, ODD, A, 2, 64), INVALID),
+                         ((0, A, A, None, 2, 64), INVALID), ((0, A, A, A, 1 << 36, 64), UNSUPPORTED),
+                         ((0, None, None, None, 0, 64), OK)):
+        assert f(*args, None) == status, args
+
+
+def test_workspace_size():
+    size = ssdq.gated_scan_workspace_size
+    assert size(1, 1, 1) >= 256 and size(1, 0, 1) >= 256 and size(3, 7, 5, packed=True) >= 256
+    assert size(3, 7, 5) == 0 and size(0, 8, 64) == 0 and size(1, 8, 0) == 0 and size(1, 1 << 31, 64) == 0
+    assert size(4, 8192, 4096) % 256 == 0
+
+
+def test_binding_refuses_before_any_launch():
+    x = torch.zeros(2, 3, 64, dtype=torch.float16)          # host tensors: refused by the binding
+    for call in (lambda: ssdq.gated_scan(x, x), lambda: ssdq.gated_scan_backward(x, x, h=x),
+                 lambda: ssdq.gated_step(torch.zeros(2, 64), x[:, 0], x[:, 0]), lambda: ssdq.checkpoint_save(x),
+                 lambda: ssdq.checkpoint_load(torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2, 1), torch.float32)):
+        with pytest.raises(ValueError, match="device tensor"):
+            call()
+    with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
+        ssdq.gated_scan(x.double(), x.double())
+    with pytest.raises(ValueError, match="gate_kind"):
+        ssdq.gated_scan(x, x, gate_kind="tanh")
+    with pytest.raises(ValueError, match="offsets"):
+        ssdq.gated_scan(x[0], x[0])
+    with pytest.raises(ValueError, match="with offsets"):
+        ssdq.gated_scan(x, x, offsets=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="sequences"):
+        ssdq.gated_scan(x[0], x[0], offsets=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="channel"):
+        ssdq.checkpoint_empty(torch.zeros(2, 0))

@@ -1,0 +1,406 @@
+"""The gated scan, its gradient and its step on the GPU against the 64-bit reference, within the error
+bounds derived in ref_gated.py plus one rounding to the output's type."""
+import numpy as np
+import pytest
+import torch
+
+import ref_gated as ref
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+DEV = "cuda:0"
+
+
+def lib():
+    import quantized_selective_state_amd as ssdq
+    return ssdq
+
+
+def half_step(dtype, values):
+    """Half a last place of `dtype` at these magnitudes (values: 64 bits)."""
+    if dtype == torch.float32:
+        return np.abs(values) * 2.0 ** -24 + 2.0 ** -149
+    info = torch.finfo(dtype)
+    return np.abs(values) * info.eps / 2 + info.tiny * info.eps / 2      # below `tiny` the spacing is constant
+
+
+def lengths(seed, sequences, tokens, before=0, behind=0):
+    rng = np.random.default_rng(seed)
+    cuts = np.sort(rng.integers(before, tokens - behind + 1, sequences - 1))
+    if sequences > 4:
+        cuts[1] = cuts[0]                                                # an empty sequence
+        cuts[2] = min(cuts[1] + 1, tokens - behind)                      # and one of one token
+        cuts = np.sort(cuts)
+    return np.concatenate([[before], cuts, [tokens - behind]]).astype(np.int32)
+
+
+class Draw:
+    """One problem: device tensors, and the same numbers in 64 bits."""
+
+    def __init__(self, seed, dtype, kind, sequences, tokens, channels, offsets=None, states=True):
+        rng = np.random.default_rng(seed)
+        self.kind, self.sequences, self.tokens, self.channels, self.host_offsets = kind, sequences, tokens, channels, offsets
+        rate = np.exp(rng.uniform(np.log(0.02), np.log(4.0), channels))
+        gate = -np.log1p(np.exp(rng.normal(-2, 0.5, (tokens, channels)))) * rate
+        if kind == "logit":
+            gate = rng.normal(size=(tokens, channels)) + rng.uniform(-1, 5, channels)
+        self.shape = (tokens, channels) if offsets is not None else (sequences, tokens // sequences, channels)
+        put = lambda a, t: torch.from_numpy(np.asarray(a, dtype=np.float32)).to(t).to(DEV)
+        width = np.exp(rng.uniform(-1, 1, channels))
+        self.gate = put(gate, dtype).view(self.shape)
+        self.u = put(rng.normal(size=(tokens, channels)) * width, dtype).view(self.shape)
+        self.dh = put(rng.normal(size=(tokens, channels)), dtype).view(self.shape)
+        self.h0 = put(rng.normal(size=(sequences, channels)), torch.float32) if states else None
+        self.dh_final = put(rng.normal(size=(sequences, channels)), torch.float32) if states else None
+        self.offsets = None if offsets is None else torch.from_numpy(offsets).to(DEV)
+        self.dtype = dtype
+
+    def host(self, t):
+        return None if t is None else t.double().cpu().numpy().reshape(-1, self.channels)
+
+    def reference(self):
+        return ref.forward(self.host(self.gate), self.host(self.u), self.host(self.h0), self.kind, self.sequences,
+                           self.host_offsets)
+
+    def gradients(self, saved):
+        return ref.backward(self.host(self.gate), self.host(self.u), saved, self.host(self.h0), self.host(self.dh),
+                            self.host(self.dh_final), self.kind, self.sequences, self.host_offsets)
+
+
+def close(got, want, bound, dtype, what):
+    got = got.double().cpu().numpy().reshape(want.shape)
+    allowed = bound + half_step(dtype, np.abs(want) + bound)
+    worst = np.max(np.abs(got - want) / allowed) if want.size else 0.0
+    print(f"  {what}: {worst:.3f} of the bound", flush=True)
+    assert np.all(np.abs(got - want) <= allowed), (what, worst)
+
+
+def covered(d):
+    rows = np.zeros(d.tokens, bool)
+    for lo, hi in ref.spans(d.tokens, d.sequences, d.host_offsets):
+        rows[lo:hi] = True
+    return rows
+
+
+def check_forward(d):
+    h = torch.full(d.shape, 7.0, dtype=d.dtype, device=DEV)
+    got, final = lib().gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind=d.kind, h=h)
+    want, want_final, bound, final_bound = d.reference()
+    torch.cuda.synchronize()
+    rows = covered(d)
+    flat = got.view(d.tokens, d.channels)
+    mask = torch.from_numpy(rows).to(DEV)
+    assert bool((flat[~mask] == 7.0).all()), "rows of no sequence were written"
+    close(flat[mask], want[rows], bound[rows], d.dtype, "h")
+    close(final, want_final, final_bound, torch.float32, "h_final")
+    return got
+
+
+def check_backward(d, h=None, checkpoint=None):
+    if checkpoint is None:
+        saved = d.host(h)
+    else:
+        saved = ref.values(*[x.cpu().numpy().reshape(d.tokens, -1) for x in checkpoint])
+    dgate, du = (torch.full(d.shape, 7.0, dtype=d.dtype, device=DEV) for _ in range(2))
+    dgate, du, dh0 = lib().gated_scan_backward(d.gate, d.dh, u=d.u if d.kind == "logit" else None, h=h,
+                                               checkpoint=checkpoint, h0=d.h0, dh_final=d.dh_final, offsets=d.offsets,
+                                               gate_kind=d.kind, dgate=dgate, du=du)
+    want = d.gradients(saved)
+    torch.cuda.synchronize()
+    rows = covered(d)
+    mask = torch.from_numpy(rows).to(DEV)
+    for name, g, w, b in (("dgate", dgate, want[0], want[3]), ("du", du, want[1], want[4])):
+        flat = g.view(d.tokens, d.channels)
+        assert bool((flat[~mask] == 7.0).all()), f"{name}: rows of no sequence were written"
+        close(flat[mask], w[rows], b[rows], d.dtype, name)
+    close(dh0, want[2], want[5], torch.float32, "dh0")
+
+
+# (sequences, tokens, channels): one token; one tile and its borders; several tiles; more tiles than are
+# joined at once; channel counts that no vector divides; one channel; a partial block; many sequences
+DENSE = [(1, 1, 1), (1, 1, 64), (3, 3, 128), (1, 256, 64), (2, 510, 72), (1, 257, 8), (2, 2 * 1023, 66), (1, 2049, 33),
+         (1, 9001, 8), (4, 4 * 700, 200), (64, 64 * 40, 64), (5, 5 * 33, 1000), (300, 300 * 2, 136), (1, 5000, 1)]
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", DENSE, ids=str)
+def test_dense(shape, dtype, kind):
+    d = Draw(11 + shape[1], TYPES[dtype], kind, *shape)
+    h = check_forward(d)
+    check_backward(d, h=h)
+    check_backward(d, checkpoint=lib().checkpoint_save(h))
+
+
+PACKED = [(1, 5, 64, 0, 0), (7, 50, 8, 0, 0), (9, 1000, 72, 3, 40), (37, 3001, 51, 0, 1), (200, 500, 64, 0, 0),
+          (6, 9300, 16, 100, 5), (1000, 40, 64, 0, 0), (2, 4500, 130, 0, 300)]
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", PACKED, ids=str)
+def test_packed(shape, dtype, kind):
+    sequences, tokens, channels, before, behind = shape
+    d = Draw(5 + tokens, TYPES[dtype], kind, sequences, tokens, channels, lengths(tokens, sequences, tokens, before, behind))
+    h = check_forward(d)
+    h = torch.where(torch.from_numpy(covered(d)).to(DEV)[:, None], h, torch.zeros_like(h))
+    check_backward(d, h=h)
+    check_backward(d, checkpoint=lib().checkpoint_save(h))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_without_states(packed):
+    d = Draw(3, torch.float32, "log", 3, 1500, 64, lengths(3, 3, 1500) if packed else None, states=False)
+    h = check_forward(d)
+    check_backward(d, h=h)
+    one, none = lib().gated_scan(d.gate, d.u, offsets=d.offsets, want_final_state=False)
+    assert none is None and torch.equal(one, h)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_tokens(packed):
+    ssdq = lib()
+    h0 = torch.randn(3, 65, device=DEV)
+    gate = torch.empty((0, 65) if packed else (3, 0, 65), dtype=torch.float16, device=DEV)
+    offsets = torch.zeros(4, dtype=torch.int32, device=DEV) if packed else None
+    h, final = ssdq.gated_scan(gate, gate, h0, offsets)
+    assert h.numel() == 0 and torch.equal(final, h0)
+    assert not ssdq.gated_scan(gate, gate, None, offsets)[1].any()
+    dgate, du, dh0 = ssdq.gated_scan_backward(gate, gate, h=gate, h0=h0, dh_final=h0, offsets=offsets)
+    assert torch.equal(dh0, h0) and dgate.numel() == du.numel() == 0
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(2, 700, 64), (3, 900, 200), (1, 5001, 51), (1, 1, 129)], ids=str)
+def test_written_checkpoint_is_that_of_h(shape, dtype):
+    ssdq = lib()
+    d = Draw(21, TYPES[dtype], "log", shape[0], shape[0] * (shape[1] // shape[0]), shape[2])
+    buffers = ssdq.checkpoint_empty(d.u)
+    plain, final = ssdq.gated_scan(d.gate, d.u, d.h0)
+    h, final2 = ssdq.gated_scan(d.gate, d.u, d.h0, checkpoint=buffers)
+    codes, scale = ssdq.checkpoint_save(h)
+    assert torch.equal(h, plain) and torch.equal(final, final2)
+    assert torch.equal(buffers[0], codes) and torch.equal(buffers[1], scale)
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+def test_training_step_against_differences(kind):
+    """Forward with a checkpoint, then backward from it: the derivative along a random direction agrees
+    with central differences of the reference, up to what the 8-bit states allow."""
+    ssdq = lib()
+    d = Draw(9, torch.float32, kind, 2, 2 * 300, 64)
+    buffers = ssdq.checkpoint_empty(d.u)
+    ssdq.gated_scan(d.gate, d.u, d.h0, gate_kind=kind, checkpoint=buffers)
+    dgate, du, dh0 = ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, checkpoint=buffers, h0=d.h0, dh_final=d.dh_final,
+                                              gate_kind=kind)
+    rng = np.random.default_rng(1)
+    g, u, s = d.host(d.gate), d.host(d.u), d.host(d.h0)
+    dg, dv, ds = (rng.normal(size=x.shape) for x in (g, u, s))
+    step = 1e-5
+
+    def loss(sign):
+        h, final, _, _ = ref.forward(g + sign * step * dg, u + sign * step * dv, s + sign * step * ds, kind, 2)
+        return (h * d.host(d.dh)).sum() + (final * d.host(d.dh_final)).sum()
+
+    want = (loss(1) - loss(-1)) / (2 * step)
+    got = (d.host(dgate) * dg).sum() + (d.host(du) * dv).sum() + (d.host(dh0) * ds).sum()
+    # a code moves a saved state by at most scale / 2, and dgate by k (1 - a) times that
+    h64, _, _, _ = d.reference()
+    k_c = d.gradients(np.ones_like(h64))[0] - d.gradients(np.zeros_like(h64))[0]      # what multiplies a saved state
+    half = np.repeat(buffers[1].double().cpu().numpy().reshape(600, -1), 64, axis=1) / 2
+    moved = np.concatenate([np.zeros((1, 64)), half[:-1]])
+    moved[::300] = 0                                                                  # first tokens start from h0
+    allowed = (np.abs(k_c * dg) * moved).sum() + 1e-4 * (np.abs(d.host(dgate) * dg).sum() + np.abs(d.host(du) * dv).sum())
+    print(f"  difference {abs(got - want):.3e}, allowed {allowed:.3e}, value {want:.3e}")
+    assert abs(got - want) <= allowed
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_prefill_in_parts_and_steps_continue_it(dtype):
+    ssdq = lib()
+    d = Draw(31, TYPES[dtype], "logit", 3, 3 * 606, 72)
+    want, want_final, bound, final_bound = d.reference()
+    state = d.h0.clone()
+    parts = []
+    for lo, hi in ((0, 1), (1, 300), (300, 600)):
+        h, _ = ssdq.gated_scan(d.gate[:, lo:hi].contiguous(), d.u[:, lo:hi].contiguous(), state, gate_kind="logit",
+                               h_final=state)                           # the state in place
+        parts.append(h)
+    for t in range(600, 606):
+        parts.append(ssdq.gated_step(state, d.gate[:, t].contiguous(), d.u[:, t].contiguous(), gate_kind="logit")[:, None])
+    # parts add a rounding of the state each, which the bound's 8 per token of distance has room for
+    close(torch.cat(parts, 1), want, bound, d.dtype, "h")
+    close(state, want_final, final_bound, torch.float32, "state")
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(1, 1), (1, 4096), (7, 33), (256, 200), (3, 1001)], ids=str)
+def test_step(shape, dtype, kind):
+    batch, channels = shape
+    d = Draw(41, TYPES[dtype], kind, batch, batch, channels)
+    state = d.h0.clone()
+    h = lib().gated_step(state, d.gate[:, 0].contiguous(), d.u[:, 0].contiguous(), gate_kind=kind)
+    want, want_final, bound, final_bound = d.reference()
+    close(h, want, bound, d.dtype, "h")
+    close(state, want_final, final_bound, torch.float32, "state")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_gates_that_close_or_saturate(dtype):
+    """Log gates of -inf, of the type's lowest value and of 0; logits of either infinity and extreme."""
+    t = TYPES[dtype]
+    low = torch.finfo(t).min
+    for kind, special in (("log", (-float("inf"), low, 0.0, -1e-4)), ("logit", (-float("inf"), float("inf"), low, 30.0))):
+        d = Draw(51, t, kind, 2, 2 * 600, 64)
+        for j, v in enumerate(special):
+            d.gate[:, j::7, j::9] = v
+        h = check_forward(d)
+        check_backward(d, h=h)
+
+
+def test_nan_and_infinity_stay_in_their_sequence_and_channel():
+    ssdq = lib()
+    for packed in (False, True):
+        offsets = np.array([0, 10, 700, 1200], np.int32) if packed else None
+        d = Draw(61, torch.float32, "log", 3, 1200, 64, offsets)
+        clean, _ = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets)
+        rows = ref.spans(1200, 3, offsets)
+        at = rows[1][0] + 5
+        u = d.u.clone()
+        u.view(1200, 64)[at, 3] = float("nan")
+        u.view(1200, 64)[at + 1, 4] = float("inf")
+        h, _ = ssdq.gated_scan(d.gate, u, d.h0, d.offsets)
+        h, clean = h.view(1200, 64), clean.view(1200, 64)
+        touched = torch.zeros(1200, 64, dtype=torch.bool, device=DEV)
+        touched[at:rows[1][1], 3] = True
+        touched[at + 1:rows[1][1], 4] = True
+        assert torch.equal(torch.isfinite(h), ~touched)
+        assert torch.equal(h[~touched], clean[~touched])
+
+
+def test_rows_of_no_sequence_are_not_read():
+    ssdq = lib()
+    offsets = np.array([40, 300, 300, 900], np.int32)
+    d = Draw(71, torch.float16, "logit", 3, 1000, 64, offsets)
+    h, final = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind="logit")
+    grads = ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, h=h, h0=d.h0, dh_final=d.dh_final, offsets=d.offsets,
+                                     gate_kind="logit")
+    rows = slice(40, 900)
+    for t in (d.gate, d.u, d.dh, h):
+        t[:40] = float("nan")
+        t[900:] = float("nan")
+    h2, final2 = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind="logit")
+    grads2 = ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, h=h, h0=d.h0, dh_final=d.dh_final, offsets=d.offsets,
+                                      gate_kind="logit")
+    assert torch.equal(h[rows], h2[rows]) and torch.equal(final, final2) and torch.equal(grads[2], grads2[2])
+    assert torch.equal(grads[0][rows], grads2[0][rows]) and torch.equal(grads[1][rows], grads2[1][rows])
+
+
+def test_offsets_out_of_range_stay_inside_the_tensors():
+    """The library cannot look at offsets on the host; whatever they hold, the kernels clamp the rows."""
+    ssdq = lib()
+    size, edge = 600 * 64, 64 * 64
+    for offsets in ([-50, 200, 5000], [400, 100, 600], [2 ** 31 - 1, -2 ** 31, 7], [0, 10 ** 9, 10 ** 9]):
+        room = torch.full((size + 2 * edge,), 7.0, device=DEV)
+        h = room[edge:edge + size].view(600, 64)
+        d = Draw(81, torch.float32, "log", 2, 600, 64, np.array([0, 1, 600], np.int32))
+        ssdq.gated_scan(d.gate, d.u, d.h0, torch.tensor(offsets, dtype=torch.int32, device=DEV), h=h)
+        torch.cuda.synchronize()
+        assert bool((room[:edge] == 7.0).all()) and bool((room[edge + size:] == 7.0).all())
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_same_bits_whatever_the_workspace_holds(packed):
+    ssdq = lib()
+    d = Draw(91, torch.bfloat16, "log", 2, 2 * 5000, 72, lengths(7, 2, 10000) if packed else None)
+    size = ssdq.gated_scan_workspace_size(2, 10000, 72, packed)
+    results = []
+    for fill in (0, 0xFF, 0x3F, None):
+        ws = torch.randint(0, 256, (size,), dtype=torch.uint8, device=DEV) if fill is None else torch.full(
+            (size,), fill, dtype=torch.uint8, device=DEV)
+        h, final = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, workspace=ws)
+        grads = ssdq.gated_scan_backward(d.gate, d.dh, h=h, h0=d.h0, dh_final=d.dh_final, offsets=d.offsets, workspace=ws)
+        results.append((h, final, *grads))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+def test_workspace_too_small_is_refused():
+    ssdq = lib()
+    d = Draw(91, torch.float32, "log", 1, 5000, 64)
+    with pytest.raises(ssdq.SSDQError) as e:
+        ssdq.gated_scan(d.gate, d.u, workspace=torch.empty(128, dtype=torch.uint8, device=DEV))
+    assert e.value.status == ssdq.SSDQ_ERROR_WORKSPACE_TOO_SMALL
+
+
+def test_binding_refuses_wrong_tensors():
+    ssdq = lib()
+    d = Draw(1, torch.float16, "log", 2, 20, 64)
+    wrong = [lambda: ssdq.gated_scan(d.gate, d.u.float()), lambda: ssdq.gated_scan(d.gate, d.u[:, :5]),
+             lambda: ssdq.gated_scan(d.gate.transpose(0, 1), d.u.transpose(0, 1)),
+             lambda: ssdq.gated_scan(d.gate, d.u, d.h0[:1]), lambda: ssdq.gated_scan(d.gate, d.u, d.h0.half()),
+             lambda: ssdq.gated_scan(d.gate, d.u, checkpoint=ssdq.checkpoint_empty(d.u[:1])),
+             lambda: ssdq.gated_scan(d.gate[0], d.u[0], offsets=torch.zeros(2, dtype=torch.int64, device=DEV)),
+             lambda: ssdq.gated_scan_backward(d.gate, d.dh),
+             lambda: ssdq.gated_scan_backward(d.gate, d.dh, h=d.u, checkpoint=ssdq.checkpoint_empty(d.u)),
+             lambda: ssdq.gated_scan_backward(d.gate, d.dh, h=d.u, gate_kind="logit"),
+             lambda: ssdq.gated_step(d.h0, d.gate[0], d.u[0]), lambda: ssdq.gated_step(d.h0[0], d.gate[0], d.u[0])]
+    for call in wrong:
+        with pytest.raises(ValueError):
+            call()
+    # a view whose first element is not 16-byte aligned: the library's own check
+    flat = torch.zeros(2 * 10 * 64 + 1, dtype=torch.float16, device=DEV)
+    with pytest.raises(ssdq.SSDQError) as e:
+        ssdq.gated_scan(flat[1:].view(2, 10, 64), d.u)
+    assert e.value.status == ssdq.SSDQ_ERROR_INVALID_VALUE
+
+
+def test_on_another_stream():
+    ssdq = lib()
+    d = Draw(13, torch.bfloat16, "log", 2, 4000, 128)
+    want, final = ssdq.gated_scan(d.gate, d.u, d.h0)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        late = d.u * 1.0                       # queued on s: the scan has to follow it there
+        h, f = ssdq.gated_scan(d.gate, late, d.h0)
+    s.synchronize()
+    assert torch.equal(h, want) and torch.equal(f, final)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_captured_training_step_replays(packed):
+    """Forward with a checkpoint and backward from it in one graph, replayed on new inputs with eager work and
+    synchronizations between; every replay equals the eager calls bit for bit."""
+    ssdq = lib()
+    offsets = [lengths(s, 5, 6000) for s in (1, 2, 3)] if packed else [None] * 3
+    draws = [Draw(100 + i, torch.bfloat16, "logit", 5, 6000, 72, o) for i, o in enumerate(offsets)]
+    fixed = Draw(100, torch.bfloat16, "logit", 5, 6000, 72, offsets[0])
+    names = ["gate", "u", "dh", "h0", "dh_final"] + (["offsets"] if packed else [])
+
+    def step(d, buffers):
+        h, final = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind="logit", checkpoint=buffers)
+        return (h, final, *ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, checkpoint=buffers, h0=d.h0, offsets=d.offsets,
+                                                    dh_final=d.dh_final, gate_kind="logit"))
+
+    want = [[t.clone() for t in step(d, ssdq.checkpoint_empty(d.u))] for d in draws]
+    buffers = ssdq.checkpoint_empty(fixed.u)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(fixed, buffers)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(fixed, buffers)
+    for i in (0, 1, 2, 1):
+        for n in names:
+            getattr(fixed, n).copy_(getattr(draws[i], n))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
+        step(draws[2], ssdq.checkpoint_empty(draws[2].u))      # eager work between the replays
+        torch.cuda.synchronize()
