@@ -140,7 +140,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the raw handle of torch.cuda.current_stream(device), without building a Stream object
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def _need(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple | None, device, optional=False):

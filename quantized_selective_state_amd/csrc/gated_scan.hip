@@ -67,21 +67,7 @@ bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed
 
 size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * sizeof(uint64_t); }
 
-typedef unsigned short u16;
-
-// Buffer accesses of VB bytes; out-of-range reads give zeros, out-of-range writes are dropped.
-template <int VB>
-struct Bytes;
-template <>
-struct Bytes<16> { typedef v4u type; };
-template <>
-struct Bytes<8> { typedef v2u type; };
-template <>
-struct Bytes<4> { typedef uint32_t type; };
-template <>
-struct Bytes<2> { typedef u16 type; };
-template <>
-struct Bytes<1> { typedef uint8_t type; };
+// Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) { v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) { v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0); }
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) { v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
@@ -93,14 +79,6 @@ __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { 
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, u16 v) { __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint8_t v) { __builtin_amdgcn_raw_buffer_store_b8(v, r, off, 0, 0); }
 
-// V neighbouring elements as loaded
-template <typename T, int V>
-struct Pack {
-  typedef typename Bytes<sizeof(T) * V>::type Raw;
-  struct Elements { T e[V]; };
-  Raw raw;
-  __device__ __forceinline__ float operator[](int v) const { return to_f32(__builtin_bit_cast(Elements, raw).e[v]); }
-};
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load_pack(Rsrc r, uint32_t off) {
   Pack<T, V> p;
@@ -181,29 +159,6 @@ __device__ __forceinline__ Tile packed_tile(const GatedArgs& g, int32_t i, Tile*
   }
   __syncthreads();
   return *shared;
-}
-
-// Largest of the unsigned images over the lanes of a row's 64 channels (LPR consecutive lanes), in
-// every one of them: magnitudes compare as integers, NaN above infinity above the rest.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
-  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false)));
-}
-template <int LPR>
-__device__ __forceinline__ uint32_t row_umax(uint32_t m) {
-  if constexpr (LPR >= 2) m = dpp_umax<0xB1>(m);
-  if constexpr (LPR >= 4) m = dpp_umax<0x4E>(m);
-  if constexpr (LPR >= 8) m = dpp_umax<0x141>(m);
-  if constexpr (LPR >= 16) m = dpp_umax<0x140>(m);
-  if constexpr (LPR >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    m = max(uint32_t(r[0]), uint32_t(r[1]));
-  }
-  if constexpr (LPR >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    m = max(uint32_t(r[0]), uint32_t(r[1]));
-  }
-  return m;
 }
 
 // What the backward pass reads the saved states from, and what the forward pass writes
@@ -437,15 +392,11 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
           for (int v = 0; v < V; ++v) most = max(most, __float_as_uint(fabsf(out[v])));
         }
         const float s = checkpoint_scale(row_umax<LPR>(most));
-        const CodeScale cs = code_scale(s);
-        struct { int8_t e[V]; } q;
-#pragma unroll
-        for (int v = 0; v < V; ++v) q.e[v] = int8_t(code_of(out[v], cs));
         const uint32_t crow = uint32_t(g.channels), srow = 4u * uint32_t(p.chans);
         const Rsrc rc = make_rsrc(g.codes + start, uint32_t(nrows) * crow);
         const Rsrc rs = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
         store_bytes(rc, in ? uint32_t(run + i) * crow + uint32_t(c) : kOutOfRange,
-                    __builtin_bit_cast(typename Bytes<V>::type, q));
+                    codes_of<V>(out, s));
         store_bytes(rs, col == 0 ? uint32_t(run + i) * srow + 4u * uint32_t(blk) : kOutOfRange, __float_as_uint(s));
       }
     }
@@ -492,15 +443,49 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(v4u* words, int64_t n,
   for (int64_t k = i; k < n; k += int64_t(gridDim.x) * 256) words[k] = v4u{~0u, ~0u, ~0u, ~0u};
 }
 
+// Elementwise over batch * channels: 4 elements per thread (16 bytes of state), whatever the row length.
+constexpr int kStep = 4;
 template <typename T, int KIND>
-__global__ void __launch_bounds__(256) gated_step_kernel(float* state, const T* gate, const T* u, T* h, int64_t n) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-    float a, m;
-    gate_terms<KIND>(to_f32(gate[i]), a, m);
-    const float v = to_f32(u[i]);
-    const float s = fmaf(a, state[i], KIND == SSDQ_GATE_LOG ? v : m * v);
-    state[i] = s;
-    h[i] = from_f32<T>(s);
+__global__ void __launch_bounds__(256) gated_step_kernel(float* __restrict__ state, const T* __restrict__ gate,
+                                                         const T* __restrict__ u, T* __restrict__ h, int64_t n) {
+  typedef Pack<T, kStep> P;
+  typedef typename P::Raw Raw;
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * kStep; i < n; i += int64_t(gridDim.x) * 256 * kStep) {
+    const bool whole = i + kStep <= n;
+    P pg, pu;
+    float s[kStep];
+    if (whole) {
+      pg.raw = *reinterpret_cast<const Raw*>(gate + i);
+      pu.raw = *reinterpret_cast<const Raw*>(u + i);
+      const v4f v = *reinterpret_cast<const v4f*>(state + i);
+#pragma unroll
+      for (int e = 0; e < kStep; ++e) s[e] = v[e];
+    } else {
+      typename P::Elements eg = {}, eu = {};
+#pragma unroll
+      for (int e = 0; e < kStep; ++e) {
+        s[e] = 0.f;
+        if (i + e < n) eg.e[e] = gate[i + e], eu.e[e] = u[i + e], s[e] = state[i + e];
+      }
+      pg.raw = __builtin_bit_cast(Raw, eg);
+      pu.raw = __builtin_bit_cast(Raw, eu);
+    }
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
+      float a, m;
+      gate_terms<KIND>(pg[e], a, m);
+      s[e] = fmaf(a, s[e], KIND == SSDQ_GATE_LOG ? pu[e] : m * pu[e]);
+    }
+    const P out = to_pack<T, kStep>(s);
+    if (whole) {
+      *reinterpret_cast<v4f*>(state + i) = v4f{s[0], s[1], s[2], s[3]};
+      *reinterpret_cast<Raw*>(h + i) = out.raw;
+    } else {
+      const auto e = __builtin_bit_cast(typename P::Elements, out.raw);
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+        if (i + k < n) state[i + k] = s[k], h[i + k] = e.e[k];
+    }
   }
 }
 
@@ -540,7 +525,8 @@ struct Scan {
 template <typename T, int KIND>
 struct Step {
   static hipError_t run(float* state, const void* gate, const void* u, void* h, int64_t n, hipStream_t stream) {
-    hipLaunchKernelGGL((gated_step_kernel<T, KIND>), dim3(uint32_t(min((n + 255) / 256, int64_t(1) << 20))), dim3(256), 0, stream, state,
+    hipLaunchKernelGGL((gated_step_kernel<T, KIND>), dim3(uint32_t(min((n + 256 * kStep - 1) / (256 * kStep), int64_t(1) << 20))),
+                       dim3(256), 0, stream, state,
                        static_cast<const T*>(gate), static_cast<const T*>(u), static_cast<T*>(h), n);
     return hipGetLastError();
   }

@@ -79,4 +79,62 @@ __device__ __forceinline__ int32_t code_of(float v, CodeScale c) {
   return int32_t(k);
 }
 
+typedef unsigned short u16;
+
+// An unsigned word, or vector of words, of VB bytes
+template <int VB>
+struct Bytes;
+template <>
+struct Bytes<16> { typedef v4u type; };
+template <>
+struct Bytes<8> { typedef v2u type; };
+template <>
+struct Bytes<4> { typedef uint32_t type; };
+template <>
+struct Bytes<2> { typedef u16 type; };
+template <>
+struct Bytes<1> { typedef uint8_t type; };
+struct Halves { v4u h[2]; };
+
+// V neighbouring elements as loaded
+template <typename T, int V>
+struct Pack {
+  typedef typename Bytes<sizeof(T) * V>::type Raw;
+  struct Elements { T e[V]; };
+  Raw raw;
+  __device__ __forceinline__ float operator[](int v) const { return to_f32(__builtin_bit_cast(Elements, raw).e[v]); }
+};
+// The codes of V neighbouring elements under scale s, packed.
+template <int V, typename P>
+__device__ __forceinline__ typename Bytes<V>::type codes_of(const P& x, float s) {
+  const CodeScale c = code_scale(s);
+  struct { int8_t e[V]; } q;
+#pragma unroll
+  for (int v = 0; v < V; ++v) q.e[v] = int8_t(code_of(x[v], c));
+  return __builtin_bit_cast(typename Bytes<V>::type, q);
+}
+
+// Largest of the unsigned images over the lanes of a row's 64 channels (LPR consecutive lanes), in
+// every one of them: magnitudes compare as integers, NaN above infinity above the rest.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false)));
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t row_umax(uint32_t m) {
+  if constexpr (LPR >= 2) m = dpp_umax<0xB1>(m);
+  if constexpr (LPR >= 4) m = dpp_umax<0x4E>(m);
+  if constexpr (LPR >= 8) m = dpp_umax<0x141>(m);
+  if constexpr (LPR >= 16) m = dpp_umax<0x140>(m);
+  if constexpr (LPR >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max(uint32_t(r[0]), uint32_t(r[1]));
+  }
+  if constexpr (LPR >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = max(uint32_t(r[0]), uint32_t(r[1]));
+  }
+  return m;
+}
+
 }  // namespace ssdq
