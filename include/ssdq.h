@@ -553,7 +553,7 @@ size_t ssdq_gated_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t
  *   workspace : device scratch of at least ssdq_gated_scan_workspace_size() bytes, owned by the
  *             caller, not shared with a concurrent call; it need not start at any value
  * Any sequences >= 1, tokens >= 0 and 1 <= channels <= 2^20 with tokens < 2^31 - 2^16 and
- * ceil(channels / 64) * (tokens / 256 + sequences) < 2^24 (else SSDQ_ERROR_UNSUPPORTED); dense
+ * ceil(channels / 64) * (tokens / 128 + sequences) < 2^24 (else SSDQ_ERROR_UNSUPPORTED); dense
  * tokens must be a multiple of sequences.  With tokens == 0 the (tokens, ...) pointers are not looked at.
  * A NaN or infinity in gate, u or h0 makes the rows after it in its sequence and channel non-finite
  * or NaN (a = 0 does not clear it: 0 times infinity is NaN), and nothing else.  The result does not

@@ -47,10 +47,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save_kernel(const T* __re
   for (int k = 0; k < kItems; ++k) {
     const Place<V> p(k, items, blocks, channels);
     const Pack<T, V> v{raw[k]};
-    uint32_t most = 0;
-#pragma unroll
-    for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(fabsf(v[e])));
-    const float s = checkpoint_scale(row_umax<LPR>(most));
+    const float s = checkpoint_scale(row_umax<LPR>(largest<T, V>(v, V)));   // (elements past the row are 0)
     if (p.in) *reinterpret_cast<typename Bytes<V>::type*>(codes + p.at) = codes_of<V>(v, s);
     if (threadIdx.x % LPR == 0 && p.item < items) scale[p.item] = s;
   }

@@ -2,69 +2,93 @@
 // single-token step (Ternary Mamba, Section 1, states the recurrence).
 //
 // The maps h -> A h + H compose associatively, (A2, H2) o (A1, H1) = (A2 A1, A2 H1 + H2), so a
-// sequence is cut into tiles of 256 tokens x 64 channels.  A block of 256 threads holds one tile in
-// registers: a thread has V neighbouring channels (16 bytes where the row length allows) of 64 / V
-// consecutive tokens.  It composes its tokens' maps, the maps are scanned over the threads of a wave
-// and the block's waves, the tile's map is published, and the state entering the tile is joined from
-// the maps of the tiles before it; then each thread runs its tokens once more from its entering state
-// and stores.  Every input is read from memory once and every output written once.
+// sequence is cut into tiles of 256 (or 128) tokens x 64 channels.  A block of four waves holds one
+// tile in registers, as it was loaded: a thread has 16 bytes (4 or 8 neighbouring channels) of 8
+// consecutive tokens (4 where fewer are in a tile).  It composes its tokens' maps, the maps are scanned
+// over the threads of a wave and the four waves, the tile's map is published, the state entering the
+// tile is joined from the maps of the tiles before it, and each thread runs its tokens once more from its
+// entering state and stores.  Every input is read from memory once and every output written once.
 //
 // The gradient's recurrence k_t = a_t (dh_t + k_{t+1}) is the same scan from a sequence's end with the
 // maps (a_t, a_t dh_t), so both directions share the code below.
+#include <algorithm>
+
 #include "gated_types.h"
 
 namespace ssdq {
 namespace {
 
 constexpr int kBlock = SSDQ_CHECKPOINT_BLOCK;   // channels of a tile, and of a checkpoint's scale
-constexpr int kRows = 256;                      // tokens of a tile
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kPerThread = kRows * kBlock / kThreads;   // elements of each tensor a thread holds
+
+constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h written beside h
+constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
+constexpr bool is_back(int mode) { return mode >= kBackward; }
+
+// Tokens of a tile.  A thread keeps the raw inputs of rows * 64 / 256 elements and forms a and b from them in
+// both passes (the exponentials cost less than the registers that would keep them).
+#ifndef ROWS32
+#define ROWS32 128
+#endif
+#ifndef ROWSLB
+#define ROWSLB 128
+#endif
+constexpr int tile_rows(int size, int kind, bool back) {
+  return size == 4 ? ROWS32 : back && kind == SSDQ_GATE_LOGIT ? ROWSLB : 256;
+}
+constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
 // Tiles of a sequence are joined in groups: a tile reads the maps of the tiles of its group before
 // it, and of the group before that only the last tile's, which publishes the state it ended with as
 // the map (0, state) once it knows that; so does a sequence's first tile.  This fixes the order of every
 // product and sum (the same bits on every run) and bounds what a tile reads (16 maps) whatever the length.
 constexpr int kGroup = 16;
+constexpr int kPeek = 4;   // maps that are read at a time
 
-// Workspace: a ticket counter and the tiles' maps (A, H), in words that are all ones until
-// published.  A published word is never all ones: A = NaN is stored with one fixed image.
-constexpr size_t kTicketBytes = 256;
+// Workspace of chained tiles: a ticket counter per 64 channels, each on a line of its own; for packed sequences
+// the table of tiles; and the tiles' maps (A, H), in words that are all ones until published.  A published word
+// is never all ones: A = NaN is stored with one fixed image.
+constexpr size_t kTicketBytes = 128;
 constexpr uint64_t kNoMap = ~uint64_t(0);
-constexpr int kMostPolls = 1 << 24;   // far beyond any wait; a state is NaN if it is ever reached
+constexpr int kMostPolls = 1 << 24;   // far beyond any wait; the state would be wrong if it were ever reached
 
-struct Plan {
-  int32_t tiles;        // most tiles of the call
-  int32_t chans;        // channel tiles
-  int32_t per_sequence; // dense: tiles of a sequence (0: packed)
-  bool single;          // every sequence is one tile: nothing is published
-  uint64_t* maps;       // (tiles, chans * 64)
-  uint32_t* ticket;
+struct Tile {
+  int32_t seq;       // -1: no tile
+  int32_t chunk;     // tiles of the sequence before this one, in scan order
+  int32_t chunks;    // tiles of the sequence
+  int32_t base;      // number of the sequence's first tile
+  int32_t first;     // the sequence's first row
+  int32_t len;       // and its rows
 };
 
-// Whole sequences: tiles of the call and whether each sequence fits one.
-bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed, Plan* p) {
+struct Plan {
+  int32_t tiles;        // most tiles of 64 channels
+  int32_t chans;        // blocks of 64 channels
+  int32_t per_sequence; // dense: tiles of a sequence (0: packed)
+  bool chained;         // some sequence may have more than one tile
+  uint32_t* tickets;
+  Tile* table;          // packed and chained: the tiles
+  uint64_t* maps;       // (tiles, chans * 64)
+};
+
+int64_t tiles_of(int64_t len, int rows) { return len <= rows ? 1 : (len + rows - 1) / rows; }
+
+// Sizes of a call for tiles of `rows` tokens; false where a launch cannot hold them.
+bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed, int rows, Plan* p) {
   if (channels > (1 << 20)) return false;   // a tile's byte offsets stay below 2^31
   p->chans = (channels + kBlock - 1) / kBlock;
-  int64_t tiles;
-  if (packed) {
-    p->per_sequence = 0;
-    p->single = tokens <= kRows;
-    tiles = p->single ? sequences : tokens / kRows + sequences;
-  } else {
-    const int64_t len = tokens / sequences;
-    const int64_t per = len <= kRows ? 1 : (len + kRows - 1) / kRows;
-    p->single = per == 1;
-    tiles = per * sequences;
-    p->per_sequence = int32_t(per);
-  }
-  // a grid holds fewer than 2^32 threads
-  if (tiles * p->chans >= (int64_t(1) << 24)) return false;
+  p->per_sequence = packed ? 0 : int32_t(tiles_of(tokens / sequences, rows));
+  p->chained = packed ? tokens > rows : p->per_sequence > 1;
+  const int64_t tiles = !packed ? int64_t(p->per_sequence) * sequences
+                        : p->chained ? tokens / rows + sequences : sequences;
+  if (tiles * p->chans >= (int64_t(1) << 24)) return false;   // a grid holds fewer than 2^32 threads
   p->tiles = int32_t(tiles);
   return true;
 }
-
+size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
+size_t ticket_bytes(const Plan& p) { return round_up(size_t(p.chans) * kTicketBytes); }
+size_t table_bytes(const Plan& p) { return p.per_sequence ? 0 : round_up(size_t(p.tiles) * sizeof(Tile)); }
 size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * sizeof(uint64_t); }
 
 // Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.
@@ -79,19 +103,50 @@ __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { 
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, u16 v) { __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint8_t v) { __builtin_amdgcn_raw_buffer_store_b8(v, r, off, 0, 0); }
 
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_pack(Rsrc r, uint32_t off) {
-  Pack<T, V> p;
-  load_bytes(r, off, p.raw);
-  return p;
-}
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> to_pack(const float (&x)[V]) {
-  typename Pack<T, V>::Elements e;
+// The rows of a tile of one tensor: V elements at byte offset `off`, out of range past the rows' end at `bytes`.
+// Rows of a multiple of V elements go through buffer accesses.  RAGGED rows start at any multiple of the
+// element's size: whole groups of V take plain accesses that need no more alignment than that, and the blocks
+// that hold the rows' ends (whole = false) go element by element, `count` of V.
+template <typename T, int V, bool RAGGED>
+struct Rows {
+  typedef Pack<T, V> P;
+  typedef typename Bytes<sizeof(T)>::type Word;
+  struct __attribute__((packed, aligned(sizeof(T)))) Loose { T e[V]; };
+  struct Words { Word e[V]; };
+  Rsrc rsrc;
+  char* base;
+  uint32_t bytes;
+  bool whole;
+  __device__ __forceinline__ Rows(const T* p, uint32_t n, bool w)
+      : rsrc(make_rsrc(p, n)), base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), whole(w) {}
+  __device__ __forceinline__ P load(uint32_t off, int count) const {
+    P v;
+    if constexpr (!RAGGED) {
+      load_bytes(rsrc, off, v.raw);
+    } else if (whole) {
+      Loose e = {};
+      if (off < bytes) e = *reinterpret_cast<const Loose*>(base + off);
+      v.raw = __builtin_bit_cast(typename P::Raw, e);
+    } else {
+      Words w;
 #pragma unroll
-  for (int v = 0; v < V; ++v) e.e[v] = from_f32<T>(x[v]);
-  return Pack<T, V>{__builtin_bit_cast(typename Pack<T, V>::Raw, e)};
-}
+      for (int k = 0; k < V; ++k) load_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, w.e[k]);
+      v.raw = __builtin_bit_cast(typename P::Raw, w);
+    }
+    return v;
+  }
+  __device__ __forceinline__ void store(uint32_t off, int count, P v) const {
+    if constexpr (!RAGGED) {
+      store_bytes(rsrc, off, v.raw);
+    } else if (whole) {
+      if (off < bytes) *reinterpret_cast<Loose*>(base + off) = __builtin_bit_cast(Loose, v.raw);
+    } else {
+      const Words w = __builtin_bit_cast(Words, v.raw);
+#pragma unroll
+      for (int k = 0; k < V; ++k) store_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, w.e[k]);
+    }
+  }
+};
 
 __device__ __forceinline__ uint64_t map_word(float A, float H) {
   const uint32_t a = A != A ? 0x7FC00000u : __float_as_uint(A);
@@ -111,169 +166,129 @@ __device__ __forceinline__ void sequence_rows(const GatedArgs& g, int s, int32_t
   first = min(max(g.offsets[s], 0), int32_t(g.tokens));
   last = min(max(g.offsets[s + 1], first), int32_t(g.tokens));
 }
-__device__ __forceinline__ int32_t sequence_tiles(int32_t len) { return len <= kRows ? 1 : (len + kRows - 1) / kRows; }
 
-struct Tile {
-  int32_t seq;       // -1: no such tile
-  int32_t chunk;     // tiles of the sequence before this one, in scan order
-  int32_t chunks;    // tiles of the sequence
-  int32_t base;      // index of the sequence's first tile in the workspace
-  int32_t first;     // the sequence's rows
-  int32_t len;
-};
 
-// Tile number i of a packed call: each thread counts the tiles of a run of sequences, a scan over the
-// block finds the run that holds tile i, and its thread the sequence.
-__device__ __forceinline__ Tile packed_tile(const GatedArgs& g, int32_t i, Tile* shared, int32_t* sums) {
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  const int per = (g.sequences + kThreads - 1) / kThreads;
-  const int s0 = min(tid * per, g.sequences), s1 = min(s0 + per, g.sequences);
-  int32_t mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    int32_t a, b;
-    sequence_rows(g, s, a, b);
-    mine += sequence_tiles(b - a);
-  }
-  int32_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int32_t v = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 63) sums[wave] = upto;
-  if (tid == 0) shared->seq = -1;
-  __syncthreads();
-  int32_t before = upto - mine;
-  for (int w = 0; w < wave; ++w) before += sums[w];
-  if (i >= before && i < before + mine) {
-    for (int s = s0; s < s1; ++s) {
-      int32_t a, b;
-      sequence_rows(g, s, a, b);
-      const int32_t n = sequence_tiles(b - a);
-      if (i < before + n) {
-        *shared = Tile{s, i - before, n, before, a, b - a};
-        break;
-      }
-      before += n;
-    }
-  }
-  __syncthreads();
-  return *shared;
-}
+// Makes the second pass form a and b from the raw inputs again instead of keeping them from the first.
+__device__ __forceinline__ void opaque(v4u& v) { asm volatile("" : "+v"(v)); }
 
-// What the backward pass reads the saved states from, and what the forward pass writes
-constexpr int kForward = 0, kForwardSave = 1, kBackward = 2, kBackwardSaved = 3;
-
-template <typename T, int KIND, int V, int MODE>
+template <typename T, int KIND, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
-  constexpr bool kBack = MODE == kBackward || MODE == kBackwardSaved;
+  constexpr bool kBack = is_back(MODE);
+  constexpr int ROWS = tile_rows(sizeof(T), KIND, kBack);
+  constexpr int V = 16 / int(sizeof(T)); // channels of a thread
   constexpr int LPR = kBlock / V;        // lanes of a row
-  constexpr int kGroups = kWave / LPR;   // runs of tokens in a wave
-  constexpr int R = kPerThread / V;      // tokens of a run
-  static_assert(kGroups * kWaves * R == kRows, "a block holds one tile");
+  constexpr int kRuns = kWave / LPR;     // runs of tokens in a wave
+  constexpr int R = ROWS / (kWaves * kRuns);   // tokens of a run
+  static_assert(R >= 1 && R * kWaves * kRuns == ROWS, "a block holds one tile");
+  typedef Pack<T, V> P;
+  typedef Rows<T, V, RAGGED> Rw;
 
   __shared__ float sA[kWaves][kBlock], sH[kWaves][kBlock], sIn[kBlock];
-  __shared__ Tile sTile;
-  __shared__ int32_t sSums[kWaves];
-  __shared__ uint32_t sTicket;
+  __shared__ int32_t sTicket;
 
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // Tiles are taken in the order in which blocks start, so that a tile's predecessors are always
-  // held by blocks that run already; they publish before they wait for anything.
-  uint32_t order = blockIdx.x;
-  if (!p.single) {
-    if (tid == 0) sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
+  // blocks then use all channels of its L2.  (With the 8 XCDs' blocks interleaved, each XCD met only the
+  // lines of one residue mod 1 KB: 109 -> 118 us at 16384 x 5120 fp16.)
+  const int32_t blk = xcd_remap(int32_t(blockIdx.x % uint32_t(p.chans)), p.chans);
+  int32_t index = int32_t(blockIdx.x / uint32_t(p.chans));
+  if (p.chained) {
+    // Tiles are taken by tickets, in the order in which blocks start, so that a tile's predecessors (lower
+    // tickets of the same channels) are held by blocks that run already and publish before they wait for anything
+    // but lower tickets: every wait ends.  One counter for all channels would serialize the starts.
+    if (tid == 0)
+      sTicket = int32_t(__hip_atomic_fetch_add(p.tickets + size_t(blk) * (kTicketBytes / sizeof(uint32_t)), 1u,
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     __syncthreads();
-    order = __builtin_amdgcn_readfirstlane(sTicket);
+    index = __builtin_amdgcn_readfirstlane(sTicket);
   }
-  const int32_t index = int32_t(order / uint32_t(p.chans));
-  const int32_t blk = int32_t(order % uint32_t(p.chans));
   Tile t;
   if (p.per_sequence) {
-    // dense: first tiles of all sequences, then their second ones, ...
-    const int32_t len = int32_t(g.tokens / g.sequences);
+    // dense: the first tiles of all sequences, then their second ones, ...
     t.chunk = index / g.sequences;
     t.seq = index - t.chunk * g.sequences;
     t.chunks = p.per_sequence;
     t.base = t.seq * p.per_sequence;
-    t.first = t.seq * len;
-    t.len = len;
-  } else {
-    t = packed_tile(g, index, &sTile, sSums);
-    t.seq = __builtin_amdgcn_readfirstlane(t.seq);
+    t.len = int32_t(g.tokens / g.sequences);
+    t.first = t.seq * t.len;
+  } else if (p.chained) {
+    t = p.table[index];
     if (t.seq < 0) return;
-    t.chunk = __builtin_amdgcn_readfirstlane(t.chunk);
-    t.chunks = __builtin_amdgcn_readfirstlane(t.chunks);
-    t.base = __builtin_amdgcn_readfirstlane(t.base);
-    t.first = __builtin_amdgcn_readfirstlane(t.first);
-    t.len = __builtin_amdgcn_readfirstlane(t.len);
+  } else {
+    int32_t last;
+    t.chunk = 0;
+    t.seq = index;
+    t.chunks = 1;
+    t.base = 0;
+    sequence_rows(g, index, t.first, last);
+    t.len = last - t.first;
   }
-  const int32_t nrows = min(kRows, t.len - t.chunk * kRows);
+  const int32_t nrows = min(ROWS, t.len - t.chunk * ROWS);
   // rows of the tile: the scan runs from the first to the last, or from the last to the first
-  const int64_t row0 = kBack ? int64_t(t.first) + t.len - t.chunk * kRows - nrows : int64_t(t.first) + t.chunk * kRows;
-
-  const int group = lane / LPR, col = (lane % LPR) * V;
-  const int c = blk * kBlock + col;
-  const bool in = c < g.channels;
-  const uint32_t rowbytes = uint32_t(g.channels) * uint32_t(sizeof(T));
-  const uint32_t tilebytes = uint32_t(nrows) * rowbytes;
-  const int run = (wave * kGroups + group) * R;   // scan position of the run's first token
-  // byte offset of scan position run + i in the tile: base + i * step; past the tile's rows it is out of
-  // range (below zero it wraps to above 2^31), and so it is in every row for a lane past the channels
-  const uint32_t base = !in ? kOutOfRange
-                            : uint32_t(kBack ? nrows - 1 - run : run) * rowbytes + uint32_t(c) * uint32_t(sizeof(T));
-  const uint32_t step = !in ? 0u : kBack ? 0u - rowbytes : rowbytes;
+  const int64_t row0 = kBack ? int64_t(t.first) + t.len - t.chunk * ROWS - nrows : int64_t(t.first) + t.chunk * ROWS;
   const int64_t start = row0 * g.channels;
 
-  const Rsrc rgate = make_rsrc(static_cast<const T*>(g.gate) + start, tilebytes);
-  const Rsrc rsrc = make_rsrc(static_cast<const T*>(kBack ? g.dh : g.u) + start, tilebytes);
-  typedef Pack<T, V> P;
+  const int group = lane / LPR, col = (lane % LPR) * V;
+  const int c = blk * kBlock + col, count = min(V, g.channels - c);
+  const bool in = c < g.channels, whole = (blk + 1) * kBlock <= g.channels;
+  const uint32_t width = uint32_t(g.channels) * uint32_t(sizeof(T)), crow = uint32_t(g.channels);
+  const uint32_t srow = 4u * uint32_t(p.chans);
+  const int run = (wave * kRuns + group) * R;   // scan position of the run's first token
+  // byte offset of token i of the run in rows of `w` bytes, `at` into the row; past the tile's rows it is out of
+  // range (below row 0 it wraps to above 2^31), and so it is for a lane past the channels
+  const auto offset = [&](int i, uint32_t w, uint32_t at) {
+    return in ? uint32_t(kBack ? nrows - 1 - run - i : run + i) * w + at : kOutOfRange;
+  };
+  const auto at_t = [&](int i) { return offset(i, width, uint32_t(c) * uint32_t(sizeof(T))); };
+  const auto at_c = [&](int i) { return offset(i, crow, uint32_t(c)); };
+  const auto at_s = [&](int i) { return offset(i, srow, 4u * uint32_t(blk)); };
+  const auto rows_of = [&](const void* x) {
+    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, whole);
+  };
+
   P pg[R], ps[R];
+  {
+    const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    pg[i] = load_pack<T, V>(rgate, base + uint32_t(i) * step);
-    ps[i] = load_pack<T, V>(rsrc, base + uint32_t(i) * step);
+    for (int i = 0; i < R; ++i) {
+      pg[i] = rg.load(at_t(i), count);
+      ps[i] = rs.load(at_t(i), count);
+    }
   }
-  // the states that the tokens start from are those of the row before; the sequence's first token
-  // starts from h0, so its row is out of range
+  // The states that the tokens start from are those of the row before; the sequence's first token starts from
+  // h0, and its row is out of range.
+  const int first_at = kBack && row0 == t.first ? nrows - 1 - run : -1;   // that token's place in the run
   P ph[R], pu[R];
-  typedef Pack<int8_t, V> PC;
-  PC pc[R];
+  Pack<int8_t, V> pc[R];
   float sc[R];
-  if constexpr (kBack) {
-    const bool has_first = row0 == t.first;
-    // position of the first token in this run, or none
-    const int first_at = has_first ? nrows - 1 - run : -1;
-    if constexpr (MODE == kBackward) {
-      const Rsrc rh = make_rsrc(static_cast<const T*>(g.h) + (start - g.channels), tilebytes);
+  if constexpr (MODE == kBackward) {
+    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, whole);
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        ph[i] = load_pack<T, V>(rh, i == first_at ? kOutOfRange : base + uint32_t(i) * step);
-    } else {
-      const uint32_t crow = uint32_t(g.channels), srow = 4u * uint32_t(p.chans);
-      const Rsrc rc = make_rsrc(g.codes + (start - g.channels), uint32_t(nrows) * crow);
-      const Rsrc rs = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
-      const uint32_t cbase = in ? uint32_t(nrows - 1 - run) * crow + uint32_t(c) : kOutOfRange;
-      const uint32_t cstep = in ? 0u - crow : 0u;
-      const uint32_t sbase = uint32_t(nrows - 1 - run) * srow + 4u * uint32_t(blk);
+    for (int i = 0; i < R; ++i) ph[i] = rh.load(i == first_at ? kOutOfRange : at_t(i), count);
+  } else if constexpr (MODE == kBackwardSaved) {
+    const Rows<int8_t, V, RAGGED> rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, whole);
+    const Rsrc rs = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        pc[i] = load_pack<int8_t, V>(rc, i == first_at ? kOutOfRange : cbase + uint32_t(i) * cstep);
-        sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : sbase - uint32_t(i) * srow);
-      }
+    for (int i = 0; i < R; ++i) {
+      pc[i] = rc.load(i == first_at ? kOutOfRange : at_c(i), count);
+      sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : at_s(i));
     }
-    if constexpr (KIND == SSDQ_GATE_LOGIT) {
-      const Rsrc ru = make_rsrc(static_cast<const T*>(g.u) + start, tilebytes);
+  }
+  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) {
+    const Rw ru = rows_of(g.u);
 #pragma unroll
-      for (int i = 0; i < R; ++i) pu[i] = load_pack<T, V>(ru, base + uint32_t(i) * step);
-    }
+    for (int i = 0; i < R; ++i) pu[i] = ru.load(at_t(i), count);
   }
 
-  // a run's map, token by token.  A row past the tile has gate and input 0: the identity for a log
-  // gate, made the identity for a logit below.
-  float a[R][V], b[R][V], cc[R][V];   // b: what a token adds (forward), dh (backward)
+  // a token's a, what it adds (backward: dh) and what multiplies its input.  A row past the tile has gate and
+  // input 0: the identity for a log gate, made the identity for a logit here.
+  const auto token = [&](int i, int v, float& a, float& b, float& m) {
+    gate_terms<KIND, sizeof(T) == 4>(pg[i][v], a, m);
+    if (KIND == SSDQ_GATE_LOGIT && run + i >= nrows) a = 1.f;
+    b = kBack || KIND == SSDQ_GATE_LOG ? ps[i][v] : m * ps[i][v];
+  };
   float A[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
@@ -281,21 +296,18 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   for (int i = 0; i < R; ++i) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float m;
-      gate_terms<KIND>(pg[i][v], a[i][v], m);
-      if constexpr (KIND == SSDQ_GATE_LOGIT) {
-        if (run + i >= nrows) a[i][v] = 1.f;
-        if constexpr (kBack) cc[i][v] = m;
-      }
-      b[i][v] = kBack || KIND == SSDQ_GATE_LOG ? ps[i][v] : m * ps[i][v];
-      A[v] *= a[i][v];
-      H[v] = kBack ? a[i][v] * (b[i][v] + H[v]) : fmaf(a[i][v], H[v], b[i][v]);
+      float a, b, m;
+      token(i, v, a, b, m);
+      A[v] *= a;
+      H[v] = kBack ? a * (b + H[v]) : fmaf(a, H[v], b);
     }
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i) opaque(pg[i].raw), opaque(ps[i].raw);
 
   // inclusive scan of the runs' maps within the wave, then each run's exclusive map
 #pragma unroll
-  for (int o = 1; o < kGroups; o <<= 1) {
+  for (int o = 1; o < kRuns; o <<= 1) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float pA = __shfl_up(A[v], o * LPR, 64), pH = __shfl_up(H[v], o * LPR, 64);
@@ -305,20 +317,15 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
       }
     }
   }
-  if (group == kGroups - 1) {
+  if (group == kRuns - 1) {
 #pragma unroll
     for (int v = 0; v < V; ++v) sA[wave][col + v] = A[v], sH[wave][col + v] = H[v];
   }
-  if constexpr (kGroups > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float pA = __shfl_up(A[v], LPR, 64), pH = __shfl_up(H[v], LPR, 64);
-      A[v] = group ? pA : 1.f;
-      H[v] = group ? pH : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
+  for (int v = 0; v < V; ++v) {
+    const float pA = __shfl_up(A[v], LPR, 64), pH = __shfl_up(H[v], LPR, 64);
+    A[v] = group ? pA : 1.f;
+    H[v] = group ? pH : 0.f;
   }
   __syncthreads();
 
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     // a lane per channel: the tile's map, and the state entering the tile
     const int64_t cpad = int64_t(p.chans) * kBlock, ch = int64_t(blk) * kBlock + lane;
     const bool some = ch < g.channels;
-    const int64_t sat = int64_t(t.seq) * g.channels + ch;
+    const int64_t at = int64_t(t.seq) * g.channels + ch;
     float tA = 1.f, tH = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -339,108 +346,157 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     float x = 0.f;
     if (t.chunk == 0) {
       // only this tile reads the initial state (which the final one may overwrite)
-      x = some && init ? init[sat] : 0.f;
+      x = some && init ? init[at] : 0.f;
     } else {
       if (!last && !ends_group) publish(maps + int64_t(t.chunk) * cpad, map_word(tA, tH));
       const int from = max(t.chunk / kGroup * kGroup - 1, 0), n = t.chunk - from;
-      uint64_t got[kGroup];
-      for (int polls = 0;; ++polls) {
-        bool all = true;
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += kPeek) {
+        uint64_t got[kPeek];
+        for (int polls = 0;; ++polls) {
+          bool all = true;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          if (j < n) {
-            got[j] = peek(maps + int64_t(from + j) * cpad);
+          for (int j = 0; j < kPeek; ++j) {
+            got[j] = peek(maps + int64_t(from + min(j0 + j, n - 1)) * cpad);
             all = all && got[j] != kNoMap;
           }
+          if (__all(all) || polls == kMostPolls) break;
+          __builtin_amdgcn_s_sleep(1);
         }
-        if (__all(all) || polls == kMostPolls) break;
-        __builtin_amdgcn_s_sleep(1);
-      }
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (j < n) x = fmaf(__uint_as_float(uint32_t(got[j])), x, __uint_as_float(uint32_t(got[j] >> 32)));
+        for (int j = 0; j < kPeek; ++j)
+          if (j0 + j < n) x = fmaf(__uint_as_float(uint32_t(got[j])), x, __uint_as_float(uint32_t(got[j] >> 32)));
+      }
     }
     sIn[lane] = x;
     const float end = fmaf(tA, x, tH);
     if (!last && (t.chunk == 0 || ends_group)) publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
     float* out = kBack ? g.dh0 : g.h_final;
-    if (last && out && some) out[sat] = t.len ? end : x;
+    if (last && out && some) out[at] = t.len ? end : x;
   }
   __syncthreads();
 
   // the state entering each run: the tile's, then the waves before, then the runs before
   float x[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float y = sIn[col + v];
-    for (int w = 0; w < wave; ++w) y = fmaf(sA[w][col + v], y, sH[w][col + v]);
-    x[v] = fmaf(A[v], y, H[v]);
+  for (int v = 0; v < V; ++v) x[v] = sIn[col + v];
+  for (int w = 0; w < wave; ++w) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = fmaf(sA[w][col + v], x[v], sH[w][col + v]);
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = fmaf(A[v], x[v], H[v]);
 
   if constexpr (!kBack) {
-    const Rsrc rh = make_rsrc(static_cast<T*>(g.h) + start, tilebytes);
+    const Rw rh = rows_of(g.h);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = fmaf(a[i][v], x[v], b[i][v]);
+      for (int v = 0; v < V; ++v) {
+        float a, b, m;
+        token(i, v, a, b, m);
+        x[v] = fmaf(a, x[v], b);
+      }
       const P out = to_pack<T, V>(x);
-      store_bytes(rh, base + uint32_t(i) * step, out.raw);
+      rh.store(at_t(i), count, out);
       if constexpr (MODE == kForwardSave) {
-        uint32_t most = 0;
-        if (in) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) most = max(most, __float_as_uint(fabsf(out[v])));
-        }
-        const float s = checkpoint_scale(row_umax<LPR>(most));
-        const uint32_t crow = uint32_t(g.channels), srow = 4u * uint32_t(p.chans);
-        const Rsrc rc = make_rsrc(g.codes + start, uint32_t(nrows) * crow);
+        const float scale = checkpoint_scale(row_umax<LPR>(largest<T, V>(out, RAGGED ? count : in ? V : 0)));
+        const Rows<int8_t, V, RAGGED> rc(g.codes + start, uint32_t(nrows) * crow, whole);
         const Rsrc rs = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
-        store_bytes(rc, in ? uint32_t(run + i) * crow + uint32_t(c) : kOutOfRange,
-                    codes_of<V>(out, s));
-        store_bytes(rs, col == 0 ? uint32_t(run + i) * srow + 4u * uint32_t(blk) : kOutOfRange, __float_as_uint(s));
+        rc.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
+        store_bytes(rs, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
       }
     }
   } else {
-    const Rsrc rdg = make_rsrc(static_cast<T*>(g.dgate) + start, tilebytes);
-    const Rsrc rdu = make_rsrc(static_cast<T*>(g.du) + start, tilebytes);
-    const int first_at = row0 == t.first ? nrows - 1 - run : -1;
+    const Rw rdg = rows_of(g.dgate), rdu = rows_of(g.du);
     float h0[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h0[v] = 0.f;
-    if (g.h0 && in && first_at >= 0 && first_at < R) {
+    if (g.h0 && first_at >= 0 && first_at < R) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h0[v] = g.h0[int64_t(t.seq) * g.channels + c + v];
+      for (int v = 0; v < V; ++v)
+        if (v < count) h0[v] = g.h0[int64_t(t.seq) * g.channels + c + v];
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float dg[V], du[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float before;
+        float a, b, m, before;
+        token(i, v, a, b, m);
         if constexpr (MODE == kBackward) before = ph[i][v];
         else before = pc[i][v] * sc[i];
         if (i == first_at) before = h0[v];
-        const float d = b[i][v] + x[v];
-        x[v] = a[i][v] * d;
+        const float d = b + x[v];
+        x[v] = a * d;
         if constexpr (KIND == SSDQ_GATE_LOG) {
           dg[v] = x[v] * before;
           du[v] = d;
         } else {
-          dg[v] = x[v] * cc[i][v] * (before - pu[i][v]);
-          du[v] = cc[i][v] * d;
+          dg[v] = x[v] * m * (before - pu[i][v]);
+          du[v] = m * d;
         }
       }
-      store_bytes(rdg, base + uint32_t(i) * step, to_pack<T, V>(dg).raw);
-      store_bytes(rdu, base + uint32_t(i) * step, to_pack<T, V>(du).raw);
+      rdg.store(at_t(i), count, to_pack<T, V>(dg));
+      rdu.store(at_t(i), count, to_pack<T, V>(du));
     }
   }
 }
 
-// Sets the ticket to 0 and every published word to "not yet".
-__global__ void __launch_bounds__(256) gated_clear_kernel(v4u* words, int64_t n, uint32_t* ticket) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i == 0) *ticket = 0;
-  for (int64_t k = i; k < n; k += int64_t(gridDim.x) * 256) words[k] = v4u{~0u, ~0u, ~0u, ~0u};
+// Before chained tiles: the tickets to 0, every map to "not yet", and for packed sequences the table of
+// tiles, by the last block.
+__global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, int64_t zeros, int64_t words,
+                                                          int rows) {
+  const bool packed = p.per_sequence == 0;
+  if (packed && blockIdx.x == gridDim.x - 1) {
+    __shared__ Tile seq[256];
+    const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+    __shared__ int64_t sums[4];
+    int64_t base = 0;   // in 64 bits: overlapping sequences could have any number of tiles
+    for (int s0 = 0; s0 < g.sequences && base < p.tiles; s0 += 256) {
+      int32_t lo = 0, hi = 0, n = 0;
+      if (s0 + tid < g.sequences) {
+        sequence_rows(g, s0 + tid, lo, hi);
+        n = hi - lo <= rows ? 1 : (hi - lo + rows - 1) / rows;
+      }
+      int64_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t v = __shfl_up(upto, o, 64);
+        if (lane >= o) upto += v;
+      }
+      __syncthreads();   // the strip before is in the table
+      if (lane == 63) sums[wave] = upto;
+      __syncthreads();
+      int64_t total = 0;
+      for (int w = 0; w < 4; ++w) {
+        if (w < wave) upto += sums[w];
+        total += sums[w];
+      }
+      const int64_t mine = base + upto - n;
+      seq[tid] = Tile{s0 + tid, 0, n, int32_t(mine < p.tiles ? mine : p.tiles), lo, hi - lo};
+      __syncthreads();
+      // tiles past the table's end (of overlapping sequences) are left out
+      const int32_t end = int32_t(base + total < p.tiles ? base + total : p.tiles);
+      for (int32_t i = int32_t(base) + tid; i < end; i += 256) {
+        int k = 0;
+        for (int step = 128; step >= 1; step >>= 1)
+          if (seq[k + step].base <= i) k += step;   // the last sequence of the strip that starts at i or before
+        Tile t = seq[k];
+        t.chunk = i - t.base;
+        p.table[i] = t;
+      }
+      base += total;
+    }
+    for (int64_t i = base + tid; i < p.tiles; i += 256) p.table[i].seq = -1;
+    return;
+  }
+  const int64_t stride = int64_t(gridDim.x - (packed ? 1 : 0)) * 256;
+  const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  v4u* tickets = reinterpret_cast<v4u*>(p.tickets);
+  v4u* maps = reinterpret_cast<v4u*>(p.maps);
+  for (int64_t k = first; k < zeros; k += stride) tickets[k] = v4u{0u, 0u, 0u, 0u};
+  for (int64_t k = first; k < words; k += stride) maps[k] = v4u{~0u, ~0u, ~0u, ~0u};
 }
 
 // Elementwise over batch * channels: 4 elements per thread (16 bytes of state), whatever the row length.
@@ -473,7 +529,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(float* __restrict__ sta
 #pragma unroll
     for (int e = 0; e < kStep; ++e) {
       float a, m;
-      gate_terms<KIND>(pg[e], a, m);
+      gate_terms<KIND, sizeof(T) == 4>(pg[e], a, m);
       s[e] = fmaf(a, s[e], KIND == SSDQ_GATE_LOG ? pu[e] : m * pu[e]);
     }
     const P out = to_pack<T, kStep>(s);
@@ -501,24 +557,37 @@ hipError_t dispatch(int32_t dtype, int32_t kind, A... args) {
   }
 }
 
-template <typename T, int KIND, int V>
+template <typename T, int KIND, bool RAGGED>
 void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t stream) {
   const dim3 grid(uint32_t(p.tiles) * uint32_t(p.chans)), block(kThreads);
   if (back) {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, V, kBackwardSaved>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, V, kBackward>), grid, block, 0, stream, g, p);
+    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kBackwardSaved, RAGGED>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kBackward, RAGGED>), grid, block, 0, stream, g, p);
   } else {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, V, kForwardSave>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, V, kForward>), grid, block, 0, stream, g, p);
+    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kForwardSave, RAGGED>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kForward, RAGGED>), grid, block, 0, stream, g, p);
   }
 }
 
 template <typename T, int KIND>
 struct Scan {
-  static hipError_t run(const GatedArgs* g, const Plan* p, bool back, hipStream_t stream) {
-    constexpr int kWide = 16 / int(sizeof(T));
-    if (g->channels % kWide == 0) launch_mode<T, KIND, kWide>(*g, *p, back, stream);
-    else launch_mode<T, KIND, 1>(*g, *p, back, stream);
+  static hipError_t run(const GatedArgs* g, bool back, hipStream_t stream) {
+    const int rows = tile_rows(sizeof(T), KIND, back);
+    Plan p = {};
+    if (!plan_sizes(g->sequences, g->tokens, g->channels, g->offsets != nullptr, rows, &p)) return hipErrorInvalidValue;
+    if (p.chained) {
+      char* ws = static_cast<char*>(g->workspace);
+      p.tickets = reinterpret_cast<uint32_t*>(ws);
+      p.table = reinterpret_cast<Tile*>(ws + ticket_bytes(p));
+      p.maps = reinterpret_cast<uint64_t*>(ws + ticket_bytes(p) + table_bytes(p));
+      const int64_t zeros = int64_t(ticket_bytes(p) / sizeof(v4u)), words = int64_t(map_bytes(p) / sizeof(v4u));
+      const uint32_t blocks = uint32_t(std::min((words + 255) / 256, int64_t(1024))) + (p.per_sequence ? 0 : 1);
+      hipLaunchKernelGGL(gated_clear_kernel, dim3(blocks), dim3(256), 0, stream, *g, p, zeros, words, rows);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (g->channels % (16 / int(sizeof(T))) == 0) launch_mode<T, KIND, false>(*g, p, back, stream);
+    else launch_mode<T, KIND, true>(*g, p, back, stream);
     return hipGetLastError();
   }
 };
@@ -532,33 +601,20 @@ struct Step {
   }
 };
 
-hipError_t launch_scan(const GatedArgs& g, bool back, hipStream_t stream) {
-  Plan p = {};
-  if (!plan_sizes(g.sequences, g.tokens, g.channels, g.offsets != nullptr, &p)) return hipErrorInvalidValue;
-  char* ws = static_cast<char*>(g.workspace);
-  p.ticket = reinterpret_cast<uint32_t*>(ws);
-  p.maps = reinterpret_cast<uint64_t*>(ws + kTicketBytes);
-  if (!p.single) {
-    const int64_t words = int64_t(map_bytes(p) / sizeof(v4u));
-    const uint32_t blocks = uint32_t(min((words + 255) / 256, int64_t(1024)));
-    hipLaunchKernelGGL(gated_clear_kernel, dim3(blocks), dim3(256), 0, stream,
-                       reinterpret_cast<v4u*>(ws + kTicketBytes), words, p.ticket);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return dispatch<Scan>(g.dtype, g.gate_kind, &g, &p, back, stream);
-}
-
 }  // namespace
 
 size_t gated_workspace_bytes(int32_t sequences, int64_t tokens, int32_t channels, bool packed) {
   Plan p = {};
-  if (!plan_sizes(sequences, tokens, channels, packed, &p)) return 0;
-  return p.single ? kTicketBytes : kTicketBytes + map_bytes(p);
+  if (!plan_sizes(sequences, tokens, channels, packed, kFewestRows, &p)) return 0;
+  return p.chained ? ticket_bytes(p) + table_bytes(p) + map_bytes(p) : 256;
 }
 
-hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t stream) { return launch_scan(a, false, stream); }
-hipError_t launch_gated_backward(const GatedArgs& a, hipStream_t stream) { return launch_scan(a, true, stream); }
+hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t stream) {
+  return dispatch<Scan>(a.dtype, a.gate_kind, &a, false, stream);
+}
+hipError_t launch_gated_backward(const GatedArgs& a, hipStream_t stream) {
+  return dispatch<Scan>(a.dtype, a.gate_kind, &a, true, stream);
+}
 hipError_t launch_gated_step(int32_t dtype, int32_t gate_kind, float* state, const void* gate, const void* u, void* h,
                              int64_t n, hipStream_t stream) {
   return dispatch<Step>(dtype, gate_kind, state, gate, u, h, n, stream);

@@ -16,36 +16,38 @@ __device__ __forceinline__ T from_f32(float v) {
   return T(v);
 }
 
-// exp(x) within about 1.5 ulp: the product x log2(e) carried as a pair, its low part applied to
-// the hardware exp2 as a factor 1 + lo ln 2.  (The hardware exp2 of the rounded product alone is
-// off by |x| 2^-24, which a recurrence over hundreds of tokens would add up.)  -inf gives 0, +inf
-// gives +inf, a result below 2^-126 gives 0.
+// exp(x).  -inf gives 0, +inf gives +inf, a result below 2^-126 gives 0.
+//
+// EXACT (for binary32 tensors): within 3 * 2^-24 of itself, the product x log2(e) carried as a pair whose low part
+// is applied to the hardware exp2 as a factor 1 + low ln 2.  Otherwise exp2 of the rounded product, within
+// (|x| + 2) 2^-24: for tensors of 16 bits that vanishes in their rounding, and in a state the part with |x|
+// cannot add up, since a gate of log x is forgotten after about 1 / |x| tokens.
+template <bool EXACT>
 __device__ __forceinline__ float exp_f32(float x) {
   constexpr float kLog2e = 1.44269502e+00f;      // log2(e) rounded to binary32
   constexpr float kLog2eLow = 1.92596298e-08f;   // log2(e) - kLog2e
   constexpr float kLn2 = 6.93147182e-01f;
   const float hi = x * kLog2e;
-  const float lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -hi));
   const float e = __builtin_amdgcn_exp2f(hi);
+  if constexpr (!EXACT) return e;
+  const float lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -hi));
   // overflow, underflow, infinities and NaN: e alone is the answer (lo may be NaN there)
   return fabsf(hi) < 128.f ? fmaf(e, lo * kLn2, e) : e;
 }
 
 // The gate's a, and what multiplies u in b (1 for a log gate).
-template <int KIND>
+template <int KIND, bool EXACT>
 __device__ __forceinline__ void gate_terms(float g, float& a, float& c) {
   if constexpr (KIND == SSDQ_GATE_LOG) {
-    a = exp_f32(g);
+    a = exp_f32<EXACT>(g);
     c = 1.f;
   } else {
-    // with e = exp(-|g|) both sigmoids keep their relative precision on either side
-    const float e = exp_f32(-fabsf(g));
-    const float small = 1.f + e;
-    float inv = __builtin_amdgcn_rcpf(small);
-    inv = fmaf(fmaf(-small, inv, 1.f), inv, inv);   // one Newton step: within an ulp
-    const float low = e * inv;
-    a = g < 0.f ? low : inv;
-    c = g < 0.f ? inv : low;
+    // 1 - a = e a keeps its relative precision where a is near 1; below -80 it is 1 to the last bit
+    const float e = exp_f32<EXACT>(-g), sum = 1.f + e;
+    const float inv = __builtin_amdgcn_rcpf(sum);
+    // one Newton step, within an ulp (a sum that overflows has the inverse 0 already)
+    a = sum < 1e38f ? fmaf(fmaf(-sum, inv, 1.f), inv, inv) : inv;
+    c = g < -80.f ? 1.f : e * a;
   }
 }
 
@@ -56,27 +58,6 @@ __device__ __forceinline__ float checkpoint_scale(uint32_t most) {
   const float m = __uint_as_float(most);
   constexpr float kSmallest = 127.f * 1.17549435e-38f;   // 127 * 2^-126
   return m < kSmallest ? 0.f : m * (1.f / 127.f);
-}
-
-// The code of v under scale s: the integer nearest to the exact quotient v / s, ties to even.
-// k = rint(v rcp(s)) is one of the two nearest integers, since the product is within 2^-14 of the
-// quotient, and v - k s is exact in one fma (|v - k s| stays near s / 2 and is a multiple of the
-// smaller operand's last place), so comparing it with s / 2 decides the rest exactly.
-struct CodeScale {
-  float rcp, half, s;
-};
-__device__ __forceinline__ CodeScale code_scale(float s) {
-  // a zero or NaN scale codes everything as 0
-  const bool some = s > 0.f;
-  return CodeScale{some ? __builtin_amdgcn_rcpf(s) : 0.f, some ? 0.5f * s : __builtin_inff(), some ? s : 0.f};
-}
-__device__ __forceinline__ int32_t code_of(float v, CodeScale c) {
-  float k = rintf(v * c.rcp);
-  const float r = fmaf(-k, c.s, v);
-  if (fabsf(r) > c.half) k += r > 0.f ? 1.f : -1.f;
-  // a tie between k and its neighbour: the even one
-  else if (fabsf(r) == c.half && (int32_t(k) & 1)) k += r > 0.f ? 1.f : -1.f;
-  return int32_t(k);
 }
 
 typedef unsigned short u16;
@@ -104,14 +85,70 @@ struct Pack {
   Raw raw;
   __device__ __forceinline__ float operator[](int v) const { return to_f32(__builtin_bit_cast(Elements, raw).e[v]); }
 };
-// The codes of V neighbouring elements under scale s, packed.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> to_pack(const float (&x)[V]) {
+  typename Pack<T, V>::Elements e;
+#pragma unroll
+  for (int v = 0; v < V; ++v) e.e[v] = from_f32<T>(x[v]);
+  return Pack<T, V>{__builtin_bit_cast(typename Pack<T, V>::Raw, e)};
+}
+
+// The codes of V neighbouring elements under scale s, packed: the integers nearest to the exact quotients, ties
+// to even.  k = rint(v rcp(s)), formed in the binade of 1.5 * 2^23 where the spacing is 1, is one of the two
+// nearest integers (the product is within 2^-14 of the quotient), and r = v - k s is exact in one fma (it stays
+// near s / 2 and is a multiple of the smaller operand's last place).  So k is right wherever |r| < s / 2, and
+// only where some |r| of the V reaches it does a branch decide.  A zero or NaN scale codes everything as 0.
 template <int V, typename P>
 __device__ __forceinline__ typename Bytes<V>::type codes_of(const P& x, float s) {
-  const CodeScale c = code_scale(s);
-  struct { int8_t e[V]; } q;
+  constexpr float kRound = 12582912.f;   // 1.5 * 2^23
+  struct { int8_t e[V]; } q = {};
+  if (s > 0.f) {
+    const float rcp = __builtin_amdgcn_rcpf(s), half = 0.5f * s;
+    float t[V], r[V], most = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) q.e[v] = int8_t(code_of(x[v], c));
+    for (int v = 0; v < V; ++v) {
+      t[v] = fmaf(x[v], rcp, kRound);
+      r[v] = fmaf(-(t[v] - kRound), s, x[v]);
+      most = fmaxf(most, fabsf(r[v]));
+    }
+    if (most >= half) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool odd = __float_as_uint(t[v]) & 1u;
+        if (fabsf(r[v]) > half || (fabsf(r[v]) == half && odd)) t[v] += r[v] > 0.f ? 1.f : -1.f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) q.e[v] = int8_t(__float_as_uint(t[v]) & 0xffu);   // the integer's low byte
+  }
   return __builtin_bit_cast(typename Bytes<V>::type, q);
+}
+
+// The largest magnitude of the first `count` of V elements, as the image of a binary32 number: magnitudes compare
+// as integers, NaN above infinity above the rest.
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+template <typename T, int V>
+__device__ __forceinline__ uint32_t largest(const Pack<T, V>& x, int count) {
+  if constexpr (sizeof(T) == 2 && V == 8) {
+    v4u w = x.raw & 0x7fff7fffu;
+    if (count < V) {   // the elements past the row's end count as 0
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] &= 2 * k + 1 < count ? 0xffffffffu : 2 * k < count ? 0xffffu : 0u;
+    }
+    const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+    const v2us m = __builtin_elementwise_max(
+        __builtin_elementwise_max(__builtin_bit_cast(v2us, w0), __builtin_bit_cast(v2us, w1)),
+        __builtin_elementwise_max(__builtin_bit_cast(v2us, w2), __builtin_bit_cast(v2us, w3)));
+    const unsigned short top = m[0] > m[1] ? m[0] : m[1];
+    return __float_as_uint(to_f32(__builtin_bit_cast(T, top)));
+  } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < count) most = max(most, __float_as_uint(fabsf(x[v])));
+    return most;
+  }
 }
 
 // Largest of the unsigned images over the lanes of a row's 64 channels (LPR consecutive lanes), in

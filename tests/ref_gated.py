@@ -10,7 +10,9 @@ N_{t-1} + |b_t|, and S_t = a_t S_{t-1} + N_t (which counts every term once per t
 
     |computed h_t - h_t| <= e (8 S_t + 24 N_t),
 
-before the one rounding to the output's type (half a step, eps / 2 relative).  The same holds for
+before the one rounding to the output's type (half a step, eps / 2 relative).  (For 16-bit tensors exp is within
+(|x| + 2) e instead: a term that passed gates of logarithms x carries y e more, y the sum of their |x|, which
+the 8 per token and the 24 cover up to y = 24 + 3 per token; beyond that the term has decayed below exp(-24).)  The same holds for
 the gradient's recurrence k from behind; a product formed from it adds at most 8 e of its magnitude."""
 from __future__ import annotations
 
