@@ -103,47 +103,80 @@ __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { 
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, u16 v) { __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint8_t v) { __builtin_amdgcn_raw_buffer_store_b8(v, r, off, 0, 0); }
 
-// The rows of a tile of one tensor: V elements at byte offset `off`, out of range past the rows' end at `bytes`.
-// Rows of a multiple of V elements go through buffer accesses.  RAGGED rows start at any multiple of the
-// element's size: whole groups of V take plain accesses that need no more alignment than that, and the blocks
-// that hold the rows' ends (whole = false) go element by element, `count` of V.
-template <typename T, int V, bool RAGGED>
+// The rows of a tile of one tensor, V elements at a time, through buffer accesses.  RAGGED rows (whose length
+// is no multiple of V) differ in two ways.  They start at any multiple of the element's size: where that may be
+// no multiple of 4 bytes (`odd`), a load takes the aligned words around the V elements and shifts them, a store
+// goes to the unaligned address as a plain access.  And the last block of channels holds the rows' ends
+// (`ends`): it goes element by element, `count` of V.
+template <typename T, int V, int R, bool RAGGED>
 struct Rows {
   typedef Pack<T, V> P;
+  typedef typename P::Raw Raw;
   typedef typename Bytes<sizeof(T)>::type Word;
+  static constexpr int kWords = sizeof(Raw) / 4;
   struct __attribute__((packed, aligned(sizeof(T)))) Loose { T e[V]; };
-  struct Words { Word e[V]; };
+  struct Elements { Word e[V]; };
+  struct Words { uint32_t w[kWords]; };
   Rsrc rsrc;
   char* base;
-  uint32_t bytes;
-  bool whole;
-  __device__ __forceinline__ Rows(const T* p, uint32_t n, bool w)
-      : rsrc(make_rsrc(p, n)), base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), whole(w) {}
-  __device__ __forceinline__ P load(uint32_t off, int count) const {
-    P v;
-    if constexpr (!RAGGED) {
-      load_bytes(rsrc, off, v.raw);
-    } else if (whole) {
-      Loose e = {};
-      if (off < bytes) e = *reinterpret_cast<const Loose*>(base + off);
-      v.raw = __builtin_bit_cast(typename P::Raw, e);
-    } else {
-      Words w;
-#pragma unroll
-      for (int k = 0; k < V; ++k) load_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, w.e[k]);
-      v.raw = __builtin_bit_cast(typename P::Raw, w);
+  uint32_t bytes, shift;   // shift: of the first row's address from a multiple of 4
+  bool odd, ends;
+  __device__ __forceinline__ Rows(const T* p, uint32_t n, uint32_t width, bool last)
+      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), odd(false), ends(RAGGED && last) {
+    if constexpr (RAGGED && sizeof(T) < 4) {
+      odd = width % 4 != 0;
+      shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
     }
-    return v;
+    rsrc = make_rsrc(p, n);
+  }
+  // off(i): byte offset of the i-th of R packs, out of range where there is none
+  template <typename F>
+  __device__ __forceinline__ void load(P (&v)[R], F off, int count) const {
+    if (RAGGED && ends) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        Elements e;
+#pragma unroll
+        for (int k = 0; k < V; ++k) load_bytes(rsrc, k < count ? off(i) + k * uint32_t(sizeof(T)) : kOutOfRange, e.e[k]);
+        v[i].raw = __builtin_bit_cast(Raw, e);
+      }
+    } else if (RAGGED && odd) {
+      // the word behind the V elements is only ever used for its first bytes, which are elements of the same row
+      // (this is not the row's last block); it may lie past the tile, so the range is one word wider
+      const Rsrc wide = make_rsrc(base - shift, bytes + shift + 4u);
+      Words w[R];
+      uint32_t behind[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint32_t at = off(i) < bytes ? (off(i) + shift) & ~3u : kOutOfRange;
+        Raw raw;
+        load_bytes(wide, at, raw);
+        w[i] = __builtin_bit_cast(Words, raw);
+        load_bytes(wide, at + 4u * kWords, behind[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint32_t by = 8u * ((off(i) + shift) & 3u);
+        Words x;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          x.w[k] = __builtin_amdgcn_alignbit(k + 1 < kWords ? w[i].w[k + 1] : behind[i], w[i].w[k], by);
+        v[i].raw = __builtin_bit_cast(Raw, x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) load_bytes(rsrc, off(i), v[i].raw);
+    }
   }
   __device__ __forceinline__ void store(uint32_t off, int count, P v) const {
-    if constexpr (!RAGGED) {
-      store_bytes(rsrc, off, v.raw);
-    } else if (whole) {
+    if (RAGGED && ends) {
+      const Elements e = __builtin_bit_cast(Elements, v.raw);
+#pragma unroll
+      for (int k = 0; k < V; ++k) store_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, e.e[k]);
+    } else if (RAGGED && odd) {
       if (off < bytes) *reinterpret_cast<Loose*>(base + off) = __builtin_bit_cast(Loose, v.raw);
     } else {
-      const Words w = __builtin_bit_cast(Words, v.raw);
-#pragma unroll
-      for (int k = 0; k < V; ++k) store_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, w.e[k]);
+      store_bytes(rsrc, off, v.raw);
     }
   }
 };
@@ -181,7 +214,8 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   constexpr int R = ROWS / (kWaves * kRuns);   // tokens of a run
   static_assert(R >= 1 && R * kWaves * kRuns == ROWS, "a block holds one tile");
   typedef Pack<T, V> P;
-  typedef Rows<T, V, RAGGED> Rw;
+  typedef Rows<T, V, R, RAGGED> Rw;
+  typedef Rows<int8_t, V, R, RAGGED> Rc;
 
   __shared__ float sA[kWaves][kBlock], sH[kWaves][kBlock], sIn[kBlock];
   __shared__ int32_t sTicket;
@@ -225,6 +259,10 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     sequence_rows(g, index, t.first, last);
     t.len = last - t.first;
   }
+  // (scalar registers for all that follows from the tile, the buffer descriptors among it)
+  t = Tile{__builtin_amdgcn_readfirstlane(t.seq),  __builtin_amdgcn_readfirstlane(t.chunk),
+           __builtin_amdgcn_readfirstlane(t.chunks), __builtin_amdgcn_readfirstlane(t.base),
+           __builtin_amdgcn_readfirstlane(t.first), __builtin_amdgcn_readfirstlane(t.len)};
   const int32_t nrows = min(ROWS, t.len - t.chunk * ROWS);
   // rows of the tile: the scan runs from the first to the last, or from the last to the first
   const int64_t row0 = kBack ? int64_t(t.first) + t.len - t.chunk * ROWS - nrows : int64_t(t.first) + t.chunk * ROWS;
@@ -232,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
 
   const int group = lane / LPR, col = (lane % LPR) * V;
   const int c = blk * kBlock + col, count = min(V, g.channels - c);
-  const bool in = c < g.channels, whole = (blk + 1) * kBlock <= g.channels;
+  const bool in = c < g.channels, ends = blk == p.chans - 1;
   const uint32_t width = uint32_t(g.channels) * uint32_t(sizeof(T)), crow = uint32_t(g.channels);
   const uint32_t srow = 4u * uint32_t(p.chans);
   const int run = (wave * kRuns + group) * R;   // scan position of the run's first token
@@ -245,17 +283,14 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   const auto at_c = [&](int i) { return offset(i, crow, uint32_t(c)); };
   const auto at_s = [&](int i) { return offset(i, srow, 4u * uint32_t(blk)); };
   const auto rows_of = [&](const void* x) {
-    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, whole);
+    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, width, ends);
   };
 
   P pg[R], ps[R];
   {
     const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      pg[i] = rg.load(at_t(i), count);
-      ps[i] = rs.load(at_t(i), count);
-    }
+    rg.load(pg, at_t, count);
+    rs.load(ps, at_t, count);
   }
   // The states that the tokens start from are those of the row before; the sequence's first token starts from
   // h0, and its row is out of range.
@@ -264,23 +299,16 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   Pack<int8_t, V> pc[R];
   float sc[R];
   if constexpr (MODE == kBackward) {
-    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, whole);
-#pragma unroll
-    for (int i = 0; i < R; ++i) ph[i] = rh.load(i == first_at ? kOutOfRange : at_t(i), count);
+    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, width, ends);
+    rh.load(ph, [&](int i) { return i == first_at ? kOutOfRange : at_t(i); }, count);
   } else if constexpr (MODE == kBackwardSaved) {
-    const Rows<int8_t, V, RAGGED> rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, whole);
+    const Rc rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, crow, ends);
+    rc.load(pc, [&](int i) { return i == first_at ? kOutOfRange : at_c(i); }, count);
     const Rsrc rs = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      pc[i] = rc.load(i == first_at ? kOutOfRange : at_c(i), count);
-      sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : at_s(i));
-    }
+    for (int i = 0; i < R; ++i) sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : at_s(i));
   }
-  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) {
-    const Rw ru = rows_of(g.u);
-#pragma unroll
-    for (int i = 0; i < R; ++i) pu[i] = ru.load(at_t(i), count);
-  }
+  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) rows_of(g.u).load(pu, at_t, count);
 
   // a token's a, what it adds (backward: dh) and what multiplies its input.  A row past the tile has gate and
   // input 0: the identity for a log gate, made the identity for a logit here.
@@ -401,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
       rh.store(at_t(i), count, out);
       if constexpr (MODE == kForwardSave) {
         const float scale = checkpoint_scale(row_umax<LPR>(largest<T, V>(out, RAGGED ? count : in ? V : 0)));
-        const Rows<int8_t, V, RAGGED> rc(g.codes + start, uint32_t(nrows) * crow, whole);
+        const Rc rc(g.codes + start, uint32_t(nrows) * crow, crow, ends);
         const Rsrc rs = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
         rc.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
         store_bytes(rs, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
