@@ -26,16 +26,18 @@ constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h w
 constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
 constexpr bool is_back(int mode) { return mode >= kBackward; }
 
-// Tokens of a tile.  A thread keeps the raw inputs of rows * 64 / 256 elements and forms a and b from them in
-// both passes (the exponentials cost less than the registers that would keep them).
-#ifndef ROWS32
-#define ROWS32 128
+// Tokens of a tile.
+#ifndef ROWSLF
+#define ROWSLF 128
 #endif
-#ifndef ROWSLB
-#define ROWSLB 128
+#ifndef AGAINLF
+#define AGAINLF 0
 #endif
 constexpr int tile_rows(int size, int kind, bool back) {
-  return size == 4 ? ROWS32 : back && kind == SSDQ_GATE_LOGIT ? ROWSLB : 256;
+  return size == 4 ? 128 : kind == SSDQ_GATE_LOGIT ? (back ? 128 : ROWSLF) : 256;
+}
+constexpr bool forms_again(int size, int kind, bool back) {
+  return kind == SSDQ_GATE_LOGIT && !back && size == 2 ? AGAINLF : true;
 }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
@@ -95,68 +97,73 @@ size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * si
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) { v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) { v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0); }
 __device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) { v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, u16& v) { v = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0); }
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint8_t& v) { v = __builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v4u v) { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) { __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0); }
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, 0); }
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, u16 v) { __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0); }
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint8_t v) { __builtin_amdgcn_raw_buffer_store_b8(v, r, off, 0, 0); }
 
 // The rows of a tile of one tensor, V elements at a time, through buffer accesses.  RAGGED rows (whose length
 // is no multiple of V) differ in two ways.  They start at any multiple of the element's size: where that may be
 // no multiple of 4 bytes (`odd`), a load takes the aligned words around the V elements and shifts them, a store
-// goes to the unaligned address as a plain access.  And the last block of channels holds the rows' ends
-// (`ends`): it goes element by element, `count` of V.
+// goes to the unaligned address as a plain access.  And in the last block of channels (`ends`) one lane of a row
+// has fewer than V elements, `tail`: it takes them in pieces of 8, 4, 2 and 1 bytes by plain accesses.
 template <typename T, int V, int R, bool RAGGED>
 struct Rows {
   typedef Pack<T, V> P;
   typedef typename P::Raw Raw;
-  typedef typename Bytes<sizeof(T)>::type Word;
-  static constexpr int kWords = sizeof(Raw) / 4;
-  struct __attribute__((packed, aligned(sizeof(T)))) Loose { T e[V]; };
-  struct Elements { Word e[V]; };
+  static constexpr int S = sizeof(T), kBytes = S * V, kWords = kBytes / 4;
+  struct __attribute__((packed, aligned(S))) Loose { Raw v; };
+  template <typename W>
+  struct __attribute__((packed, aligned(S))) Piece { W v; };
   struct Words { uint32_t w[kWords]; };
   Rsrc rsrc;
   char* base;
   uint32_t bytes, shift;   // shift: of the first row's address from a multiple of 4
+  int tail;
   bool odd, ends;
-  __device__ __forceinline__ Rows(const T* p, uint32_t n, uint32_t width, bool last)
-      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), odd(false), ends(RAGGED && last) {
-    if constexpr (RAGGED && sizeof(T) < 4) {
-      odd = width % 4 != 0;
+  __device__ __forceinline__ Rows(const T* p, uint32_t n, int32_t channels, bool last)
+      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false) {
+    if constexpr (RAGGED) {
+      odd = channels * S % 4 != 0;
       shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
+      tail = channels % V;
+      ends = last;
     }
     rsrc = make_rsrc(p, n);
   }
-  // off(i): byte offset of the i-th of R packs, out of range where there is none
+  // f(piece of W, its byte offset among the tail's elements) for every piece of the tail
+  template <typename F>
+  __device__ __forceinline__ void pieces(F f) const {
+    int at = 0;
+    if constexpr (kBytes > 8)
+      if (tail * S & 8) f(uint64_t{}, at), at += 8;
+    if constexpr (kBytes > 4 && S <= 4)
+      if (tail * S & 4) f(uint32_t{}, at), at += 4;
+    if constexpr (S <= 2)
+      if (tail * S & 2) f(u16{}, at), at += 2;
+    if constexpr (S == 1)
+      if (tail & 1) f(uint8_t{}, at);
+  }
+  // off(i): byte offset of the i-th of R packs, out of range where there is none; count: the lane's elements
   template <typename F>
   __device__ __forceinline__ void load(P (&v)[R], F off, int count) const {
-    if (RAGGED && ends) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        Elements e;
-#pragma unroll
-        for (int k = 0; k < V; ++k) load_bytes(rsrc, k < count ? off(i) + k * uint32_t(sizeof(T)) : kOutOfRange, e.e[k]);
-        v[i].raw = __builtin_bit_cast(Raw, e);
-      }
-    } else if (RAGGED && odd) {
-      // the word behind the V elements is only ever used for its first bytes, which are elements of the same row
-      // (this is not the row's last block); it may lie past the tile, so the range is one word wider
+    const auto at = [&](int i) { return RAGGED && count < V ? kOutOfRange : off(i); };
+    if (RAGGED && odd) {
+      // Every word read holds at least one byte of the row: V elements have another one of the row behind them
+      // (its tail), so the word behind starts inside the row.  It may end past the tile: the range is a word wider.
       const Rsrc wide = make_rsrc(base - shift, bytes + shift + 4u);
       Words w[R];
       uint32_t behind[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const uint32_t at = off(i) < bytes ? (off(i) + shift) & ~3u : kOutOfRange;
+        const uint32_t word = at(i) < bytes ? (at(i) + shift) & ~3u : kOutOfRange;
         Raw raw;
-        load_bytes(wide, at, raw);
+        load_bytes(wide, word, raw);
         w[i] = __builtin_bit_cast(Words, raw);
-        load_bytes(wide, at + 4u * kWords, behind[i]);
+        load_bytes(wide, word + uint32_t(kBytes), behind[i]);
       }
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const uint32_t by = 8u * ((off(i) + shift) & 3u);
+        const uint32_t by = 8u * ((at(i) + shift) & 3u);
         Words x;
 #pragma unroll
         for (int k = 0; k < kWords; ++k)
@@ -165,18 +172,54 @@ struct Rows {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_bytes(rsrc, off(i), v[i].raw);
+      for (int i = 0; i < R; ++i) load_bytes(rsrc, at(i), v[i].raw);
+    }
+    if (RAGGED && ends) {
+      if (count > 0 && count < V) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          Words x = {};
+          if (off(i) < bytes) {
+            pieces([&](auto piece, int o) {
+              typedef decltype(piece) W;
+              const W got = reinterpret_cast<const Piece<W>*>(base + off(i) + o)->v;
+              if constexpr (sizeof(W) == 8) {
+                x.w[0] = uint32_t(got);
+                x.w[1] = uint32_t(got >> 32);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                  if (o / 4 == k) x.w[k] |= uint32_t(got) << (8 * (o % 4));
+              }
+            });
+          }
+          v[i].raw = __builtin_bit_cast(Raw, x);
+        }
+      }
     }
   }
   __device__ __forceinline__ void store(uint32_t off, int count, P v) const {
-    if (RAGGED && ends) {
-      const Elements e = __builtin_bit_cast(Elements, v.raw);
-#pragma unroll
-      for (int k = 0; k < V; ++k) store_bytes(rsrc, k < count ? off + k * uint32_t(sizeof(T)) : kOutOfRange, e.e[k]);
-    } else if (RAGGED && odd) {
-      if (off < bytes) *reinterpret_cast<Loose*>(base + off) = __builtin_bit_cast(Loose, v.raw);
+    if (RAGGED && odd) {
+      if (off < bytes && count >= V) reinterpret_cast<Loose*>(base + off)->v = v.raw;
     } else {
-      store_bytes(rsrc, off, v.raw);
+      store_bytes(rsrc, RAGGED && count < V ? kOutOfRange : off, v.raw);
+    }
+    if (RAGGED && ends) {
+      if (count > 0 && count < V && off < bytes) {
+        const Words x = __builtin_bit_cast(Words, v.raw);
+        pieces([&](auto piece, int o) {
+          typedef decltype(piece) W;
+          uint64_t word = 0;
+          if constexpr (sizeof(W) == 8) {
+            word = uint64_t(x.w[0]) | uint64_t(x.w[1]) << 32;
+          } else {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k)
+              if (o / 4 == k) word = x.w[k] >> (8 * (o % 4));
+          }
+          reinterpret_cast<Piece<W>*>(base + off + o)->v = W(word);
+        });
+      }
     }
   }
 };
@@ -274,6 +317,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   const uint32_t width = uint32_t(g.channels) * uint32_t(sizeof(T)), crow = uint32_t(g.channels);
   const uint32_t srow = 4u * uint32_t(p.chans);
   const int run = (wave * kRuns + group) * R;   // scan position of the run's first token
+  const bool busy = wave * kRuns * R < nrows;   // a wave without rows holds the identity and stores nothing
   // byte offset of token i of the run in rows of `w` bytes, `at` into the row; past the tile's rows it is out of
   // range (below row 0 it wraps to above 2^31), and so it is for a lane past the channels
   const auto offset = [&](int i, uint32_t w, uint32_t at) {
@@ -283,11 +327,11 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   const auto at_c = [&](int i) { return offset(i, crow, uint32_t(c)); };
   const auto at_s = [&](int i) { return offset(i, srow, 4u * uint32_t(blk)); };
   const auto rows_of = [&](const void* x) {
-    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, width, ends);
+    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, g.channels, ends);
   };
 
   P pg[R], ps[R];
-  {
+  if (busy) {
     const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
     rg.load(pg, at_t, count);
     rs.load(ps, at_t, count);
@@ -298,17 +342,20 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   P ph[R], pu[R];
   Pack<int8_t, V> pc[R];
   float sc[R];
-  if constexpr (MODE == kBackward) {
-    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, width, ends);
+  if (!busy) {
+  } else if constexpr (MODE == kBackward) {
+    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, g.channels, ends);
     rh.load(ph, [&](int i) { return i == first_at ? kOutOfRange : at_t(i); }, count);
   } else if constexpr (MODE == kBackwardSaved) {
-    const Rc rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, crow, ends);
+    const Rc rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, g.channels, ends);
     rc.load(pc, [&](int i) { return i == first_at ? kOutOfRange : at_c(i); }, count);
     const Rsrc rs = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
 #pragma unroll
     for (int i = 0; i < R; ++i) sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : at_s(i));
   }
-  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) rows_of(g.u).load(pu, at_t, count);
+  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) {
+    if (busy) rows_of(g.u).load(pu, at_t, count);
+  }
 
   // a token's a, what it adds (backward: dh) and what multiplies its input.  A row past the tile has gate and
   // input 0: the identity for a log gate, made the identity for a logit here.
@@ -320,28 +367,31 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   float A[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
+  if (busy) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, b, m;
-      token(i, v, a, b, m);
-      A[v] *= a;
-      H[v] = kBack ? a * (b + H[v]) : fmaf(a, H[v], b);
+      for (int v = 0; v < V; ++v) {
+        float a, b, m;
+        token(i, v, a, b, m);
+        A[v] *= a;
+        H[v] = kBack ? a * (b + H[v]) : fmaf(a, H[v], b);
+      }
     }
-  }
+    if constexpr (forms_again(sizeof(T), KIND, kBack)) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) opaque(pg[i].raw), opaque(ps[i].raw);
-
-  // inclusive scan of the runs' maps within the wave, then each run's exclusive map
+      for (int i = 0; i < R; ++i) opaque(pg[i].raw), opaque(ps[i].raw);
+    }
+    // inclusive scan of the runs' maps within the wave
 #pragma unroll
-  for (int o = 1; o < kRuns; o <<= 1) {
+    for (int o = 1; o < kRuns; o <<= 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float pA = __shfl_up(A[v], o * LPR, 64), pH = __shfl_up(H[v], o * LPR, 64);
-      if (group >= o) {
-        H[v] = fmaf(A[v], pH, H[v]);
-        A[v] *= pA;
+      for (int v = 0; v < V; ++v) {
+        const float pA = __shfl_up(A[v], o * LPR, 64), pH = __shfl_up(H[v], o * LPR, 64);
+        if (group >= o) {
+          H[v] = fmaf(A[v], pH, H[v]);
+          A[v] *= pA;
+        }
       }
     }
   }
@@ -349,6 +399,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) sA[wave][col + v] = A[v], sH[wave][col + v] = H[v];
   }
+  // each run's exclusive map
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float pA = __shfl_up(A[v], LPR, 64), pH = __shfl_up(H[v], LPR, 64);
@@ -403,6 +454,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     if (last && out && some) out[at] = t.len ? end : x;
   }
   __syncthreads();
+  if (!busy) return;
 
   // the state entering each run: the tile's, then the waves before, then the runs before
   float x[V];
@@ -429,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
       rh.store(at_t(i), count, out);
       if constexpr (MODE == kForwardSave) {
         const float scale = checkpoint_scale(row_umax<LPR>(largest<T, V>(out, RAGGED ? count : in ? V : 0)));
-        const Rc rc(g.codes + start, uint32_t(nrows) * crow, crow, ends);
+        const Rc rc(g.codes + start, uint32_t(nrows) * crow, g.channels, ends);
         const Rsrc rs = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
         rc.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
         store_bytes(rs, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
