@@ -102,33 +102,36 @@ __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) { __bui
 __device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, 0); }
 
 // The rows of a tile of one tensor, V elements at a time, through buffer accesses.  RAGGED rows (whose length
-// is no multiple of V) differ in two ways.  They start at any multiple of the element's size: where that may be
-// no multiple of 4 bytes (`odd`), a load takes the aligned words around the V elements and shifts them, a store
-// goes to the unaligned address as a plain access.  And in the last block of channels (`ends`) one lane of a row
-// has fewer than V elements, `tail`: it takes them in pieces of 8, 4, 2 and 1 bytes by plain accesses.
+// is no multiple of V) start at any multiple of the element's size, and in the last block of channels (`ends`) one
+// lane of a row has fewer than V elements, `tail`.  A load takes the aligned words that hold the elements (one
+// more than they fill) and shifts them when all tensors' loads are under way; where rows end, word by
+// word.  A store goes to the unaligned address as a plain access, that of a tail in pieces of 8, 4, 2 and 1 bytes.
 template <typename T, int V, int R, bool RAGGED>
 struct Rows {
   typedef Pack<T, V> P;
   typedef typename P::Raw Raw;
   static constexpr int S = sizeof(T), kBytes = S * V, kWords = kBytes / 4;
+  static constexpr bool kShifted = RAGGED && S < 4;   // rows of 4-byte elements start at whole words
   struct __attribute__((packed, aligned(S))) Loose { Raw v; };
   template <typename W>
   struct __attribute__((packed, aligned(S))) Piece { W v; };
   struct Words { uint32_t w[kWords]; };
+  struct Staged { Words x; uint32_t behind; };
   Rsrc rsrc;
   char* base;
-  uint32_t bytes, shift;   // shift: of the first row's address from a multiple of 4
+  uint32_t bytes, shift;   // shift: of the first row's address from a whole word
   int tail;
   bool odd, ends;
   __device__ __forceinline__ Rows(const T* p, uint32_t n, int32_t channels, bool last)
       : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false) {
     if constexpr (RAGGED) {
       odd = channels * S % 4 != 0;
-      shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
+      if constexpr (kShifted) shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
       tail = channels % V;
       ends = last;
     }
-    rsrc = make_rsrc(p, n);
+    // the last row's last word may end past the row
+    rsrc = make_rsrc(base - shift, kShifted && n ? n + shift + 3u : n);
   }
   // f(piece of W, its byte offset among the tail's elements) for every piece of the tail
   template <typename F>
@@ -145,64 +148,54 @@ struct Rows {
   }
   // off(i): byte offset of the i-th of R packs, out of range where there is none; count: the lane's elements
   template <typename F>
-  __device__ __forceinline__ void load(P (&v)[R], F off, int count) const {
-    const auto at = [&](int i) { return RAGGED && count < V ? kOutOfRange : off(i); };
-    if (RAGGED && odd) {
-      // Every word read holds at least one byte of the row: V elements have another one of the row behind them
-      // (its tail), so the word behind starts inside the row.  It may end past the tile: the range is a word wider.
-      const Rsrc wide = make_rsrc(base - shift, bytes + shift + 4u);
-      Words w[R];
-      uint32_t behind[R];
+  __device__ __forceinline__ void stage(Staged (&v)[R], F off, int count) const {
+    // Every word read holds at least one byte of the row: V elements have another one of the row behind them (its
+    // tail), and at a row's end no word is read that starts past it.
+    const auto word = [&](int i) { return off(i) < bytes ? (off(i) + shift) & ~3u : kOutOfRange; };
+    if (RAGGED && ends) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const uint32_t word = at(i) < bytes ? (at(i) + shift) & ~3u : kOutOfRange;
-        Raw raw;
-        load_bytes(wide, word, raw);
-        w[i] = __builtin_bit_cast(Words, raw);
-        load_bytes(wide, word + uint32_t(kBytes), behind[i]);
-      }
+        const uint32_t end = off(i) + shift + uint32_t(max(min(count, V), 0) * S);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const uint32_t by = 8u * ((at(i) + shift) & 3u);
-        Words x;
-#pragma unroll
-        for (int k = 0; k < kWords; ++k)
-          x.w[k] = __builtin_amdgcn_alignbit(k + 1 < kWords ? w[i].w[k + 1] : behind[i], w[i].w[k], by);
-        v[i].raw = __builtin_bit_cast(Raw, x);
+        for (int k = 0; k <= kWords; ++k) {
+          const uint32_t at = word(i) + 4u * uint32_t(k);
+          uint32_t got = 0;
+          if (k < kWords || kShifted) load_bytes(rsrc, at < end ? at : kOutOfRange, got);
+          if (k < kWords) v[i].x.w[k] = got;
+          else v[i].behind = got;
+        }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_bytes(rsrc, at(i), v[i].raw);
-    }
-    if (RAGGED && ends) {
-      if (count > 0 && count < V) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          Words x = {};
-          if (off(i) < bytes) {
-            pieces([&](auto piece, int o) {
-              typedef decltype(piece) W;
-              const W got = reinterpret_cast<const Piece<W>*>(base + off(i) + o)->v;
-              if constexpr (sizeof(W) == 8) {
-                x.w[0] = uint32_t(got);
-                x.w[1] = uint32_t(got >> 32);
-              } else {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k)
-                  if (o / 4 == k) x.w[k] |= uint32_t(got) << (8 * (o % 4));
-              }
-            });
-          }
-          v[i].raw = __builtin_bit_cast(Raw, x);
-        }
+      for (int i = 0; i < R; ++i) {
+        Raw raw;
+        load_bytes(rsrc, RAGGED ? word(i) : off(i), raw);
+        v[i].x = __builtin_bit_cast(Words, raw);
+        v[i].behind = 0;
+        if constexpr (kShifted) load_bytes(rsrc, word(i) + uint32_t(kBytes), v[i].behind);
       }
     }
   }
+  template <typename F>
+  __device__ __forceinline__ void finish(P (&v)[R], const Staged (&from)[R], F off) const {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      Words x = from[i].x;
+      if constexpr (kShifted) {
+        const uint32_t by = 8u * ((off(i) + shift) & 3u);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          x.w[k] = __builtin_amdgcn_alignbit(k + 1 < kWords ? from[i].x.w[k + 1] : from[i].behind, from[i].x.w[k], by);
+      }
+      v[i].raw = __builtin_bit_cast(Raw, x);
+    }
+  }
   __device__ __forceinline__ void store(uint32_t off, int count, P v) const {
+    // (where rows are whole words, a buffer access would do; one that is unaligned is left to the compiler)
     if (RAGGED && odd) {
       if (off < bytes && count >= V) reinterpret_cast<Loose*>(base + off)->v = v.raw;
     } else {
-      store_bytes(rsrc, RAGGED && count < V ? kOutOfRange : off, v.raw);
+      store_bytes(RAGGED ? make_rsrc(base, bytes) : rsrc, RAGGED && count < V ? kOutOfRange : off, v.raw);
     }
     if (RAGGED && ends) {
       if (count > 0 && count < V && off < bytes) {
@@ -330,31 +323,41 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, g.channels, ends);
   };
 
-  P pg[R], ps[R];
+  const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
+  typename Rw::Staged vg[R], vs[R], vh[R], vu[R];
+  typename Rc::Staged vc[R];
   if (busy) {
-    const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
-    rg.load(pg, at_t, count);
-    rs.load(ps, at_t, count);
+    rg.stage(vg, at_t, count);
+    rs.stage(vs, at_t, count);
   }
   // The states that the tokens start from are those of the row before; the sequence's first token starts from
   // h0, and its row is out of range.
   const int first_at = kBack && row0 == t.first ? nrows - 1 - run : -1;   // that token's place in the run
-  P ph[R], pu[R];
-  Pack<int8_t, V> pc[R];
+  const auto at_h = [&](int i) { return i == first_at ? kOutOfRange : at_t(i); };
+  const auto at_hc = [&](int i) { return i == first_at ? kOutOfRange : at_c(i); };
+  const T* const hbase = MODE == kBackward ? static_cast<const T*>(g.h) + (start - g.channels) : nullptr;
+  const int8_t* const cbase = MODE == kBackwardSaved ? g.codes + (start - g.channels) : nullptr;
+  const Rw rh(hbase, uint32_t(nrows) * width, g.channels, ends), ru = rows_of(g.u);
+  const Rc rc(cbase, uint32_t(nrows) * crow, g.channels, ends);
   float sc[R];
-  if (!busy) {
-  } else if constexpr (MODE == kBackward) {
-    const Rw rh(static_cast<const T*>(g.h) + (start - g.channels), uint32_t(nrows) * width, g.channels, ends);
-    rh.load(ph, [&](int i) { return i == first_at ? kOutOfRange : at_t(i); }, count);
-  } else if constexpr (MODE == kBackwardSaved) {
-    const Rc rc(g.codes + (start - g.channels), uint32_t(nrows) * crow, g.channels, ends);
-    rc.load(pc, [&](int i) { return i == first_at ? kOutOfRange : at_c(i); }, count);
-    const Rsrc rs = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
+  if (busy) {
+    if constexpr (MODE == kBackward) rh.stage(vh, at_h, count);
+    if constexpr (MODE == kBackwardSaved) {
+      rc.stage(vc, at_hc, count);
+      const Rsrc rscale = make_rsrc(g.scale + (row0 - 1) * p.chans, uint32_t(nrows) * srow);
 #pragma unroll
-    for (int i = 0; i < R; ++i) sc[i] = buf_loadf(rs, i == first_at ? kOutOfRange : at_s(i));
+      for (int i = 0; i < R; ++i) sc[i] = buf_loadf(rscale, i == first_at ? kOutOfRange : at_s(i));
+    }
+    if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) ru.stage(vu, at_t, count);
   }
-  if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) {
-    if (busy) rows_of(g.u).load(pu, at_t, count);
+  P pg[R], ps[R], ph[R], pu[R];
+  Pack<int8_t, V> pc[R];
+  if (busy) {
+    rg.finish(pg, vg, at_t);
+    rs.finish(ps, vs, at_t);
+    if constexpr (MODE == kBackward) rh.finish(ph, vh, at_h);
+    if constexpr (MODE == kBackwardSaved) rc.finish(pc, vc, at_hc);
+    if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) ru.finish(pu, vu, at_t);
   }
 
   // a token's a, what it adds (backward: dh) and what multiplies its input.  A row past the tile has gate and
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   for (int v = 0; v < V; ++v) x[v] = fmaf(A[v], x[v], H[v]);
 
   if constexpr (!kBack) {
-    const Rw rh = rows_of(g.h);
+    const Rw out_rows = rows_of(g.h);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
@@ -478,13 +481,13 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
         x[v] = fmaf(a, x[v], b);
       }
       const P out = to_pack<T, V>(x);
-      rh.store(at_t(i), count, out);
+      out_rows.store(at_t(i), count, out);
       if constexpr (MODE == kForwardSave) {
         const float scale = checkpoint_scale(row_umax<LPR>(largest<T, V>(out, RAGGED ? count : in ? V : 0)));
-        const Rc rc(g.codes + start, uint32_t(nrows) * crow, g.channels, ends);
-        const Rsrc rs = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
-        rc.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
-        store_bytes(rs, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
+        const Rc out_codes(g.codes + start, uint32_t(nrows) * crow, g.channels, ends);
+        const Rsrc out_scale = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
+        out_codes.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
+        store_bytes(out_scale, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
       }
     }
   } else {
