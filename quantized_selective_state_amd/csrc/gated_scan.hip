@@ -360,11 +360,20 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     if constexpr (kBack && KIND == SSDQ_GATE_LOGIT) ru.finish(pu, vu, at_t);
   }
 
-  // a token's a, what it adds (backward: dh) and what multiplies its input.  A row past the tile has gate and
-  // input 0: the identity for a log gate, made the identity for a logit here.
+  // A row past the tile has gate and input 0: the identity for a log gate.  For a logit it is +infinity.
+  if constexpr (KIND == SSDQ_GATE_LOGIT) {
+    if (nrows < ROWS) {
+      float inf[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) inf[v] = __builtin_inff();
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (run + i >= nrows) pg[i] = to_pack<T, V>(inf);
+    }
+  }
+  // a token's a, what it adds (backward: dh) and what multiplies its input
   const auto token = [&](int i, int v, float& a, float& b, float& m) {
     gate_terms<KIND, sizeof(T) == 4>(pg[i][v], a, m);
-    if (KIND == SSDQ_GATE_LOGIT && run + i >= nrows) a = 1.f;
     b = kBack || KIND == SSDQ_GATE_LOG ? ps[i][v] : m * ps[i][v];
   };
   float A[V], H[V];

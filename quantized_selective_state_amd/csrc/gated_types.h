@@ -42,11 +42,13 @@ __device__ __forceinline__ void gate_terms(float g, float& a, float& c) {
     a = exp_f32<EXACT>(g);
     c = 1.f;
   } else {
-    // 1 - a = e a keeps its relative precision where a is near 1; below -80 it is 1 to the last bit
+    // 1 - a = e a keeps its relative precision where a is near 1; below -80 it is 1 to the last bit (and e a might
+    // be infinity times 0)
     const float e = exp_f32<EXACT>(-g), sum = 1.f + e;
-    const float inv = __builtin_amdgcn_rcpf(sum);
-    // one Newton step, within an ulp (a sum that overflows has the inverse 0 already)
-    a = sum < 1e38f ? fmaf(fmaf(-sum, inv, 1.f), inv, inv) : inv;
+    a = __builtin_amdgcn_rcpf(sum);
+    // The hardware reciprocal is within 1.6 of 2^-24 and low by 0.1 of it on average.  For binary32 tensors one
+    // Newton step follows; beside the rounding of 16-bit ones it is not seen (a state of 1000 tokens is 6e-6 low).
+    if constexpr (EXACT) a = sum < 1e38f ? fmaf(fmaf(-sum, a, 1.f), a, a) : a;
     c = g < -80.f ? 1.f : e * a;
   }
 }
