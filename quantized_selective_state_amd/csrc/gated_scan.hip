@@ -26,19 +26,14 @@ constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h w
 constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
 constexpr bool is_back(int mode) { return mode >= kBackward; }
 
-// Tokens of a tile.
-#ifndef ROWSLF
-#define ROWSLF 128
-#endif
-#ifndef AGAINLF
-#define AGAINLF 0
-#endif
-constexpr int tile_rows(int size, int kind, bool back) {
-  return size == 4 ? 128 : kind == SSDQ_GATE_LOGIT ? (back ? 128 : ROWSLF) : 256;
-}
-constexpr bool forms_again(int size, int kind, bool back) {
-  return kind == SSDQ_GATE_LOGIT && !back && size == 2 ? AGAINLF : true;
-}
+// Tokens of a tile.  A thread holds the raw inputs of rows * 64 / 256 elements of each tensor; within the
+// registers of two blocks per CU 256 tokens of 16 bits fit, and for a logit gate, whose second pass would cost as many
+// exponentials and reciprocals again, half of that with a and b kept beside them (forward packed 9001 x 1531 bf16:
+// 31.0 us, 29.8 formed again, 32.9 with 256 tokens; backward 12345 x 2008 fp16: 76 us, 97 with 256).
+constexpr int tile_rows(int size, int kind) { return size == 4 || kind == SSDQ_GATE_LOGIT ? 128 : 256; }
+// Whether the second pass forms a and b from the raw inputs again (the registers that would keep them cost more than
+// the exponentials of a log gate: four blocks per CU instead of two, 51 -> 46 us at 8192 x 4096 bf16).
+constexpr bool forms_again(int size, int kind, bool back) { return size == 4 || kind == SSDQ_GATE_LOG || back; }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
 // Tiles of a sequence are joined in groups: a tile reads the maps of the tiles of its group before
@@ -240,10 +235,20 @@ __device__ __forceinline__ void sequence_rows(const GatedArgs& g, int s, int32_t
 // Makes the second pass form a and b from the raw inputs again instead of keeping them from the first.
 __device__ __forceinline__ void opaque(v4u& v) { asm volatile("" : "+v"(v)); }
 
+// What the waves of a block exchange.
+struct Shared {
+  float A[kWaves][kBlock], H[kWaves][kBlock];   // the waves' maps
+  float in[kBlock];                             // the state entering the tile
+  int32_t ticket;
+};
+
+// One tile.  carry: where a block walks its sequence, the state after the tile before, and then after this one (a lane
+// of the first wave per channel).
 template <typename T, int KIND, int MODE, bool RAGGED>
-__global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
+__device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, const Tile& t, int32_t blk, Shared& sh,
+                                         float& carry) {
   constexpr bool kBack = is_back(MODE);
-  constexpr int ROWS = tile_rows(sizeof(T), KIND, kBack);
+  constexpr int ROWS = tile_rows(sizeof(T), KIND);
   constexpr int V = 16 / int(sizeof(T)); // channels of a thread
   constexpr int LPR = kBlock / V;        // lanes of a row
   constexpr int kRuns = kWave / LPR;     // runs of tokens in a wave
@@ -253,52 +258,9 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   typedef Rows<T, V, R, RAGGED> Rw;
   typedef Rows<int8_t, V, R, RAGGED> Rc;
 
-  __shared__ float sA[kWaves][kBlock], sH[kWaves][kBlock], sIn[kBlock];
-  __shared__ int32_t sTicket;
-
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
-  // blocks then use all channels of its L2.  (With the 8 XCDs' blocks interleaved, each XCD met only the
-  // lines of one residue mod 1 KB: 109 -> 118 us at 16384 x 5120 fp16.)
-  const int32_t blk = xcd_remap(int32_t(blockIdx.x % uint32_t(p.chans)), p.chans);
-  int32_t index = int32_t(blockIdx.x / uint32_t(p.chans));
-  if (p.chained) {
-    // Tiles are taken by tickets, in the order in which blocks start, so that a tile's predecessors (lower
-    // tickets of the same channels) are held by blocks that run already and publish before they wait for anything
-    // but lower tickets: every wait ends.  One counter for all channels would serialize the starts.
-    if (tid == 0)
-      sTicket = int32_t(__hip_atomic_fetch_add(p.tickets + size_t(blk) * (kTicketBytes / sizeof(uint32_t)), 1u,
-                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    __syncthreads();
-    index = __builtin_amdgcn_readfirstlane(sTicket);
-  }
-  Tile t;
-  if (p.per_sequence) {
-    // dense: the first tiles of all sequences, then their second ones, ...
-    t.chunk = index / g.sequences;
-    t.seq = index - t.chunk * g.sequences;
-    t.chunks = p.per_sequence;
-    t.base = t.seq * p.per_sequence;
-    t.len = int32_t(g.tokens / g.sequences);
-    t.first = t.seq * t.len;
-  } else if (p.chained) {
-    t = p.table[index];
-    if (t.seq < 0) return;
-  } else {
-    int32_t last;
-    t.chunk = 0;
-    t.seq = index;
-    t.chunks = 1;
-    t.base = 0;
-    sequence_rows(g, index, t.first, last);
-    t.len = last - t.first;
-  }
-  // (scalar registers for all that follows from the tile, the buffer descriptors among it)
-  t = Tile{__builtin_amdgcn_readfirstlane(t.seq),  __builtin_amdgcn_readfirstlane(t.chunk),
-           __builtin_amdgcn_readfirstlane(t.chunks), __builtin_amdgcn_readfirstlane(t.base),
-           __builtin_amdgcn_readfirstlane(t.first), __builtin_amdgcn_readfirstlane(t.len)};
   const int32_t nrows = min(ROWS, t.len - t.chunk * ROWS);
   // rows of the tile: the scan runs from the first to the last, or from the last to the first
   const int64_t row0 = kBack ? int64_t(t.first) + t.len - t.chunk * ROWS - nrows : int64_t(t.first) + t.chunk * ROWS;
@@ -409,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   }
   if (group == kRuns - 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) sA[wave][col + v] = A[v], sH[wave][col + v] = H[v];
+    for (int v = 0; v < V; ++v) sh.A[wave][col + v] = A[v], sh.H[wave][col + v] = H[v];
   }
   // each run's exclusive map
 #pragma unroll
@@ -428,8 +390,8 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     float tA = 1.f, tH = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      tH = fmaf(sA[w][lane], tH, sH[w][lane]);
-      tA *= sA[w][lane];
+      tH = fmaf(sh.A[w][lane], tH, sh.H[w][lane]);
+      tA *= sh.A[w][lane];
     }
     const float* init = kBack ? g.dh_final : g.h0;
     const bool last = t.chunk == t.chunks - 1, ends_group = t.chunk % kGroup == kGroup - 1;
@@ -438,6 +400,8 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     if (t.chunk == 0) {
       // only this tile reads the initial state (which the final one may overwrite)
       x = some && init ? init[at] : 0.f;
+    } else if (!p.chained) {
+      x = carry;
     } else {
       if (!last && !ends_group) publish(maps + int64_t(t.chunk) * cpad, map_word(tA, tH));
       const int from = max(t.chunk / kGroup * kGroup - 1, 0), n = t.chunk - from;
@@ -459,22 +423,23 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
           if (j0 + j < n) x = fmaf(__uint_as_float(uint32_t(got[j])), x, __uint_as_float(uint32_t(got[j] >> 32)));
       }
     }
-    sIn[lane] = x;
+    sh.in[lane] = x;
     const float end = fmaf(tA, x, tH);
-    if (!last && (t.chunk == 0 || ends_group)) publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
+    carry = end;
+    if (p.chained && !last && (t.chunk == 0 || ends_group)) publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
     float* out = kBack ? g.dh0 : g.h_final;
     if (last && out && some) out[at] = t.len ? end : x;
   }
   __syncthreads();
-  if (!busy) return;
+  if (!busy) return;   // (the block goes on behind the tile)
 
   // the state entering each run: the tile's, then the waves before, then the runs before
   float x[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = sIn[col + v];
+  for (int v = 0; v < V; ++v) x[v] = sh.in[col + v];
   for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = fmaf(sA[w][col + v], x[v], sH[w][col + v]);
+    for (int v = 0; v < V; ++v) x[v] = fmaf(sh.A[w][col + v], x[v], sh.H[w][col + v]);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) x[v] = fmaf(A[v], x[v], H[v]);
@@ -531,6 +496,60 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
       }
       rdg.store(at_t(i), count, to_pack<T, V>(dg));
       rdu.store(at_t(i), count, to_pack<T, V>(du));
+    }
+  }
+}
+
+// WALK: a block walks its sequence of several tiles (an instance of its own: the loop costs registers).
+template <typename T, int KIND, int MODE, bool RAGGED, bool WALK>
+__global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
+  __shared__ Shared sh;
+  // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
+  // blocks then use all channels of its L2.  (With the 8 XCDs' blocks interleaved, each XCD met only the
+  // lines of one residue mod 1 KB: 109 -> 118 us at 16384 x 5120 fp16.)
+  const int32_t blk = xcd_remap(int32_t(blockIdx.x % uint32_t(p.chans)), p.chans);
+  int32_t index = int32_t(blockIdx.x / uint32_t(p.chans));
+  if (p.chained) {
+    // Tiles are taken by tickets, in the order in which blocks start, so that a tile's predecessors (lower
+    // tickets of the same channels) are held by blocks that run already and publish before they wait for anything
+    // but lower tickets: every wait ends.  One counter for all channels would serialize the starts.
+    if (threadIdx.x == 0)
+      sh.ticket = int32_t(__hip_atomic_fetch_add(p.tickets + size_t(blk) * (kTicketBytes / sizeof(uint32_t)), 1u,
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    __syncthreads();
+    index = __builtin_amdgcn_readfirstlane(sh.ticket);
+  }
+  Tile t;
+  if (p.per_sequence) {
+    // dense: the first tiles of all sequences, then their second ones, ...
+    t.chunk = index / g.sequences;
+    t.seq = index - t.chunk * g.sequences;
+    t.chunks = p.per_sequence;
+    t.base = t.seq * p.per_sequence;
+    t.len = int32_t(g.tokens / g.sequences);
+    t.first = t.seq * t.len;
+  } else if (p.chained) {
+    t = p.table[index];
+    if (t.seq < 0) return;
+  } else {
+    int32_t last;
+    t.chunk = 0;
+    t.seq = index;
+    t.chunks = 1;
+    t.base = 0;
+    sequence_rows(g, index, t.first, last);
+    t.len = last - t.first;
+  }
+  // (scalar registers for all that follows from the tile, the buffer descriptors among it)
+  t = Tile{__builtin_amdgcn_readfirstlane(t.seq),  __builtin_amdgcn_readfirstlane(t.chunk),
+           __builtin_amdgcn_readfirstlane(t.chunks), __builtin_amdgcn_readfirstlane(t.base),
+           __builtin_amdgcn_readfirstlane(t.first), __builtin_amdgcn_readfirstlane(t.len)};
+  float carry = 0.f;
+  run_tile<T, KIND, MODE, RAGGED>(g, p, t, blk, sh, carry);
+  if constexpr (WALK) {
+    while (++t.chunk < t.chunks) {
+      __syncthreads();   // every wave has read the maps of the tile before
+      run_tile<T, KIND, MODE, RAGGED>(g, p, t, blk, sh, carry);
     }
   }
 }
@@ -649,24 +668,28 @@ hipError_t dispatch(int32_t dtype, int32_t kind, A... args) {
   }
 }
 
-template <typename T, int KIND, bool RAGGED>
+template <typename T, int KIND, bool RAGGED, bool WALK>
 void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t stream) {
   const dim3 grid(uint32_t(p.tiles) * uint32_t(p.chans)), block(kThreads);
   if (back) {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kBackwardSaved, RAGGED>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, kBackward, RAGGED>), grid, block, 0, stream, g, p);
+    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kBackwardSaved, RAGGED, WALK>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kBackward, RAGGED, WALK>), grid, block, 0, stream, g, p);
   } else {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kForwardSave, RAGGED>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, kForward, RAGGED>), grid, block, 0, stream, g, p);
+    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kForwardSave, RAGGED, WALK>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kForward, RAGGED, WALK>), grid, block, 0, stream, g, p);
   }
 }
 
 template <typename T, int KIND>
 struct Scan {
   static hipError_t run(const GatedArgs* g, bool back, hipStream_t stream) {
-    const int rows = tile_rows(sizeof(T), KIND, back);
+    const int rows = tile_rows(sizeof(T), KIND);
     Plan p = {};
     if (!plan_sizes(g->sequences, g->tokens, g->channels, g->offsets != nullptr, rows, &p)) return hipErrorInvalidValue;
+    // Two tiles: one block for both, and no maps.  (1 x 512 x 4096 bf16: 10.2 us against 7.5 and 5 for clearing the
+    // maps; three tiles would take 15 against 14.)
+    const bool walk = p.per_sequence == 2;
+    if (walk) p.chained = false, p.tiles = g->sequences;
     if (p.chained) {
       char* ws = static_cast<char*>(g->workspace);
       p.tickets = reinterpret_cast<uint32_t*>(ws);
@@ -678,8 +701,14 @@ struct Scan {
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (g->channels % (16 / int(sizeof(T))) == 0) launch_mode<T, KIND, false>(*g, p, back, stream);
-    else launch_mode<T, KIND, true>(*g, p, back, stream);
+    const bool ragged = g->channels % (16 / int(sizeof(T))) != 0;
+    if (walk) {
+      if (ragged) launch_mode<T, KIND, true, true>(*g, p, back, stream);
+      else launch_mode<T, KIND, false, true>(*g, p, back, stream);
+    } else {
+      if (ragged) launch_mode<T, KIND, true, false>(*g, p, back, stream);
+      else launch_mode<T, KIND, false, false>(*g, p, back, stream);
+    }
     return hipGetLastError();
   }
 };
