@@ -10,6 +10,7 @@ libssdq.so is missing, importing this package fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -549,13 +550,29 @@ def _kind(gate_kind: str) -> int:
     return code
 
 
+def _expect(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape, device, optional=False) -> None:
+    """_need, with the checks of a tensor that is as it should be in one expression."""
+    if t is None and optional:
+        return
+    if t is None or not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device
+                         and t.is_contiguous()):
+        _need(t, name, dtype, shape, device, optional)
+
+
+def _at(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
 def _call(function, where: str, device: torch.device, *args) -> None:
     """One library call on the current stream of `device`, with that device current."""
-    if device.index == torch.cuda.current_device():
-        _check(function(*args, _stream(device)), where)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = function(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(function(*args, _stream(device)), where)
+            status = function(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != SSDQ_SUCCESS:
+        raise SSDQError(status, where)
 
 
 def checkpoint_empty(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
@@ -567,9 +584,9 @@ def checkpoint_empty(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
             torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=x.device))
 
 
-def _need_checkpoint(codes, scale, shape, device):
-    _need(codes, "codes", torch.int8, shape, device)
-    _need(scale, "scale", torch.float32, (*shape[:-1], -(-shape[-1] // CHECKPOINT_BLOCK)), device)
+def _expect_checkpoint(codes, scale, shape, device):
+    _expect(codes, "codes", torch.int8, shape, device)
+    _expect(scale, "scale", torch.float32, (*shape[:-1], -(-shape[-1] // CHECKPOINT_BLOCK)), device)
 
 
 def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
@@ -577,12 +594,16 @@ def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | No
     fp32 scale per 64 channels (..., ceil(C/64)) (ssdq_checkpoint_save).  Returns (codes, scale);
     `out` may give the two tensors."""
     dtype = _element_type(x, "x")
-    codes, scale = checkpoint_empty(x) if out is None else out
-    _need(x, "x", x.dtype, None, None)
-    _need_checkpoint(codes, scale, tuple(x.shape), x.device)
-    channels = x.shape[-1]
-    _call(lib.ssdq_checkpoint_save, "ssdq_checkpoint_save", x.device, dtype, _ptr(x), _ptr(codes), _ptr(scale),
-          x.numel() // channels, channels)
+    shape, dev = x.shape, x.device
+    _expect(x, "x", x.dtype, shape, dev)
+    if out is None:
+        codes, scale = checkpoint_empty(x)
+    else:
+        codes, scale = out
+        _expect_checkpoint(codes, scale, shape, dev)
+    channels = shape[-1]
+    _call(lib.ssdq_checkpoint_save, "ssdq_checkpoint_save", dev, dtype, x.data_ptr(), codes.data_ptr(),
+          scale.data_ptr(), x.numel() // channels, channels)
     return codes, scale
 
 
@@ -590,17 +611,19 @@ def checkpoint_load(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype
     """The values codes * scale of an 8-bit checkpoint as a tensor of `dtype` (ssdq_checkpoint_load)."""
     if codes.dim() < 1 or codes.shape[-1] == 0:
         raise ValueError("codes must have a last axis of at least one channel")
-    _need_checkpoint(codes, scale, tuple(codes.shape), None)
+    shape, dev = codes.shape, codes.device
+    _expect_checkpoint(codes, scale, shape, dev)
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    _need(scale, "scale", torch.float32, None, codes.device)
-    _need(out, "out", dtype, tuple(codes.shape), codes.device)
-    channels = codes.shape[-1]
-    _call(lib.ssdq_checkpoint_load, "ssdq_checkpoint_load", codes.device, _element_type(out, "out"), _ptr(codes),
-          _ptr(scale), _ptr(out), codes.numel() // channels, channels)
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _expect(out, "out", dtype, shape, dev)
+    channels = shape[-1]
+    _call(lib.ssdq_checkpoint_load, "ssdq_checkpoint_load", dev, _element_type(out, "out"), codes.data_ptr(),
+          scale.data_ptr(), out.data_ptr(), codes.numel() // channels, channels)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_scan_workspace_size(sequences: int, tokens: int, channels: int, packed: bool = False) -> int:
     """Workspace bytes of gated_scan and gated_scan_backward (0: sizes that they do not take)."""
     return int(lib.ssdq_gated_scan_workspace_size(sequences, tokens, channels, int(packed)))
@@ -622,7 +645,7 @@ def _gated_sizes(gate: torch.Tensor, offsets: torch.Tensor | None) -> tuple[int,
 
 
 def _gated_workspace(workspace, sequences, tokens, channels, packed, device, where):
-    need = lib.ssdq_gated_scan_workspace_size(sequences, tokens, channels, packed)
+    need = gated_scan_workspace_size(sequences, tokens, channels, packed)
     if need == 0:
         raise SSDQError(SSDQ_ERROR_UNSUPPORTED, where)
     if workspace is None:
@@ -641,24 +664,24 @@ def gated_scan(gate: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None = No
     checkpoint: (codes, scale) as of checkpoint_empty(u), which then receive the 8-bit checkpoint
     of h.  h, h_final and workspace may give those tensors."""
     sequences, tokens, channels = _gated_sizes(gate, offsets)
-    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, tuple(gate.shape)
-    _need(gate, "gate", gate.dtype, None, None)
-    _need(u, "u", gate.dtype, shape, dev)
-    _need(h0, "h0", torch.float32, (sequences, channels), dev, optional=True)
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
+    _expect(gate, "gate", gate.dtype, shape, dev)
+    _expect(u, "u", gate.dtype, shape, dev)
+    _expect(h0, "h0", torch.float32, (sequences, channels), dev, optional=True)
     if h is None:
         h = torch.empty_like(gate)
     else:
-        _need(h, "h", gate.dtype, shape, dev)
+        _expect(h, "h", gate.dtype, shape, dev)
     if h_final is not None:
-        _need(h_final, "h_final", torch.float32, (sequences, channels), dev)
+        _expect(h_final, "h_final", torch.float32, (sequences, channels), dev)
     elif want_final_state:
         h_final = torch.empty((sequences, channels), dtype=torch.float32, device=dev)
     codes, scale = (None, None) if checkpoint is None else checkpoint
     if checkpoint is not None:
-        _need_checkpoint(codes, scale, shape, dev)
+        _expect_checkpoint(codes, scale, shape, dev)
     workspace = _gated_workspace(workspace, sequences, tokens, channels, offsets is not None, dev, "ssdq_gated_scan")
-    _call(lib.ssdq_gated_scan, "ssdq_gated_scan", dev, dtype, kind, _ptr(gate), _ptr(u), _ptr(h0), _ptr(offsets),
-          _ptr(h), _ptr(h_final), _ptr(codes), _ptr(scale), sequences, tokens, channels, _ptr(workspace),
+    _call(lib.ssdq_gated_scan, "ssdq_gated_scan", dev, dtype, kind, _at(gate), _at(u), _at(h0), _at(offsets),
+          _at(h), _at(h_final), _at(codes), _at(scale), sequences, tokens, channels, _at(workspace),
           workspace.numel())
     return h, h_final
 
@@ -673,37 +696,37 @@ def gated_scan_backward(gate: torch.Tensor, dh: torch.Tensor, u: torch.Tensor | 
     gate, offsets and h0 are those of the forward call.  dgate, du, dh0 and workspace may give those
     tensors."""
     sequences, tokens, channels = _gated_sizes(gate, offsets)
-    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, tuple(gate.shape)
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
     states = (sequences, channels)
-    _need(gate, "gate", gate.dtype, None, None)
-    _need(dh, "dh", gate.dtype, shape, dev)
-    _need(u, "u", gate.dtype, shape, dev, optional=gate_kind == "log")
+    _expect(gate, "gate", gate.dtype, shape, dev)
+    _expect(dh, "dh", gate.dtype, shape, dev)
+    _expect(u, "u", gate.dtype, shape, dev, optional=gate_kind == "log")
     if (h is None) == (checkpoint is None):
         raise ValueError("give the states of the forward pass as h or as checkpoint, one of them")
     codes, scale = (None, None) if checkpoint is None else checkpoint
     if checkpoint is None:
-        _need(h, "h", gate.dtype, shape, dev)
+        _expect(h, "h", gate.dtype, shape, dev)
     else:
-        _need_checkpoint(codes, scale, shape, dev)
-    _need(h0, "h0", torch.float32, states, dev, optional=True)
-    _need(dh_final, "dh_final", torch.float32, states, dev, optional=True)
+        _expect_checkpoint(codes, scale, shape, dev)
+    _expect(h0, "h0", torch.float32, states, dev, optional=True)
+    _expect(dh_final, "dh_final", torch.float32, states, dev, optional=True)
     if dgate is None:
         dgate = torch.empty_like(gate)
     else:
-        _need(dgate, "dgate", gate.dtype, shape, dev)
+        _expect(dgate, "dgate", gate.dtype, shape, dev)
     if du is None:
         du = torch.empty_like(gate)
     else:
-        _need(du, "du", gate.dtype, shape, dev)
+        _expect(du, "du", gate.dtype, shape, dev)
     if dh0 is None:
         dh0 = torch.empty(states, dtype=torch.float32, device=dev)
     else:
-        _need(dh0, "dh0", torch.float32, states, dev)
+        _expect(dh0, "dh0", torch.float32, states, dev)
     workspace = _gated_workspace(workspace, sequences, tokens, channels, offsets is not None, dev,
                                  "ssdq_gated_scan_backward")
-    _call(lib.ssdq_gated_scan_backward, "ssdq_gated_scan_backward", dev, dtype, kind, _ptr(gate), _ptr(u), _ptr(h),
-          _ptr(codes), _ptr(scale), _ptr(h0), _ptr(dh), _ptr(dh_final), _ptr(offsets), _ptr(dgate), _ptr(du),
-          _ptr(dh0), sequences, tokens, channels, _ptr(workspace), workspace.numel())
+    _call(lib.ssdq_gated_scan_backward, "ssdq_gated_scan_backward", dev, dtype, kind, _at(gate), _at(u), _at(h),
+          _at(codes), _at(scale), _at(h0), _at(dh), _at(dh_final), _at(offsets), _at(dgate), _at(du),
+          _at(dh0), sequences, tokens, channels, _at(workspace), workspace.numel())
     return dgate, du, dh0
 
 
@@ -713,13 +736,13 @@ def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_ki
     place; gate and u (batch, channels); returns h, the updated state in their type."""
     if state.dim() != 2:
         raise ValueError("state must be (batch, channels)")
-    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), state.device, tuple(state.shape)
-    _need(state, "state", torch.float32, None, None)
-    _need(gate, "gate", gate.dtype, shape, dev)
-    _need(u, "u", gate.dtype, shape, dev)
+    dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), state.device, state.shape
+    _expect(state, "state", torch.float32, shape, dev)
+    _expect(gate, "gate", gate.dtype, shape, dev)
+    _expect(u, "u", gate.dtype, shape, dev)
     if h is None:
         h = torch.empty_like(gate)
     else:
-        _need(h, "h", gate.dtype, shape, dev)
-    _call(lib.ssdq_gated_step, "ssdq_gated_step", dev, dtype, kind, _ptr(state), _ptr(gate), _ptr(u), _ptr(h), *shape)
+        _expect(h, "h", gate.dtype, shape, dev)
+    _call(lib.ssdq_gated_step, "ssdq_gated_step", dev, dtype, kind, _at(state), _at(gate), _at(u), _at(h), *shape)
     return h
