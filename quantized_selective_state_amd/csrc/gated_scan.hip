@@ -26,14 +26,12 @@ constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h w
 constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
 constexpr bool is_back(int mode) { return mode >= kBackward; }
 
-// Tokens of a tile.  A thread holds the raw inputs of rows * 64 / 256 elements of each tensor; within the
-// registers of two blocks per CU 256 tokens of 16 bits fit, and for a logit gate, whose second pass would cost as many
-// exponentials and reciprocals again, half of that with a and b kept beside them (forward packed 9001 x 1531 bf16:
-// 31.0 us, 29.8 formed again, 32.9 with 256 tokens; backward 12345 x 2008 fp16: 76 us, 97 with 256).
-constexpr int tile_rows(int size, int kind) { return size == 4 || kind == SSDQ_GATE_LOGIT ? 128 : 256; }
-// Whether the second pass forms a and b from the raw inputs again (the registers that would keep them cost more than
-// the exponentials of a log gate: four blocks per CU instead of two, 51 -> 46 us at 8192 x 4096 bf16).
-constexpr bool forms_again(int size, int kind, bool back) { return size == 4 || kind == SSDQ_GATE_LOG || back; }
+// Tokens of a tile.  A thread holds rows * 64 / 256 elements of each tensor, and no more of them than leaves four (a
+// log gate) or three blocks per CU.
+#ifndef RLOGIT
+#define RLOGIT 128
+#endif
+constexpr int tile_rows(int size, int kind) { return size == 4 ? 128 : kind == SSDQ_GATE_LOGIT ? RLOGIT : 256; }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
 // Tiles of a sequence are joined in groups: a tile reads the maps of the tiles of its group before
@@ -232,8 +230,9 @@ __device__ __forceinline__ void sequence_rows(const GatedArgs& g, int s, int32_t
 }
 
 
-// Makes the second pass form a and b from the raw inputs again instead of keeping them from the first.
+// Makes the second pass form a and b again from what is kept, instead of keeping those from the first.
 __device__ __forceinline__ void opaque(v4u& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void opaque(float& v) { asm volatile("" : "+v"(v)); }
 
 // What the waves of a block exchange.
 struct Shared {
@@ -333,10 +332,18 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
         if (run + i >= nrows) pg[i] = to_pack<T, V>(inf);
     }
   }
-  // a token's a, what it adds (backward: dh) and what multiplies its input
-  const auto token = [&](int i, int v, float& a, float& b, float& m) {
-    gate_terms<KIND, sizeof(T) == 4>(pg[i][v], a, m);
-    b = kBack || KIND == SSDQ_GATE_LOG ? ps[i][v] : m * ps[i][v];
+  // A token's a, what it adds (backward: dh) and what multiplies its input; again: in the second pass.  A log
+  // gate's exponential is formed twice, a logit's sigmoids are kept as one number.
+  float pair[R][V];
+  const auto token = [&](int i, int v, bool again, float& a, float& b, float& m) {
+    if constexpr (KIND == SSDQ_GATE_LOG) {
+      gate_terms<KIND, sizeof(T) == 4>(pg[i][v], a, m);
+      b = ps[i][v];
+    } else {
+      if (!again) pair[i][v] = logit_pair<sizeof(T) == 4>(pg[i][v]);
+      split_pair(pair[i][v], a, m);
+      b = kBack ? ps[i][v] : m * ps[i][v];
+    }
   };
   float A[V], H[V];
 #pragma unroll
@@ -347,14 +354,20 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float a, b, m;
-        token(i, v, a, b, m);
+        token(i, v, false, a, b, m);
         A[v] *= a;
         H[v] = kBack ? a * (b + H[v]) : fmaf(a, H[v], b);
       }
     }
-    if constexpr (forms_again(sizeof(T), KIND, kBack)) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) opaque(pg[i].raw), opaque(ps[i].raw);
+    for (int i = 0; i < R; ++i) {
+      if constexpr (KIND == SSDQ_GATE_LOG) {
+        opaque(pg[i].raw);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) opaque(pair[i][v]);
+      }
+      opaque(ps[i].raw);
     }
     // inclusive scan of the runs' maps within the wave
 #pragma unroll
@@ -451,7 +464,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float a, b, m;
-        token(i, v, a, b, m);
+        token(i, v, true, a, b, m);
         x[v] = fmaf(a, x[v], b);
       }
       const P out = to_pack<T, V>(x);
@@ -480,7 +493,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float a, b, m, before;
-        token(i, v, a, b, m);
+        token(i, v, true, a, b, m);
         if constexpr (MODE == kBackward) before = ph[i][v];
         else before = pc[i][v] * sc[i];
         if (i == first_at) before = h0[v];

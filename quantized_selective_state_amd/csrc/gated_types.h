@@ -35,6 +35,24 @@ __device__ __forceinline__ float exp_f32(float x) {
   return fabsf(hi) < 128.f ? fmaf(e, lo * kLn2, e) : e;
 }
 
+// A logit's two sigmoids, a and 1 - a, as one number: the smaller of them (which keeps its relative precision), with
+// the logit's sign.
+template <bool EXACT>
+__device__ __forceinline__ float logit_pair(float g) {
+  const float e = exp_f32<EXACT>(-fabsf(g)), sum = 1.f + e;
+  float inv = __builtin_amdgcn_rcpf(sum);
+  // The hardware reciprocal is within 1.6 of 2^-24 and low by 0.1 of it on average.  For binary32 tensors one Newton
+  // step follows; beside the rounding of 16-bit ones it is not seen (a state of 1000 tokens is 6e-6 low).
+  if constexpr (EXACT) inv = fmaf(fmaf(-sum, inv, 1.f), inv, inv);
+  return copysignf(e * inv, g);
+}
+__device__ __forceinline__ void split_pair(float pair, float& a, float& c) {
+  const float low = fabsf(pair), high = 1.f - low;
+  const bool negative = __float_as_int(pair) < 0;
+  a = negative ? low : high;
+  c = negative ? high : low;
+}
+
 // The gate's a, and what multiplies u in b (1 for a log gate).
 template <int KIND, bool EXACT>
 __device__ __forceinline__ void gate_terms(float g, float& a, float& c) {
@@ -42,14 +60,7 @@ __device__ __forceinline__ void gate_terms(float g, float& a, float& c) {
     a = exp_f32<EXACT>(g);
     c = 1.f;
   } else {
-    // 1 - a = e a keeps its relative precision where a is near 1; below -80 it is 1 to the last bit (and e a might
-    // be infinity times 0)
-    const float e = exp_f32<EXACT>(-g), sum = 1.f + e;
-    a = __builtin_amdgcn_rcpf(sum);
-    // The hardware reciprocal is within 1.6 of 2^-24 and low by 0.1 of it on average.  For binary32 tensors one
-    // Newton step follows; beside the rounding of 16-bit ones it is not seen (a state of 1000 tokens is 6e-6 low).
-    if constexpr (EXACT) a = sum < 1e38f ? fmaf(fmaf(-sum, a, 1.f), a, a) : a;
-    c = g < -80.f ? 1.f : e * a;
+    split_pair(logit_pair<EXACT>(g), a, c);
   }
 }
 
