@@ -62,6 +62,7 @@ struct Plan {
   int32_t chans;        // blocks of 64 channels
   int32_t per_sequence; // dense: tiles of a sequence (0: packed)
   bool chained;         // some sequence may have more than one tile
+  bool load_nt, store_nt;   // non-temporal accesses (choose_streams)
   uint32_t* tickets;
   Tile* table;          // packed and chained: the tiles
   uint64_t* maps;       // (tiles, chans * 64)
@@ -86,13 +87,20 @@ size_t ticket_bytes(const Plan& p) { return round_up(size_t(p.chans) * kTicketBy
 size_t table_bytes(const Plan& p) { return p.per_sequence ? 0 : round_up(size_t(p.tiles) * sizeof(Tile)); }
 size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * sizeof(uint64_t); }
 
-// Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) { v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) { v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0); }
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) { v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v4u v) { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0); }
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) { __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0); }
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, 0); }
+// Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.  NT: non-temporal.
+constexpr int kNt = 2;
+template <bool NT = false>
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) { v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT ? kNt : 0); }
+template <bool NT = false>
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) { v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, NT ? kNt : 0); }
+template <bool NT = false>
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) { v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, NT ? kNt : 0); }
+template <bool NT = false>
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v4u v) { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, NT ? kNt : 0); }
+template <bool NT = false>
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) { __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, NT ? kNt : 0); }
+template <bool NT = false>
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, NT ? kNt : 0); }
 
 // The rows of a tile of one tensor, V elements at a time, through buffer accesses.  RAGGED rows (whose length
 // is no multiple of V) start at any multiple of the element's size, and in the last block of channels (`ends`) one
@@ -114,9 +122,9 @@ struct Rows {
   char* base;
   uint32_t bytes, shift;   // shift: of the first row's address from a whole word
   int tail;
-  bool odd, ends;
-  __device__ __forceinline__ Rows(const T* p, uint32_t n, int32_t channels, bool last)
-      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false) {
+  bool odd, ends, nt;
+  __device__ __forceinline__ Rows(const T* p, uint32_t n, int32_t channels, bool last, bool stream)
+      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false), nt(stream) {
     if constexpr (RAGGED) {
       odd = channels * S % 4 != 0;
       if constexpr (kShifted) shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
@@ -158,6 +166,13 @@ struct Rows {
           else v[i].behind = got;
         }
       }
+    } else if (!RAGGED && nt) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        Raw raw;
+        load_bytes<true>(rsrc, off(i), raw);
+        v[i].x = __builtin_bit_cast(Words, raw);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -187,6 +202,8 @@ struct Rows {
     // (where rows are whole words, a buffer access would do; one that is unaligned is left to the compiler)
     if (RAGGED && odd) {
       if (off < bytes && count >= V) reinterpret_cast<Loose*>(base + off)->v = v.raw;
+    } else if (!RAGGED && nt) {
+      store_bytes<true>(rsrc, off, v.raw);
     } else {
       store_bytes(RAGGED ? make_rsrc(base, bytes) : rsrc, RAGGED && count < V ? kOutOfRange : off, v.raw);
     }
@@ -280,11 +297,11 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   const auto at_t = [&](int i) { return offset(i, width, uint32_t(c) * uint32_t(sizeof(T))); };
   const auto at_c = [&](int i) { return offset(i, crow, uint32_t(c)); };
   const auto at_s = [&](int i) { return offset(i, srow, 4u * uint32_t(blk)); };
-  const auto rows_of = [&](const void* x) {
-    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, g.channels, ends);
+  const auto rows_of = [&](const void* x, bool nt) {
+    return Rw(static_cast<const T*>(x) + start, uint32_t(nrows) * width, g.channels, ends, nt);
   };
 
-  const Rw rg = rows_of(g.gate), rs = rows_of(kBack ? g.dh : g.u);
+  const Rw rg = rows_of(g.gate, p.load_nt), rs = rows_of(kBack ? g.dh : g.u, p.load_nt);
   typename Rw::Staged vg[R], vs[R], vh[R], vu[R];
   typename Rc::Staged vc[R];
   if (busy) {
@@ -298,8 +315,8 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   const auto at_hc = [&](int i) { return i == first_at ? kOutOfRange : at_c(i); };
   const T* const hbase = MODE == kBackward ? static_cast<const T*>(g.h) + (start - g.channels) : nullptr;
   const int8_t* const cbase = MODE == kBackwardSaved ? g.codes + (start - g.channels) : nullptr;
-  const Rw rh(hbase, uint32_t(nrows) * width, g.channels, ends), ru = rows_of(g.u);
-  const Rc rc(cbase, uint32_t(nrows) * crow, g.channels, ends);
+  const Rw rh(hbase, uint32_t(nrows) * width, g.channels, ends, p.load_nt), ru = rows_of(g.u, p.load_nt);
+  const Rc rc(cbase, uint32_t(nrows) * crow, g.channels, ends, false);
   float sc[R];
   if (busy) {
     if constexpr (MODE == kBackward) rh.stage(vh, at_h, count);
@@ -458,7 +475,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   for (int v = 0; v < V; ++v) x[v] = fmaf(A[v], x[v], H[v]);
 
   if constexpr (!kBack) {
-    const Rw out_rows = rows_of(g.h);
+    const Rw out_rows = rows_of(g.h, p.store_nt);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
@@ -471,14 +488,14 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
       out_rows.store(at_t(i), count, out);
       if constexpr (MODE == kForwardSave) {
         const float scale = checkpoint_scale(row_umax<LPR>(largest<T, V>(out, RAGGED ? count : in ? V : 0)));
-        const Rc out_codes(g.codes + start, uint32_t(nrows) * crow, g.channels, ends);
+        const Rc out_codes(g.codes + start, uint32_t(nrows) * crow, g.channels, ends, false);
         const Rsrc out_scale = make_rsrc(g.scale + row0 * p.chans, uint32_t(nrows) * srow);
         out_codes.store(at_c(i), count, Pack<int8_t, V>{codes_of<V>(out, scale)});
         store_bytes(out_scale, col == 0 ? at_s(i) : kOutOfRange, __float_as_uint(scale));
       }
     }
   } else {
-    const Rw rdg = rows_of(g.dgate), rdu = rows_of(g.du);
+    const Rw rdg = rows_of(g.dgate, p.store_nt), rdu = rows_of(g.du, p.store_nt);
     float h0[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h0[v] = 0.f;
@@ -693,6 +710,22 @@ void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t strea
   }
 }
 
+// Non-temporal accesses, for rows of whole 128-byte lines (lines that two blocks share are worth keeping: packed 9001 x
+// 1531 bf16 30 against 38 us).  Loads, once a call touches more than the 256 MiB of the Infinity Cache, since what a
+// call reads is then gone before anything reads it again (forward 16384 x 5120 fp16 106 -> 97 us, backward 8192 x 4096
+// fp32 137 -> 121 us; below, 21 against 26 us); stores, once the outputs alone do (training step 32768 x 8192 bf16
+// forward 422 -> 346 us, backward 499 -> 428; a smaller output stays for what reads it: backward fp32 above 121 against
+// 132 us).  Not in the gradient of a logit gate, which reads four tensors: 298 us plain against 311 for 256 M
+// elements of bf16, 563 against 695 for as many of fp32.
+void choose_streams(const GatedArgs& g, int kind, bool back, int size, Plan* p) {
+  constexpr int64_t kCache = int64_t(256) << 20;
+  const int64_t tensor = g.tokens * g.channels * size, outputs = (back ? 2 : 1) * tensor;
+  const int64_t inputs = 2 * tensor + (!back ? 0 : g.codes ? tensor / size : tensor);
+  const bool lines = int64_t(g.channels) * size % 128 == 0, never = back && kind == SSDQ_GATE_LOGIT;
+  p->load_nt = lines && !never && inputs + outputs > kCache;
+  p->store_nt = lines && !never && outputs > kCache;
+}
+
 template <typename T, int KIND>
 struct Scan {
   static hipError_t run(const GatedArgs* g, bool back, hipStream_t stream) {
@@ -714,6 +747,7 @@ struct Scan {
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
+    choose_streams(*g, KIND, back, sizeof(T), &p);
     const bool ragged = g->channels % (16 / int(sizeof(T))) != 0;
     if (walk) {
       if (ragged) launch_mode<T, KIND, true, true>(*g, p, back, stream);
