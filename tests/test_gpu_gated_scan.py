@@ -404,3 +404,103 @@ def test_captured_training_step_replays(packed):
             assert torch.equal(a, b)
         step(draws[2], ssdq.checkpoint_empty(draws[2].u))      # eager work between the replays
         torch.cuda.synchronize()
+
+
+def test_large_calls_equal_their_parts():
+    """Calls that outgrow the Infinity Cache take non-temporal accesses; sequence by sequence the same call is
+    below that.  Same tiles, same order: the same bits."""
+    ssdq = lib()
+    g = torch.Generator(device=DEV).manual_seed(5)
+    shape = (4, 5000, 8192)
+    make = lambda: torch.randn(shape, generator=g, device=DEV).to(torch.bfloat16)
+    gate, u, dh = -make().abs(), make(), make()
+    h0 = torch.randn(4, 8192, generator=g, device=DEV)
+    buffers = ssdq.checkpoint_empty(u)
+    h, final = ssdq.gated_scan(gate, u, h0, checkpoint=buffers)
+    grads = ssdq.gated_scan_backward(gate, dh, checkpoint=buffers, h0=h0, dh_final=h0)
+    full = ssdq.gated_scan_backward(gate, dh, h=h, h0=h0, dh_final=h0)
+    for s in range(4):
+        one = slice(s, s + 1)
+        h1, final1 = ssdq.gated_scan(gate[one], u[one], h0[one])
+        assert torch.equal(h1, h[one]) and torch.equal(final1, final[one])
+        for whole, states in ((grads, dict(checkpoint=(buffers[0][one], buffers[1][one]))), (full, dict(h=h[one]))):
+            part = ssdq.gated_scan_backward(gate[one], dh[one], h0=h0[one], dh_final=h0[one], **states)
+            assert all(torch.equal(a, b[one]) for a, b in zip(part, whole))
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements in a tensor: the last sequences equal the same ones alone."""
+    ssdq = lib()
+    channels, ends = 8192, [0, 262000, 262300, 262300, 262800]
+    tokens = ends[-1]
+    assert tokens * channels > 2 ** 31
+    period = torch.randn(800, channels, device=DEV).to(torch.bfloat16)
+
+    def fill(scale):
+        t = torch.empty(tokens, channels, dtype=torch.bfloat16, device=DEV)
+        t[:-800] = 0.25 * scale                      # the rows that are compared hold numbers of their own
+        t[-800:] = period * scale
+        return t
+
+    gate, u, dh = fill(-0.5).clamp_(max=0), fill(1.0), fill(0.7)
+    h0 = torch.randn(4, channels, device=DEV)
+    offsets = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    buffers = ssdq.checkpoint_empty(u)
+    h, final = ssdq.gated_scan(gate, u, h0, offsets, checkpoint=buffers)
+    dgate, du, dh0 = ssdq.gated_scan_backward(gate, dh, checkpoint=buffers, h0=h0, dh_final=h0, offsets=offsets)
+    lo = ends[1]
+    part = offsets[1:] - lo
+    cut = lambda t: t[lo:].clone()
+    saved = ssdq.checkpoint_empty(cut(u))
+    h1, final1 = ssdq.gated_scan(cut(gate), cut(u), h0[1:].clone(), part, checkpoint=saved)
+    grads = ssdq.gated_scan_backward(cut(gate), cut(dh), checkpoint=saved, h0=h0[1:].clone(), dh_final=h0[1:].clone(),
+                                     offsets=part)
+    torch.cuda.synchronize()
+    assert torch.equal(h1, h[lo:]) and torch.equal(final1, final[1:]) and torch.equal(final[2], h0[2])
+    assert torch.equal(saved[0], buffers[0][lo:]) and torch.equal(saved[1], buffers[1][lo:])
+    assert torch.equal(grads[0], dgate[lo:]) and torch.equal(grads[1], du[lo:]) and torch.equal(grads[2], dh0[1:])
+    codes, scale = ssdq.checkpoint_save(h)
+    assert torch.equal(codes, buffers[0]) and torch.equal(scale, buffers[1])
+    assert torch.equal(ssdq.checkpoint_load(codes, scale, torch.bfloat16)[lo:],
+                       ssdq.checkpoint_load(codes[lo:].clone(), scale[lo:].clone(), torch.bfloat16))
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, many tiles: neither call sees the other's."""
+    ssdq = lib()
+    draws = [Draw(s, torch.bfloat16, "log", 1, 20000, 512) for s in (1, 2)]
+    want = [ssdq.gated_scan(d.gate, d.u, d.h0) for d in draws]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in draws]
+    for _ in range(3):
+        got = []
+        for d, s in zip(draws, streams):
+            with torch.cuda.stream(s):
+                got.append(ssdq.gated_scan(d.gate, d.u, d.h0))
+        torch.cuda.synchronize()
+        for (h, f), (h1, f1) in zip(want, got):
+            assert torch.equal(h, h1) and torch.equal(f, f1)
+
+
+@pytest.mark.parametrize("sequences,tokens", [(1, 4097), (3, 3 * 640)])
+@pytest.mark.parametrize("channels", [63, 65, 67, 1001])
+def test_ragged_rows_leave_their_neighbours(channels, sequences, tokens):
+    """Rows that no vector divides, written inside a larger buffer: nothing before or behind them changes."""
+    ssdq = lib()
+    for dtype in TYPES.values():
+        d = Draw(channels, dtype, "logit", sequences, tokens, channels)
+        edge, size = 1024, tokens * channels
+        rooms = [torch.full((size + 2 * edge,), 7.0, dtype=dtype, device=DEV) for _ in range(3)]
+        h, dgate, du = (r[edge:edge + size].view(d.shape) for r in rooms)
+        code_room = torch.full((size + 2 * edge,), 77, dtype=torch.int8, device=DEV)
+        buffers = (code_room[edge:edge + size].view(d.shape), ssdq.checkpoint_empty(d.u)[1])
+        ssdq.gated_scan(d.gate, d.u, d.h0, gate_kind="logit", h=h, checkpoint=buffers)
+        ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, checkpoint=buffers, h0=d.h0, gate_kind="logit", dgate=dgate, du=du)
+        torch.cuda.synchronize()
+        for r in rooms:
+            assert bool((r[:edge] == 7.0).all()) and bool((r[edge + size:] == 7.0).all())
+        assert bool((code_room[:edge] == 77).all()) and bool((code_room[edge + size:] == 77).all())
+        codes, scale = ssdq.checkpoint_save(h.contiguous())
+        assert torch.equal(codes, buffers[0]) and torch.equal(scale, buffers[1])
+        want, _, bound, _ = d.reference()
+        close(h, want, bound, dtype, "h")
