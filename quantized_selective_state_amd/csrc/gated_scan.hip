@@ -3,14 +3,21 @@
 //
 // The maps h -> A h + H compose associatively, (A2, H2) o (A1, H1) = (A2 A1, A2 H1 + H2), so a
 // sequence is cut into tiles of 256 (or 128) tokens x 64 channels.  A block of four waves holds one
-// tile in registers, as it was loaded: a thread has 16 bytes (4 or 8 neighbouring channels) of 8
-// consecutive tokens (4 where fewer are in a tile).  It composes its tokens' maps, the maps are scanned
-// over the threads of a wave and the four waves, the tile's map is published, the state entering the
-// tile is joined from the maps of the tiles before it, and each thread runs its tokens once more from its
-// entering state and stores.  Every input is read from memory once and every output written once.
+// tile in registers, as it was loaded: a thread has 16 bytes (8 or 4 neighbouring channels) of 8 or 4
+// consecutive tokens.  It composes its tokens' maps, the maps are scanned over the threads of a wave and
+// the four waves, the tile's map is published, the state entering the tile is joined from the maps of the
+// tiles before it, and each thread runs its tokens once more from its entering state and stores.  Every
+// input is read from memory once and every output written once.
 //
 // The gradient's recurrence k_t = a_t (dh_t + k_{t+1}) is the same scan from a sequence's end with the
 // maps (a_t, a_t dh_t), so both directions share the code below.
+//
+// HBM-bound: under one operation per byte.  A training step of 8 x 4096 x 8192 bf16 (forward with its 8-bit
+// checkpoint, backward from it) runs at 5.5 TB/s, a copy of 1 GiB at 5.1.  What that took, beside the single
+// pass: enough bytes in flight (64 KB per block and four blocks per CU, hence raw inputs in the registers and the
+// gates formed in both passes; persistent blocks with prefetched tiles had half of that and took twice as long),
+// channels mapped to XCDs in runs, and non-temporal accesses for large calls.  Gates from logits cost a reciprocal
+// more per element and are near the vector units' limit as well (35 x 256 x 1536 bf16: 21 us, from logs 17).
 #include <algorithm>
 
 #include "gated_types.h"
@@ -26,12 +33,11 @@ constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h w
 constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
 constexpr bool is_back(int mode) { return mode >= kBackward; }
 
-// Tokens of a tile.  A thread holds rows * 64 / 256 elements of each tensor, and no more of them than leaves four (a
-// log gate) or three blocks per CU.
-#ifndef RLOGIT
-#define RLOGIT 128
-#endif
-constexpr int tile_rows(int size, int kind) { return size == 4 ? 128 : kind == SSDQ_GATE_LOGIT ? RLOGIT : 256; }
+// Tokens of a tile.  A thread holds rows * 64 / 256 elements of each tensor, and no more of them than leaves three or
+// four blocks per CU: 256 tokens of a log gate in 16 bits (forward 8192 x 4096 bf16: 44 us, 47 with 128), 128 of 4
+// bytes (backward 8192 x 4096: 134 us, 138 with 256) and where a logit's sigmoids are kept too (backward 12345 x 2008
+// fp16: 76 us, 97 with 256).
+constexpr int tile_rows(int size, int kind) { return size == 4 || kind == SSDQ_GATE_LOGIT ? 128 : 256; }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
 // Tiles of a sequence are joined in groups: a tile reads the maps of the tiles of its group before
@@ -46,7 +52,7 @@ constexpr int kPeek = 4;   // maps that are read at a time
 // is never all ones: A = NaN is stored with one fixed image.
 constexpr size_t kTicketBytes = 128;
 constexpr uint64_t kNoMap = ~uint64_t(0);
-constexpr int kMostPolls = 1 << 24;   // far beyond any wait; the state would be wrong if it were ever reached
+constexpr int kMostPolls = 1 << 24;   // seconds, far beyond any wait; the state would be NaN if it were ever reached
 
 struct Tile {
   int32_t seq;       // -1: no tile
@@ -90,17 +96,29 @@ size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * si
 // Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.  NT: non-temporal.
 constexpr int kNt = 2;
 template <bool NT = false>
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) { v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v4u& v) {
+  v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT ? kNt : 0);
+}
 template <bool NT = false>
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) { v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, v2u& v) {
+  v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, NT ? kNt : 0);
+}
 template <bool NT = false>
-__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) { v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void load_bytes(Rsrc r, uint32_t off, uint32_t& v) {
+  v = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, NT ? kNt : 0);
+}
 template <bool NT = false>
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v4u v) { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v4u v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, NT ? kNt : 0);
+}
 template <bool NT = false>
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) { __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, v2u v) {
+  __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, NT ? kNt : 0);
+}
 template <bool NT = false>
-__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) { __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, NT ? kNt : 0); }
+__device__ __forceinline__ void store_bytes(Rsrc r, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, NT ? kNt : 0);
+}
 
 // The rows of a tile of one tensor, V elements at a time, through buffer accesses.  RAGGED rows (whose length
 // is no multiple of V) start at any multiple of the element's size, and in the last block of channels (`ends`) one
@@ -124,7 +142,8 @@ struct Rows {
   int tail;
   bool odd, ends, nt;
   __device__ __forceinline__ Rows(const T* p, uint32_t n, int32_t channels, bool last, bool stream)
-      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false), nt(stream) {
+      : base(reinterpret_cast<char*>(const_cast<T*>(p))), bytes(n), shift(0), tail(0), odd(false), ends(false),
+        nt(stream) {
     if constexpr (RAGGED) {
       odd = channels * S % 4 != 0;
       if constexpr (kShifted) shift = uint32_t(reinterpret_cast<uintptr_t>(p)) & 3u;
@@ -456,7 +475,8 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
     sh.in[lane] = x;
     const float end = fmaf(tA, x, tH);
     carry = end;
-    if (p.chained && !last && (t.chunk == 0 || ends_group)) publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
+    if (p.chained && !last && (t.chunk == 0 || ends_group))
+      publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
     float* out = kBack ? g.dh0 : g.h_final;
     if (last && out && some) out[at] = t.len ? end : x;
   }
@@ -536,13 +556,13 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   __shared__ Shared sh;
   // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
   // blocks then use all channels of its L2.  (With the 8 XCDs' blocks interleaved, each XCD met only the
-  // lines of one residue mod 1 KB: 109 -> 118 us at 16384 x 5120 fp16.)
+  // lines of one residue mod 1 KB: 118 us against 109 at 16384 x 5120 fp16.)
   const int32_t blk = xcd_remap(int32_t(blockIdx.x % uint32_t(p.chans)), p.chans);
   int32_t index = int32_t(blockIdx.x / uint32_t(p.chans));
   if (p.chained) {
     // Tiles are taken by tickets, in the order in which blocks start, so that a tile's predecessors (lower
     // tickets of the same channels) are held by blocks that run already and publish before they wait for anything
-    // but lower tickets: every wait ends.  One counter for all channels would serialize the starts.
+    // but lower tickets: every wait ends.  One counter for all channels would serialize the starts (3.4 ns each).
     if (threadIdx.x == 0)
       sh.ticket = int32_t(__hip_atomic_fetch_add(p.tickets + size_t(blk) * (kTicketBytes / sizeof(uint32_t)), 1u,
                                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
@@ -640,7 +660,8 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, i
   for (int64_t k = first; k < words; k += stride) maps[k] = v4u{~0u, ~0u, ~0u, ~0u};
 }
 
-// Elementwise over batch * channels: 4 elements per thread (16 bytes of state), whatever the row length.
+// The step: elementwise over batch * channels, 4 elements per thread (16 bytes of state), whatever the row length.
+// HBM-bound (14 bytes per element of 16 bits): 6.3 us at 256 x 8192 fp16, 4.7 TB/s; the call itself takes 7.8.
 constexpr int kStep = 4;
 template <typename T, int KIND>
 __global__ void __launch_bounds__(256) gated_step_kernel(float* __restrict__ state, const T* __restrict__ gate,
@@ -762,8 +783,8 @@ struct Scan {
 template <typename T, int KIND>
 struct Step {
   static hipError_t run(float* state, const void* gate, const void* u, void* h, int64_t n, hipStream_t stream) {
-    hipLaunchKernelGGL((gated_step_kernel<T, KIND>), dim3(uint32_t(min((n + 256 * kStep - 1) / (256 * kStep), int64_t(1) << 20))),
-                       dim3(256), 0, stream, state,
+    const int64_t blocks = std::min((n + 256 * kStep - 1) / (256 * kStep), int64_t(1) << 20);
+    hipLaunchKernelGGL((gated_step_kernel<T, KIND>), dim3(uint32_t(blocks)), dim3(256), 0, stream, state,
                        static_cast<const T*>(gate), static_cast<const T*>(u), static_cast<T*>(h), n);
     return hipGetLastError();
   }

@@ -523,8 +523,7 @@ ssdq_status ssdq_frontend_step(void* conv_state, const void* xbc, const float* c
 
 namespace {
 
-constexpr int64_t kMostElements = int64_t(1) << 40;   // byte offsets of 4-byte elements stay far inside 64 bits
-constexpr int64_t kMostStates = int64_t(1) << 36;
+constexpr int64_t kMostStates = int64_t(1) << 36;   // elements of a step, blocks of a checkpoint
 
 bool ok_dtype(int32_t d) { return d == SSDQ_DTYPE_F32 || d == SSDQ_DTYPE_F16 || d == SSDQ_DTYPE_BF16; }
 bool ok_gate(int32_t g) { return g == SSDQ_GATE_LOG || g == SSDQ_GATE_LOGIT; }
@@ -533,8 +532,6 @@ ssdq_status check_gated_shape(int32_t sequences, int64_t tokens, int32_t channel
   if (sequences <= 0 || tokens < 0 || channels <= 0) return SSDQ_ERROR_INVALID_VALUE;
   if (!packed && tokens % sequences != 0) return SSDQ_ERROR_INVALID_VALUE;
   if (tokens >= (int64_t(1) << 31) - (int64_t(1) << 16)) return SSDQ_ERROR_UNSUPPORTED;   // rows in 32 bits
-  if (tokens * channels >= kMostElements || int64_t(sequences) * channels >= kMostStates)
-    return SSDQ_ERROR_UNSUPPORTED;
   if (gated_workspace_bytes(sequences, tokens, channels, packed) == 0) return SSDQ_ERROR_UNSUPPORTED;
   return SSDQ_SUCCESS;
 }
