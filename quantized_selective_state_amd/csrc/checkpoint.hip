@@ -13,7 +13,7 @@ namespace {
 constexpr int kBlock = SSDQ_CHECKPOINT_BLOCK;
 constexpr int kThreads = 256;
 constexpr int kItems = 4;
-constexpr int64_t kMostItems = int64_t(1) << 28;   // of one launch: item numbers in 32 bits, threads below 2^32
+constexpr int64_t kMostItems = int64_t(1) << 27;   // of one launch: 16 threads each where rows are ragged, 2^31 in all
 
 // the channels of lane `col` and item number of its k-th item; an item past the end has no channels
 template <int V>
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) checkpoint_load_kernel(const int8_t*
   }
 }
 
-// f(rows of this launch, row offset) over as many launches as the item numbers need: one, but for tensors of
-// more than 2^34 elements
+// f(rows of this launch, row offset) over as many launches as the threads need: one, but for more than 2^27 blocks
+// of 64 channels
 template <typename F>
 hipError_t over_rows(int64_t rows, int32_t blocks, F f) {
   const int64_t most = kMostItems / blocks > 0 ? kMostItems / blocks : 1;

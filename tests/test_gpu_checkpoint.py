@@ -98,3 +98,15 @@ def test_refusals():
             call()
     with pytest.raises(ssdq.SSDQError):
         ssdq.checkpoint_load(torch.zeros(129, dtype=torch.int8, device=DEV)[1:].view(1, 128), scale[:1], torch.half)
+
+
+def test_more_blocks_than_a_launch_holds():
+    """A grid holds fewer than 2^32 threads and a row of one channel takes 16: 2^28 rows are several launches."""
+    ssdq, rows = lib(), 2 ** 28 + 5
+    x = torch.randn(rows, 1, device=DEV, dtype=torch.bfloat16)
+    x[::1000] = 0
+    codes, scale = ssdq.checkpoint_save(x)
+    assert torch.equal(codes, (127 * x.sign()).to(torch.int8))               # a block of one channel: code 127
+    assert torch.equal(scale, x.float().abs() * torch.tensor(1 / 127, device=DEV))
+    back = ssdq.checkpoint_load(codes, scale, torch.bfloat16)
+    assert torch.equal(back, (codes.float() * scale).to(torch.bfloat16))
