@@ -556,7 +556,9 @@ size_t ssdq_gated_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t
  * ceil(channels / 64) * (tokens / 128 + sequences) < 2^24 (else SSDQ_ERROR_UNSUPPORTED); dense
  * tokens must be a multiple of sequences.  With tokens == 0 the (tokens, ...) pointers are not looked at.
  * A NaN or infinity in gate, u or h0 makes the rows after it in its sequence and channel non-finite
- * or NaN (a = 0 does not clear it: 0 times infinity is NaN), and nothing else.  The result does not
+ * or NaN (a = 0 does not clear it: 0 times infinity is NaN), and nothing else.  Products of a over up to
+ * 256 neighbouring tokens of a sequence are formed on the way: where one is past binary32's range (only log
+ * gates above 0 can reach that) h may be infinite or NaN though the recurrence is not.  The result does not
  * depend on timing: calls with the same arguments give the same bits.
  */
 ssdq_status ssdq_gated_scan(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const float* h0,

@@ -504,3 +504,89 @@ def test_ragged_rows_leave_their_neighbours(channels, sequences, tokens):
         assert torch.equal(codes, buffers[0]) and torch.equal(scale, buffers[1])
         want, _, bound, _ = d.reference()
         close(h, want, bound, dtype, "h")
+
+
+def test_states_in_place():
+    """h_final may be h0's tensor and dh0 that of dh_final: one tile, two, and many."""
+    ssdq = lib()
+    offsets = np.array([0, 1, 1, 700, 1500], np.int32)
+    for d in (Draw(s, torch.bfloat16, "log", 4, 4 * n, 72) for s, n in enumerate((5, 400, 5000))):
+        in_place(ssdq, d)
+    in_place(ssdq, Draw(9, torch.float32, "log", 4, 1500, 72, offsets))
+
+
+def in_place(ssdq, d):
+    h, final = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets)
+    dh0 = ssdq.gated_scan_backward(d.gate, d.dh, h=h, h0=d.h0, dh_final=d.dh_final, offsets=d.offsets)[2]
+    state, back = d.h0.clone(), d.dh_final.clone()
+    h2, final2 = ssdq.gated_scan(d.gate, d.u, state, d.offsets, h_final=state)
+    ssdq.gated_scan_backward(d.gate, d.dh, h=h, h0=d.h0, dh_final=back, offsets=d.offsets, dh0=back)
+    assert final2 is state and torch.equal(state, final) and torch.equal(h2, h) and torch.equal(back, dh0)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_gates_above_one(dtype):
+    """Log gates on both sides of 0 (the state grows by up to e^14), products within the range."""
+    d = Draw(91, TYPES[dtype], "log", 2, 2 * 700, 72)
+    d.gate.copy_(torch.randn_like(d.gate, dtype=torch.float32) * 0.05)
+    d.gate[:, :, ::5] = 0.02
+    if TYPES[dtype] == torch.float16:
+        d.u.mul_(2.0 ** -13)                      # h stays below 65504
+        d.h0.mul_(2.0 ** -13)
+    h = check_forward(d)
+    if TYPES[dtype] != torch.float16:             # (its gradients would not stay below 65504)
+        check_backward(d, h=h)
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different sizes and one eager one take turns on one workspace and one stream."""
+    ssdq = lib()
+    offsets = np.array([0, 3, 900, 2000], np.int32)
+    draws = [Draw(95, torch.bfloat16, "log", 2, 2 * 1500, 200), Draw(96, torch.float16, "logit", 3, 2000, 66, offsets)]
+    size = max(ssdq.gated_scan_workspace_size(d.sequences, d.tokens, d.channels, d.offsets is not None) for d in draws)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    run = lambda d: ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind=d.kind, workspace=ws)[0]
+    want = [run(d).clone() for d in draws]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for d in draws:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(d))
+        graphs.append(g)
+    for turn in range(4):
+        for out in outs:
+            out.zero_()
+        for k in ((0, 1), (1, 0), (0, 0, 1), (1, 1, 0))[turn]:
+            graphs[k].replay()
+        eager = run(draws[turn % 2])
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[turn % 2]) and all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_as_many_tiles_as_a_grid_holds():
+    """Sequences of one token, one fewer of them than is refused: 2^32 threads but a block or two."""
+    ssdq, n = lib(), 2 ** 24 - 2
+    gate, u, h0 = -torch.rand(n, 1, 1, device=DEV), torch.randn(n, 1, 1, device=DEV), torch.randn(n, 1, device=DEV)
+    h, final = ssdq.gated_scan(gate, u, h0)
+    a = gate.double().exp().view(n, 1)
+    want = a * h0.double() + u.double().view(n, 1)
+    # exp within 3, the products and sums within 24 half steps of the terms' magnitudes
+    bound = 2.0 ** -24 * 32 * (a * h0.double().abs() + u.double().abs().view(n, 1))
+    assert bool(((final.double() - want).abs() <= bound).all()) and torch.equal(h.view(n, 1), final)
+    with pytest.raises(ssdq.SSDQError):
+        ssdq.gated_scan(torch.zeros(2 ** 24, 1, 1, device=DEV), torch.zeros(2 ** 24, 1, 1, device=DEV))
+
+
+def test_step_of_more_elements_than_32_bits_count():
+    ssdq, rows, channels = lib(), 32769, 65537                     # rows * channels > 2^31, and odd
+    gate = torch.randn(rows, channels, device=DEV, dtype=torch.float16)
+    u = torch.randn(rows, channels, device=DEV, dtype=torch.float16)
+    state = torch.randn(rows, channels, device=DEV)
+    before = state.clone()
+    h = ssdq.gated_step(state, gate, u, gate_kind="logit")
+    for lo in range(0, rows, 8192):
+        part = slice(lo, min(lo + 8192, rows))
+        s = before[part].clone()
+        got = ssdq.gated_step(s, gate[part].clone(), u[part].clone(), gate_kind="logit")
+        assert torch.equal(got, h[part]) and torch.equal(s, state[part]), lo
