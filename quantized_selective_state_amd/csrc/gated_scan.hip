@@ -40,22 +40,31 @@ constexpr bool is_back(int mode) { return mode >= kBackward; }
 constexpr int tile_rows(int size, int kind) { return size == 4 || kind == SSDQ_GATE_LOGIT ? 128 : 256; }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
+// What a block does: one tile; or, in instances of their own (for the registers), a sequence of several tiles, or also
+// short sequences.  Neighbouring sequences that fit in a wave (a quarter of a tile's tokens) together, each in runs of
+// tokens of its own, then share it, and a block has four such waves: the same sums in the same order as in a block
+// alone.  (256 sequences of 8 tokens x 4096 bf16: 17 us against 71 with a block each.)
+constexpr int kTile = 0, kWalk = 1, kShort = 2;
+constexpr int runs_of(int size) { return 16 / size; }   // runs of tokens side by side in a wave
+
 // Tiles of a sequence are joined in groups: a tile reads the maps of the tiles of its group before
 // it, and of the group before that only the last tile's, which publishes the state it ended with as
 // the map (0, state) once it knows that; so does a sequence's first tile.  This fixes the order of every
 // product and sum (the same bits on every run) and bounds what a tile reads (16 maps) whatever the length.
 constexpr int kGroup = 16;
 constexpr int kPeek = 4;   // maps that are read at a time
+constexpr int kManyBlocks = 2048;   // twice as many as run at once
 
 // Workspace of chained tiles: a ticket counter per 64 channels, each on a line of its own; for packed sequences
-// the table of tiles; and the tiles' maps (A, H), in words that are all ones until published.  A published word
-// is never all ones: A = NaN is stored with one fixed image.
+// the table of tiles and the list of waves of short sequences; and the tiles' maps (A, H), in words that are all ones
+// until published.  A published word is never all ones: A = NaN is stored with one fixed image.
 constexpr size_t kTicketBytes = 128;
 constexpr uint64_t kNoMap = ~uint64_t(0);
 constexpr int kMostPolls = 1 << 24;   // seconds, far beyond any wait; the state would be NaN if it were ever reached
 
+constexpr int32_t kNoTile = -1, kShared = -2;
 struct Tile {
-  int32_t seq;       // -1: no tile
+  int32_t seq;       // or kNoTile, or kShared: waves of short sequences, number `chunk` and the next three, of `chunks`
   int32_t chunk;     // tiles of the sequence before this one, in scan order
   int32_t chunks;    // tiles of the sequence
   int32_t base;      // number of the sequence's first tile
@@ -67,30 +76,53 @@ struct Plan {
   int32_t tiles;        // most tiles of 64 channels
   int32_t chans;        // blocks of 64 channels
   int32_t per_sequence; // dense: tiles of a sequence (0: packed)
-  bool chained;         // some sequence may have more than one tile
+  bool chained;         // some sequence may have more than one tile, or short ones share blocks by the table
+  bool sharing;         // short sequences share blocks
+  int32_t per_wave;     // one length that fits in a wave: sequences to a wave (else 0)
   bool load_nt, store_nt;   // non-temporal accesses (choose_streams)
   uint32_t* tickets;
   Tile* table;          // packed and chained: the tiles
+  uint32_t* shorts;     // and the waves of short sequences: the first one, and how many (2^k) in the top bits
   uint64_t* maps;       // (tiles, chans * 64)
 };
 
 int64_t tiles_of(int64_t len, int rows) { return len <= rows ? 1 : (len + rows - 1) / rows; }
 
 // Sizes of a call for tiles of `rows` tokens; false where a launch cannot hold them.
-bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed, int rows, Plan* p) {
+bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed, int rows, int runs, Plan* p) {
   if (channels > (1 << 20)) return false;   // a tile's byte offsets stay below 2^31
   p->chans = (channels + kBlock - 1) / kBlock;
   p->per_sequence = packed ? 0 : int32_t(tiles_of(tokens / sequences, rows));
   p->chained = packed ? tokens > rows : p->per_sequence > 1;
-  const int64_t tiles = !packed ? int64_t(p->per_sequence) * sequences
-                        : p->chained ? tokens / rows + sequences : sequences;
+  int64_t tiles = !packed ? int64_t(p->per_sequence) * sequences
+                  : p->chained ? tokens / rows + sequences : sequences;
   if (tiles * p->chans >= (int64_t(1) << 24)) return false;   // a grid holds fewer than 2^32 threads
+  const int64_t fits = rows / kWaves;
+  if (packed) {
+    // The table of tiles is worth its launch where a block per sequence would be more blocks than run at once (60
+    // sequences, 200 tokens x 4096 bf16: 15.4 us against 17.6; 20 sequences: 14.6 against 12.3), and sharing where
+    // sequences are shorter than a tile on average (200 sequences, 8192 tokens x 4096: 55 us against 74; 37
+    // sequences, 9001 tokens x 1531: 33 against 31).
+    p->chained = p->chained || int64_t(sequences) * p->chans > kManyBlocks;
+    p->sharing = p->chained && tokens / rows < sequences;
+    const int64_t most = std::min(int64_t(sequences), tokens / (fits + 1));   // sequences that do not fit in a wave
+    if (p->sharing) tiles = tokens / rows + most + (sequences - most + kWaves - 1) / kWaves;
+    else if (p->chained) tiles = tokens / rows + sequences;
+  } else if (tokens / sequences <= fits) {
+    p->sharing = true;
+    const int64_t len = tokens / sequences, run = fits / runs;
+    p->per_wave = int32_t(runs / std::max(int64_t(1), (len + run - 1) / run));
+    tiles = (int64_t(sequences) + p->per_wave * kWaves - 1) / (p->per_wave * kWaves);
+  }
   p->tiles = int32_t(tiles);
   return true;
 }
 size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
 size_t ticket_bytes(const Plan& p) { return round_up(size_t(p.chans) * kTicketBytes); }
 size_t table_bytes(const Plan& p) { return p.per_sequence ? 0 : round_up(size_t(p.tiles) * sizeof(Tile)); }
+size_t short_bytes(int32_t sequences, const Plan& p) {
+  return p.per_sequence ? 0 : round_up(size_t(sequences) * sizeof(int32_t));
+}
 size_t map_bytes(const Plan& p) { return size_t(p.tiles) * p.chans * kBlock * sizeof(uint64_t); }
 
 // Buffer accesses: out-of-range reads give zeros, out-of-range writes are dropped.  NT: non-temporal.
@@ -278,8 +310,9 @@ struct Shared {
 };
 
 // One tile.  carry: where a block walks its sequence, the state after the tile before, and then after this one (a lane
-// of the first wave per channel).
-template <typename T, int KIND, int MODE, bool RAGGED>
+// of the first wave per channel).  TOGETHER: a wave has whole sequences of its own, t.chunks of them (or none) from t.seq,
+// in the rows t.first and t.len.
+template <typename T, int KIND, int MODE, bool RAGGED, bool TOGETHER>
 __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, const Tile& t, int32_t blk, Shared& sh,
                                          float& carry) {
   constexpr bool kBack = is_back(MODE);
@@ -306,11 +339,39 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   const bool in = c < g.channels, ends = blk == p.chans - 1;
   const uint32_t width = uint32_t(g.channels) * uint32_t(sizeof(T)), crow = uint32_t(g.channels);
   const uint32_t srow = 4u * uint32_t(p.chans);
-  const int run = (wave * kRuns + group) * R;   // scan position of the run's first token
-  const bool busy = wave * kRuns * R < nrows;   // a wave without rows holds the identity and stores nothing
+  const int slot = TOGETHER ? 0 : wave;
+  // the lane's run: its sequence, which of that one's runs in this wave it is, the scan position of its first token, how
+  // many tokens come from there on, and the row of the first one in the tile
+  int32_t seq = t.seq;
+  int rank = group, run = (slot * kRuns + group) * R, left = nrows - run, row = kBack ? left - 1 : run;
+  bool closes = group == min(kRuns - 1, max(nrows - slot * kRuns * R - 1, 0) / R);   // the last with tokens
+  if constexpr (TOGETHER) {
+    int32_t lo = 0, hi = 0;
+    if (lane < t.chunks) {
+      if (p.per_wave) lo = (t.seq + lane) * int32_t(g.tokens / g.sequences), hi = lo + int32_t(g.tokens / g.sequences);
+      else sequence_rows(g, t.seq + lane, lo, hi);
+    }
+    int at = 0, mine = 0, before = 0, of = 0, first = 0, len = 0;   // at: runs given to the sequences so far
+    for (int j = 0; j < t.chunks; ++j) {
+      const int f = __builtin_amdgcn_readlane(lo, j), n = __builtin_amdgcn_readlane(hi, j) - f;
+      const int runs = max(1, (n + R - 1) / R);
+      if (group >= at) mine = j, before = at, of = runs, first = f, len = n;
+      at += runs;
+    }
+    rank = group - before;
+    run = rank * R;
+    // (sequences that overlap or leave the tile's rows, of offsets out of order, are left out)
+    const bool is = t.chunks > 0 && rank < of && first >= t.first && first - t.first <= nrows - len;
+    seq = is ? t.seq + mine : -1;
+    left = is ? len - run : 0;
+    row = first - t.first + (kBack ? left - 1 : run);
+    closes = is && rank == of - 1;
+  }
+  const bool busy = slot * kRuns * R < nrows;   // a wave without rows holds the identity and stores nothing
   // byte offset of token i of the run in rows of `w` bytes, `at` into the row; past the tile's rows it is out of
   // range (below row 0 it wraps to above 2^31), and so it is for a lane past the channels
   const auto offset = [&](int i, uint32_t w, uint32_t at) {
+    if constexpr (TOGETHER) return in && i < left ? uint32_t(kBack ? row - i : row + i) * w + at : kOutOfRange;
     return in ? uint32_t(kBack ? nrows - 1 - run - i : run + i) * w + at : kOutOfRange;
   };
   const auto at_t = [&](int i) { return offset(i, width, uint32_t(c) * uint32_t(sizeof(T))); };
@@ -329,7 +390,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   }
   // The states that the tokens start from are those of the row before; the sequence's first token starts from
   // h0, and its row is out of range.
-  const int first_at = kBack && row0 == t.first ? nrows - 1 - run : -1;   // that token's place in the run
+  const int first_at = kBack && row0 == t.first ? left - 1 : -1;   // that token's place in the run
   const auto at_h = [&](int i) { return i == first_at ? kOutOfRange : at_t(i); };
   const auto at_hc = [&](int i) { return i == first_at ? kOutOfRange : at_c(i); };
   const T* const hbase = MODE == kBackward ? static_cast<const T*>(g.h) + (start - g.channels) : nullptr;
@@ -359,13 +420,13 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 
   // A row past the tile has gate and input 0: the identity for a log gate.  For a logit it is +infinity.
   if constexpr (KIND == SSDQ_GATE_LOGIT) {
-    if (nrows < ROWS) {
+    if (TOGETHER || nrows < ROWS) {
       float inf[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) inf[v] = __builtin_inff();
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (run + i >= nrows) pg[i] = to_pack<T, V>(inf);
+        if (i >= left) pg[i] = to_pack<T, V>(inf);
     }
   }
   // A token's a, what it adds (backward: dh) and what multiplies its input; again: in the second pass.  A log
@@ -411,14 +472,27 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float pA = __shfl_up(A[v], o * LPR, 64), pH = __shfl_up(H[v], o * LPR, 64);
-        if (group >= o) {
+        if (rank >= o) {
           H[v] = fmaf(A[v], pH, H[v]);
           A[v] *= pA;
         }
       }
     }
   }
-  if (group == kRuns - 1) {
+  const float* const init = kBack ? g.dh_final : g.h0;
+  float* const out = kBack ? g.dh0 : g.h_final;
+  float x[V];   // the state that enters the run; together: first that which the sequence starts from
+  if constexpr (TOGETHER) {
+    const int64_t at = int64_t(seq) * g.channels + c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = init && seq >= 0 && v < count ? init[at + v] : 0.f;
+    if (out && closes) {
+      // (the whole wave has read the first states, which these may overwrite)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < count) out[at + v] = run + left ? fmaf(A[v], x[v], H[v]) : x[v];
+    }
+  } else if (closes) {
 #pragma unroll
     for (int v = 0; v < V; ++v) sh.A[wave][col + v] = A[v], sh.H[wave][col + v] = H[v];
   }
@@ -426,12 +500,12 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float pA = __shfl_up(A[v], LPR, 64), pH = __shfl_up(H[v], LPR, 64);
-    A[v] = group ? pA : 1.f;
-    H[v] = group ? pH : 0.f;
+    A[v] = rank ? pA : 1.f;
+    H[v] = rank ? pH : 0.f;
   }
   __syncthreads();
 
-  if (wave == 0) {
+  if (wave == 0 && !TOGETHER) {
     // a lane per channel: the tile's map, and the state entering the tile
     const int64_t cpad = int64_t(p.chans) * kBlock, ch = int64_t(blk) * kBlock + lane;
     const bool some = ch < g.channels;
@@ -442,15 +516,14 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
       tH = fmaf(sh.A[w][lane], tH, sh.H[w][lane]);
       tA *= sh.A[w][lane];
     }
-    const float* init = kBack ? g.dh_final : g.h0;
     const bool last = t.chunk == t.chunks - 1, ends_group = t.chunk % kGroup == kGroup - 1;
     uint64_t* maps = p.maps + int64_t(t.base) * cpad + ch;
-    float x = 0.f;
+    float first_state = 0.f;
     if (t.chunk == 0) {
       // only this tile reads the initial state (which the final one may overwrite)
-      x = some && init ? init[at] : 0.f;
+      first_state = some && init ? init[at] : 0.f;
     } else if (!p.chained) {
-      x = carry;
+      first_state = carry;
     } else {
       if (!last && !ends_group) publish(maps + int64_t(t.chunk) * cpad, map_word(tA, tH));
       const int from = max(t.chunk / kGroup * kGroup - 1, 0), n = t.chunk - from;
@@ -469,25 +542,25 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
         }
 #pragma unroll
         for (int j = 0; j < kPeek; ++j)
-          if (j0 + j < n) x = fmaf(__uint_as_float(uint32_t(got[j])), x, __uint_as_float(uint32_t(got[j] >> 32)));
+          if (j0 + j < n)
+            first_state = fmaf(__uint_as_float(uint32_t(got[j])), first_state, __uint_as_float(uint32_t(got[j] >> 32)));
       }
     }
-    sh.in[lane] = x;
-    const float end = fmaf(tA, x, tH);
-    carry = end;
+    sh.in[lane] = first_state;
+    carry = fmaf(tA, first_state, tH);
     if (p.chained && !last && (t.chunk == 0 || ends_group))
-      publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, end));
-    float* out = kBack ? g.dh0 : g.h_final;
-    if (last && out && some) out[at] = t.len ? end : x;
+      publish(maps + int64_t(t.chunk) * cpad, map_word(0.f, carry));
+    if (last && out && some) out[at] = t.len ? carry : first_state;
   }
   __syncthreads();
+  if constexpr (!TOGETHER) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = sh.in[col + v];
+  }
   if (!busy) return;   // (the block goes on behind the tile)
 
   // the state entering each run: the tile's, then the waves before, then the runs before
-  float x[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = sh.in[col + v];
-  for (int w = 0; w < wave; ++w) {
+  for (int w = 0; w < slot; ++w) {
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = fmaf(sh.A[w][col + v], x[v], sh.H[w][col + v]);
   }
@@ -522,7 +595,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
     if (g.h0 && first_at >= 0 && first_at < R) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (v < count) h0[v] = g.h0[int64_t(t.seq) * g.channels + c + v];
+        if (v < count) h0[v] = g.h0[int64_t(seq) * g.channels + c + v];
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -550,8 +623,7 @@ __device__ __forceinline__ void run_tile(const GatedArgs& g, const Plan& p, cons
   }
 }
 
-// WALK: a block walks its sequence of several tiles (an instance of its own: the loop costs registers).
-template <typename T, int KIND, int MODE, bool RAGGED, bool WALK>
+template <typename T, int KIND, int MODE, bool RAGGED, int WORK>
 __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   __shared__ Shared sh;
   // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
@@ -570,7 +642,16 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     index = __builtin_amdgcn_readfirstlane(sh.ticket);
   }
   Tile t;
-  if (p.per_sequence) {
+  bool together = false;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  if (WORK == kShort && p.per_wave) {
+    const int64_t first = (int64_t(index) * kWaves + wave) * p.per_wave;
+    t = Tile{int32_t(min(first, int64_t(g.sequences))), 0, 0, 0, 0, 0};
+    t.chunks = min(p.per_wave, g.sequences - t.seq);
+    t.first = t.seq * int32_t(g.tokens / g.sequences);
+    t.len = t.chunks * int32_t(g.tokens / g.sequences);
+    together = true;
+  } else if (p.per_sequence) {
     // dense: the first tiles of all sequences, then their second ones, ...
     t.chunk = index / g.sequences;
     t.seq = index - t.chunk * g.sequences;
@@ -578,48 +659,73 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
     t.base = t.seq * p.per_sequence;
     t.len = int32_t(g.tokens / g.sequences);
     t.first = t.seq * t.len;
-  } else if (p.chained) {
-    t = p.table[index];
-    if (t.seq < 0) return;
   } else {
-    int32_t last;
-    t.chunk = 0;
-    t.seq = index;
-    t.chunks = 1;
-    t.base = 0;
-    sequence_rows(g, index, t.first, last);
-    t.len = last - t.first;
+    t = p.chained ? p.table[index] : Tile{index, 0, 1, 0, 0, 0};
+    if (t.seq == kNoTile) return;
+    together = WORK == kShort && t.seq == kShared;
+    if (together) {
+      const int32_t k = t.chunk + wave;
+      const bool is = k < t.chunks;
+      const uint32_t w = is ? p.shorts[k] : 0u;
+      t = Tile{int32_t(w & 0xFFFFFFu), 0, 0, 0, 0, 0};
+      if (is) {
+        t.chunks = min(int32_t(1u << (w >> 24)), g.sequences - t.seq);
+        int32_t end, ignored;
+        sequence_rows(g, t.seq, t.first, end);
+        sequence_rows(g, t.seq + t.chunks - 1, ignored, end);
+        t.len = max(end - t.first, 0);
+      }
+    } else if (!p.chained) {
+      int32_t end;
+      sequence_rows(g, t.seq, t.first, end);
+      t.len = end - t.first;
+    }
+    together = __builtin_amdgcn_readfirstlane(together);
   }
   // (scalar registers for all that follows from the tile, the buffer descriptors among it)
   t = Tile{__builtin_amdgcn_readfirstlane(t.seq),  __builtin_amdgcn_readfirstlane(t.chunk),
            __builtin_amdgcn_readfirstlane(t.chunks), __builtin_amdgcn_readfirstlane(t.base),
            __builtin_amdgcn_readfirstlane(t.first), __builtin_amdgcn_readfirstlane(t.len)};
   float carry = 0.f;
-  run_tile<T, KIND, MODE, RAGGED>(g, p, t, blk, sh, carry);
-  if constexpr (WALK) {
+  if constexpr (WORK == kShort) {
+    if (together) return run_tile<T, KIND, MODE, RAGGED, true>(g, p, t, blk, sh, carry);
+  }
+  run_tile<T, KIND, MODE, RAGGED, false>(g, p, t, blk, sh, carry);
+  if constexpr (WORK == kWalk) {
     while (++t.chunk < t.chunks) {
       __syncthreads();   // every wave has read the maps of the tile before
-      run_tile<T, KIND, MODE, RAGGED>(g, p, t, blk, sh, carry);
+      run_tile<T, KIND, MODE, RAGGED, false>(g, p, t, blk, sh, carry);
     }
   }
 }
 
 // Before chained tiles: the tickets to 0, every map to "not yet", and for packed sequences the table of
-// tiles, by the last block.
+// tiles, by the last block: those of the sequences that do not fit in a wave, then those of waves of short ones (of 8,
+// 4 or 2 sequences whose number starts at a multiple of that, if they fit in a wave together, or of one).
 __global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, int64_t zeros, int64_t words,
-                                                          int rows) {
+                                                          int rows, int runs) {
   const bool packed = p.per_sequence == 0;
   if (packed && blockIdx.x == gridDim.x - 1) {
     __shared__ Tile seq[256];
     const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     __shared__ int64_t sums[4];
+    __shared__ int32_t counts[4];
     int64_t base = 0;   // in 64 bits: overlapping sequences could have any number of tiles
+    int32_t shorts = 0;
     for (int s0 = 0; s0 < g.sequences && base < p.tiles; s0 += 256) {
       int32_t lo = 0, hi = 0, n = 0;
+      bool fits = false;
       if (s0 + tid < g.sequences) {
         sequence_rows(g, s0 + tid, lo, hi);
-        n = hi - lo <= rows ? 1 : (hi - lo + rows - 1) / rows;
+        fits = p.sharing && hi - lo <= rows / kWaves;
+        n = fits ? 0 : hi - lo <= rows ? 1 : (hi - lo + rows - 1) / rows;
       }
+      const int run = rows / kWaves / runs;
+      const int one = s0 + tid >= g.sequences ? 0 : fits ? max(1, (hi - lo + run - 1) / run) : runs + 1;
+      const int two = one + __shfl_xor(one, 1, 64), four = two + __shfl_xor(two, 2, 64);
+      const int log = four + __shfl_xor(four, 4, 64) <= runs ? 3 : four <= runs ? 2 : two <= runs ? 1 : 0;
+      fits = fits && tid % (1 << log) == 0;   // the first sequence of a wave
+      const uint64_t fitting = __ballot(fits);
       int64_t upto = n;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -627,13 +733,16 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, i
         if (lane >= o) upto += v;
       }
       __syncthreads();   // the strip before is in the table
-      if (lane == 63) sums[wave] = upto;
+      if (lane == 63) sums[wave] = upto, counts[wave] = __popcll(fitting);
       __syncthreads();
       int64_t total = 0;
+      int32_t at = shorts + __popcll(fitting & ((uint64_t(1) << lane) - 1));
       for (int w = 0; w < 4; ++w) {
-        if (w < wave) upto += sums[w];
+        if (w < wave) upto += sums[w], at += counts[w];
         total += sums[w];
+        shorts += counts[w];
       }
+      if (fits) p.shorts[at] = uint32_t(s0 + tid) | uint32_t(log) << 24;
       const int64_t mine = base + upto - n;
       seq[tid] = Tile{s0 + tid, 0, n, int32_t(mine < p.tiles ? mine : p.tiles), lo, hi - lo};
       __syncthreads();
@@ -649,7 +758,10 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, i
       }
       base += total;
     }
-    for (int64_t i = base + tid; i < p.tiles; i += 256) p.table[i].seq = -1;
+    for (int64_t i = base + tid; i < p.tiles; i += 256) {
+      const int64_t k = (i - base) * kWaves;
+      p.table[i] = Tile{k < shorts ? kShared : kNoTile, int32_t(k < shorts ? k : 0), shorts, 0, 0, 0};
+    }
     return;
   }
   const int64_t stride = int64_t(gridDim.x - (packed ? 1 : 0)) * 256;
@@ -719,15 +831,16 @@ hipError_t dispatch(int32_t dtype, int32_t kind, A... args) {
   }
 }
 
-template <typename T, int KIND, bool RAGGED, bool WALK>
+template <typename T, int KIND, bool RAGGED, int WORK>
 void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t stream) {
   const dim3 grid(uint32_t(p.tiles) * uint32_t(p.chans)), block(kThreads);
   if (back) {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kBackwardSaved, RAGGED, WALK>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, kBackward, RAGGED, WALK>), grid, block, 0, stream, g, p);
+    if (g.codes)
+      hipLaunchKernelGGL((gated_kernel<T, KIND, kBackwardSaved, RAGGED, WORK>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kBackward, RAGGED, WORK>), grid, block, 0, stream, g, p);
   } else {
-    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kForwardSave, RAGGED, WALK>), grid, block, 0, stream, g, p);
-    else hipLaunchKernelGGL((gated_kernel<T, KIND, kForward, RAGGED, WALK>), grid, block, 0, stream, g, p);
+    if (g.codes) hipLaunchKernelGGL((gated_kernel<T, KIND, kForwardSave, RAGGED, WORK>), grid, block, 0, stream, g, p);
+    else hipLaunchKernelGGL((gated_kernel<T, KIND, kForward, RAGGED, WORK>), grid, block, 0, stream, g, p);
   }
 }
 
@@ -752,7 +865,8 @@ struct Scan {
   static hipError_t run(const GatedArgs* g, bool back, hipStream_t stream) {
     const int rows = tile_rows(sizeof(T), KIND);
     Plan p = {};
-    if (!plan_sizes(g->sequences, g->tokens, g->channels, g->offsets != nullptr, rows, &p)) return hipErrorInvalidValue;
+    if (!plan_sizes(g->sequences, g->tokens, g->channels, g->offsets != nullptr, rows, runs_of(sizeof(T)), &p))
+      return hipErrorInvalidValue;
     // Two tiles: one block for both, and no maps.  (1 x 512 x 4096 bf16: 10.2 us against 7.5 and 5 for clearing the
     // maps; three tiles would take 15 against 14.)
     const bool walk = p.per_sequence == 2;
@@ -761,21 +875,26 @@ struct Scan {
       char* ws = static_cast<char*>(g->workspace);
       p.tickets = reinterpret_cast<uint32_t*>(ws);
       p.table = reinterpret_cast<Tile*>(ws + ticket_bytes(p));
-      p.maps = reinterpret_cast<uint64_t*>(ws + ticket_bytes(p) + table_bytes(p));
+      p.shorts = reinterpret_cast<uint32_t*>(ws + ticket_bytes(p) + table_bytes(p));
+      p.maps = reinterpret_cast<uint64_t*>(ws + ticket_bytes(p) + table_bytes(p) + short_bytes(g->sequences, p));
       const int64_t zeros = int64_t(ticket_bytes(p) / sizeof(v4u)), words = int64_t(map_bytes(p) / sizeof(v4u));
       const uint32_t blocks = uint32_t(std::min((words + 255) / 256, int64_t(1024))) + (p.per_sequence ? 0 : 1);
-      hipLaunchKernelGGL(gated_clear_kernel, dim3(blocks), dim3(256), 0, stream, *g, p, zeros, words, rows);
+      hipLaunchKernelGGL(gated_clear_kernel, dim3(blocks), dim3(256), 0, stream, *g, p, zeros, words, rows,
+                         runs_of(sizeof(T)));
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     choose_streams(*g, KIND, back, sizeof(T), &p);
     const bool ragged = g->channels % (16 / int(sizeof(T))) != 0;
     if (walk) {
-      if (ragged) launch_mode<T, KIND, true, true>(*g, p, back, stream);
-      else launch_mode<T, KIND, false, true>(*g, p, back, stream);
+      if (ragged) launch_mode<T, KIND, true, kWalk>(*g, p, back, stream);
+      else launch_mode<T, KIND, false, kWalk>(*g, p, back, stream);
+    } else if (p.sharing) {
+      if (ragged) launch_mode<T, KIND, true, kShort>(*g, p, back, stream);
+      else launch_mode<T, KIND, false, kShort>(*g, p, back, stream);
     } else {
-      if (ragged) launch_mode<T, KIND, true, false>(*g, p, back, stream);
-      else launch_mode<T, KIND, false, false>(*g, p, back, stream);
+      if (ragged) launch_mode<T, KIND, true, kTile>(*g, p, back, stream);
+      else launch_mode<T, KIND, false, kTile>(*g, p, back, stream);
     }
     return hipGetLastError();
   }
@@ -794,8 +913,8 @@ struct Step {
 
 size_t gated_workspace_bytes(int32_t sequences, int64_t tokens, int32_t channels, bool packed) {
   Plan p = {};
-  if (!plan_sizes(sequences, tokens, channels, packed, kFewestRows, &p)) return 0;
-  return p.chained ? ticket_bytes(p) + table_bytes(p) + map_bytes(p) : 256;
+  if (!plan_sizes(sequences, tokens, channels, packed, kFewestRows, runs_of(4), &p)) return 0;
+  return p.chained ? ticket_bytes(p) + table_bytes(p) + short_bytes(sequences, p) + map_bytes(p) : 256;
 }
 
 hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t stream) {

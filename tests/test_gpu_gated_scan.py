@@ -590,3 +590,86 @@ def test_step_of_more_elements_than_32_bits_count():
         s = before[part].clone()
         got = ssdq.gated_step(s, gate[part].clone(), u[part].clone(), gate_kind="logit")
         assert torch.equal(got, h[part]) and torch.equal(s, state[part]), lo
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("channels", [64, 75, 200])
+def test_short_sequences_share_blocks(channels, dtype, kind):
+    """Packed sequences of 0 to 90 tokens with a few long ones among them, and as many of one length: within the
+    bounds, and bit for bit what each gives in a call of its own."""
+    ssdq = lib()
+    rng = np.random.default_rng(channels)
+    sizes = rng.integers(0, 20, 301)
+    sizes[rng.integers(0, 301, 40)] = rng.integers(30, 91, 40)          # around the tokens of a wave: 32, 64
+    sizes[[7, 150, 300]] = (700, 129, 300)
+    offsets = np.concatenate([[3], 3 + np.cumsum(sizes)]).astype(np.int32)
+    d = Draw(101, TYPES[dtype], kind, 301, int(offsets[-1]) + 2, channels, offsets)
+    h = check_forward(d)
+    check_backward(d, h=h)
+    u = d.u if kind == "logit" else None
+    saved = ssdq.checkpoint_empty(d.u)
+    h, final = ssdq.gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind=kind, checkpoint=saved)
+    grads = ssdq.gated_scan_backward(d.gate, d.dh, u=u, checkpoint=saved, h0=d.h0, dh_final=d.dh_final,
+                                     offsets=d.offsets, gate_kind=kind)
+    for s in (0, 1, 7, 8, 40, 149, 150, 151, 299, 300):
+        lo, hi = int(offsets[s]), int(offsets[s + 1])
+        cut = lambda t: t[lo:hi].clone()[None]
+        one = lambda t: t[s:s + 1].clone()
+        h1, final1 = ssdq.gated_scan(cut(d.gate), cut(d.u), one(d.h0), gate_kind=kind)
+        assert torch.equal(h1[0], h[lo:hi]) and torch.equal(final1[0], final[s]), s
+        part = ssdq.gated_scan_backward(cut(d.gate), cut(d.dh), u=None if u is None else cut(u),
+                                        checkpoint=(cut(saved[0]), cut(saved[1])), h0=one(d.h0),
+                                        dh_final=one(d.dh_final), gate_kind=kind)
+        assert torch.equal(part[0][0], grads[0][lo:hi]) and torch.equal(part[1][0], grads[1][lo:hi]), s
+        assert torch.equal(part[2][0], grads[2][s]), s
+    state, back = d.h0.clone(), d.dh_final.clone()
+    ssdq.gated_scan(d.gate, d.u, state, d.offsets, gate_kind=kind, h_final=state)
+    ssdq.gated_scan_backward(d.gate, d.dh, u=u, checkpoint=saved, h0=d.h0, dh_final=back, offsets=d.offsets,
+                             gate_kind=kind, dh0=back)
+    assert torch.equal(state, final) and torch.equal(back, grads[2])
+
+
+@pytest.mark.parametrize("sequences,seqlen,channels", [(5, 3, 64), (4, 32, 72), (9, 33, 75), (130, 64, 8), (3, 65, 200)])
+def test_many_sequences_of_few_tokens(sequences, seqlen, channels):
+    for dtype in TYPES.values():
+        for kind in ("log", "logit"):
+            d = Draw(103, dtype, kind, sequences, sequences * seqlen, channels)
+            check_backward(d, h=check_forward(d))
+
+
+def test_few_tokens_in_many_sequences():
+    """Fewer tokens than a tile has, but more sequences and channels than blocks run at once; most sequences empty."""
+    offsets = np.sort(np.random.default_rng(5).integers(0, 91, 400)).astype(np.int32)
+    for kind in ("log", "logit"):
+        d = Draw(104, torch.bfloat16, kind, 399, 95, 1000, offsets)
+        check_backward(d, h=check_forward(d))
+
+
+def test_one_block_for_each_of_many_sequences():
+    """One sequence fewer than is refused, each of one more token than fits in a wave: a grid of nearly 2^32 threads."""
+    ssdq, n, seqlen = lib(), 2 ** 24 - 2, 33
+    gate = -torch.rand(n, seqlen, 1, device=DEV)
+    u, h0 = torch.randn(n, seqlen, 1, device=DEV), torch.randn(n, 1, device=DEV)
+    h, final = ssdq.gated_scan(gate, u, h0)
+    for part in (slice(0, 4096), slice(n // 2, n // 2 + 4096), slice(n - 4096, n)):
+        h1, final1 = ssdq.gated_scan(gate[part].clone(), u[part].clone(), h0[part].clone())
+        assert torch.equal(h1, h[part]) and torch.equal(final1, final[part])
+        with torch.no_grad():
+            a, x = gate[part].double().exp(), h0[part].double()
+            for t in range(seqlen):
+                x = a[:, t] * x + u[part][:, t].double()
+        assert torch.allclose(final1.double(), x, rtol=1e-4, atol=1e-4)
+
+
+def test_overlapping_short_sequences_stay_inside_the_tensors():
+    """Offsets out of order among sequences that fit in a wave, in rows that are no whole words."""
+    ssdq = lib()
+    for offsets in ([0, 500, 3, 20, 5, 9, 600, 2, 4], [590, 600, -5, 7, 600, 600, 0, 12, 11], [599] * 9,
+                    [0, 10 ** 9, 3, 2 ** 31 - 1, -2 ** 31, 4, 8, 600, 590]):
+        room = torch.full((8 + 600 * 67 + 8 * 67,), 7.0, dtype=torch.bfloat16, device=DEV)
+        h = room[8:8 + 600 * 67].view(600, 67)
+        d = Draw(82, torch.bfloat16, "log", 8, 600, 67, np.arange(9, dtype=np.int32))
+        ssdq.gated_scan(d.gate, d.u, d.h0, torch.tensor(offsets, dtype=torch.int32, device=DEV), h=h)
+        torch.cuda.synchronize()
+        assert bool((room[:8] == 7.0).all()) and bool((room[8 + 600 * 67:] == 7.0).all())
