@@ -534,6 +534,7 @@ def state_update(state, x, x_scale, B, B_scale, C, C_scale, dt, A, D=None, y=Non
 CHECKPOINT_BLOCK = 64                      # channels that share one scale
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _GATE_KINDS = {"log": 0, "logit": 1}       # ssdq_gate_kind
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _element_type(t: torch.Tensor, name: str) -> int:
@@ -557,6 +558,12 @@ def _expect(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape, device
     if t is None or not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device
                          and t.is_contiguous()):
         _need(t, name, dtype, shape, device, optional)
+
+
+def _int32(n: int, what: str) -> None:
+    """Sizes that the library takes as int32: ctypes would pass on the low 32 bits of a larger one."""
+    if n > _INT32_MAX:
+        raise ValueError(f"{what} must be below 2^31, got {n}")
 
 
 def _at(t: torch.Tensor | None) -> int | None:
@@ -595,6 +602,7 @@ def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | No
     `out` may give the two tensors."""
     dtype = _element_type(x, "x")
     shape, dev = x.shape, x.device
+    _int32(shape[-1], "the channels of x")
     _expect(x, "x", x.dtype, shape, dev)
     if out is None:
         codes, scale = checkpoint_empty(x)
@@ -612,6 +620,7 @@ def checkpoint_load(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype
     if codes.dim() < 1 or codes.shape[-1] == 0:
         raise ValueError("codes must have a last axis of at least one channel")
     shape, dev = codes.shape, codes.device
+    _int32(shape[-1], "the channels of codes")
     _expect_checkpoint(codes, scale, shape, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
@@ -626,6 +635,8 @@ def checkpoint_load(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype
 @functools.lru_cache(maxsize=1024)
 def gated_scan_workspace_size(sequences: int, tokens: int, channels: int, packed: bool = False) -> int:
     """Workspace bytes of gated_scan and gated_scan_backward (0: sizes that they do not take)."""
+    if not all(0 <= n <= _INT32_MAX for n in (sequences, tokens, channels)):
+        return 0
     return int(lib.ssdq_gated_scan_workspace_size(sequences, tokens, channels, int(packed)))
 
 
@@ -635,11 +646,13 @@ def _gated_sizes(gate: torch.Tensor, offsets: torch.Tensor | None) -> tuple[int,
     if offsets is None:
         if gate.dim() != 3:
             raise ValueError("gate must be (batch, seqlen, channels), or (tokens, channels) with offsets")
+        _int32(max(gate.shape[0], gate.shape[2]), "batch and channels")
         return gate.shape[0], gate.shape[0] * gate.shape[1], gate.shape[2]
     if gate.dim() != 2:
         raise ValueError("gate must be (tokens, channels) with offsets")
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must hold sequences + 1 >= 2 values")
+    _int32(max(offsets.numel(), gate.shape[1]), "offsets and channels")
     _need(offsets, "offsets", torch.int32, None, gate.device)
     return offsets.numel() - 1, gate.shape[0], gate.shape[1]
 
@@ -737,6 +750,7 @@ def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_ki
     if state.dim() != 2:
         raise ValueError("state must be (batch, channels)")
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), state.device, state.shape
+    _int32(max(shape), "batch and channels")
     _expect(state, "state", torch.float32, shape, dev)
     _expect(gate, "gate", gate.dtype, shape, dev)
     _expect(u, "u", gate.dtype, shape, dev)

@@ -94,3 +94,26 @@ def test_binding_refuses_before_any_launch():
         ssdq.gated_scan(x[0], x[0], offsets=torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="channel"):
         ssdq.checkpoint_empty(torch.zeros(2, 0))
+
+
+def test_sizes_of_more_than_32_bits():
+    """A size past int32 is refused, not passed on by its low 32 bits (meta tensors: shapes without memory)."""
+    wide = 2 ** 32 + 64
+    size = ssdq.gated_scan_workspace_size
+    assert size(1, 384, 64) > 0
+    assert size(1, 384, wide) == size(2 ** 32 + 1, 384, 64) == size(1, 2 ** 64 + 384, 64) == 0
+    assert size(-2 ** 32 + 1, 384, 64) == size(1, 384, 64 - 2 ** 32) == 0
+    meta = lambda *shape, dtype=torch.float16: torch.empty(shape, dtype=dtype, device="meta")
+    x = meta(1, wide)
+    codes, scale = ssdq.checkpoint_empty(x)
+    flat = meta(2, wide)
+    for call in (lambda: ssdq.checkpoint_save(x), lambda: ssdq.checkpoint_load(codes, scale, torch.float16),
+                 lambda: ssdq.gated_scan(x[None], x[None]), lambda: ssdq.gated_scan_backward(x[None], x[None], h=x[None]),
+                 lambda: ssdq.gated_scan(meta(2 ** 32 + 1, 0, 64), meta(2 ** 32 + 1, 0, 64)),
+                 lambda: ssdq.gated_scan(flat, flat, offsets=meta(2, dtype=torch.int32)),
+                 lambda: ssdq.gated_scan(meta(2, 64), meta(2, 64), offsets=meta(2 ** 32 + 2, dtype=torch.int32)),
+                 lambda: ssdq.gated_step(meta(1, wide, dtype=torch.float32), x, x),
+                 lambda: ssdq.gated_step(meta(2 ** 32 + 1, 8, dtype=torch.float32), meta(2 ** 32 + 1, 8),
+                                         meta(2 ** 32 + 1, 8))):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            call()
