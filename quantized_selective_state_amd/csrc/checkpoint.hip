@@ -104,6 +104,10 @@ hipError_t over_rows(int64_t rows, int32_t blocks, F f) {
   return hipSuccess;
 }
 
+// blocks of a row: up to 2^25 (channels + 63 may pass 31 bits)
+constexpr int32_t blocks_of(int32_t channels) { return int32_t((int64_t(channels) + kBlock - 1) / kBlock); }
+static_assert(blocks_of(0x7FFFFFFF) == 1 << 25 && blocks_of(65) == 2, "any row length has its blocks");
+
 template <int V>
 dim3 grid_of(int64_t items) {
   constexpr int64_t kPer = int64_t(kItems) * kThreads / (kBlock / V);
@@ -112,7 +116,7 @@ dim3 grid_of(int64_t items) {
 
 template <typename T, int V>
 hipError_t save(const void* x, int8_t* codes, float* scale, int64_t rows, int32_t channels, hipStream_t stream) {
-  const int32_t blocks = (channels + kBlock - 1) / kBlock;
+  const int32_t blocks = blocks_of(channels);
   return over_rows(rows, blocks, [&](int64_t n, int64_t r) {
     hipLaunchKernelGGL((checkpoint_save_kernel<T, V>), grid_of<V>(n * blocks), dim3(kThreads), 0, stream,
                        static_cast<const T*>(x) + r * channels, codes + r * channels, scale + r * blocks,
@@ -121,7 +125,7 @@ hipError_t save(const void* x, int8_t* codes, float* scale, int64_t rows, int32_
 }
 template <typename T, int V>
 hipError_t load(const int8_t* codes, const float* scale, void* x, int64_t rows, int32_t channels, hipStream_t stream) {
-  const int32_t blocks = (channels + kBlock - 1) / kBlock;
+  const int32_t blocks = blocks_of(channels);
   return over_rows(rows, blocks, [&](int64_t n, int64_t r) {
     hipLaunchKernelGGL((checkpoint_load_kernel<T, V>), grid_of<V>(n * blocks), dim3(kThreads), 0, stream,
                        codes + r * channels, scale + r * blocks, static_cast<T*>(x) + r * channels,

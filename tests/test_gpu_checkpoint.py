@@ -110,3 +110,21 @@ def test_more_blocks_than_a_launch_holds():
     assert torch.equal(scale, x.float().abs() * torch.tensor(1 / 127, device=DEV))
     back = ssdq.checkpoint_load(codes, scale, torch.bfloat16)
     assert torch.equal(back, (codes.float() * scale).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("channels", [2 ** 31 - 1, 2 ** 31 - 8], ids=["one-lane-each", "vectors"])
+def test_the_longest_rows(channels):
+    """Rows of nearly 2^31 channels: 2^25 blocks, whose last one equals the same channels as a row alone."""
+    ssdq = lib()
+    x = torch.full((1, channels), 0.5, device=DEV, dtype=torch.bfloat16)
+    lo = channels // 64 * 64 - 6400                                           # the last blocks, a partial one among them
+    x[0, lo:] = torch.randn(channels - lo, device=DEV)
+    codes, scale = ssdq.checkpoint_save(x)
+    assert scale.shape == (1, 2 ** 25)
+    want_codes, want_scale = ssdq.checkpoint_save(x[:, lo:].clone())
+    assert torch.equal(codes[:, lo:], want_codes) and torch.equal(scale[:, lo // 64:], want_scale)
+    assert bool((codes[:, :lo] == 127).all())
+    assert bool((scale[:, :lo // 64] == torch.tensor(0.5, device=DEV) * torch.tensor(1 / 127, device=DEV)).all())
+    back = ssdq.checkpoint_load(codes, scale, torch.bfloat16)
+    assert torch.equal(back[:, lo:], ssdq.checkpoint_load(want_codes, want_scale, torch.bfloat16))
+    assert bool((back[:, :lo] == 0.5).all())
