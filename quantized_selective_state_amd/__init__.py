@@ -566,6 +566,17 @@ def _int32(n: int, what: str) -> None:
         raise ValueError(f"{what} must be below 2^31, got {n}")
 
 
+def _no_gradient_lost(where: str, *tensors: torch.Tensor | None) -> None:
+    """The calls are no autograd nodes: where torch would record one, a result without it would drop gradients."""
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{where} records no gradient, but one of its tensors requires it: call it under "
+                             "torch.no_grad(), on detached tensors or within a torch.autograd.Function (whose backward "
+                             "calls gated_scan_backward)")
+
+
 def _at(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -675,7 +686,9 @@ def gated_scan(gate: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None = No
     offsets (sequences + 1) int32 on the device, in fp32, fp16 or bf16; h0 and h_final (batch,
     channels) fp32.  gate_kind "log": a = exp(gate), b = u; "logit": a = sigmoid(gate), b = (1 - a) u.
     checkpoint: (codes, scale) as of checkpoint_empty(u), which then receive the 8-bit checkpoint
-    of h.  h, h_final and workspace may give those tensors."""
+    of h.  h, h_final and workspace may give those tensors.  Tensors that require a gradient are refused
+    where autograd is on: the call records none (so are those of gated_scan_backward and gated_step)."""
+    _no_gradient_lost("gated_scan", gate, u, h0, h, h_final)
     sequences, tokens, channels = _gated_sizes(gate, offsets)
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
     _expect(gate, "gate", gate.dtype, shape, dev)
@@ -708,6 +721,7 @@ def gated_scan_backward(gate: torch.Tensor, dh: torch.Tensor, u: torch.Tensor | 
     checkpoint (codes, scale) (ssdq_gated_scan_backward).  u is needed with gate_kind "logit" only;
     gate, offsets and h0 are those of the forward call.  dgate, du, dh0 and workspace may give those
     tensors."""
+    _no_gradient_lost("gated_scan_backward", gate, dh, u, h, h0, dh_final, dgate, du, dh0)
     sequences, tokens, channels = _gated_sizes(gate, offsets)
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
     states = (sequences, channels)
@@ -747,6 +761,7 @@ def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_ki
                h: torch.Tensor | None = None) -> torch.Tensor:
     """One decode token of gated_scan (ssdq_gated_step): state (batch, channels) fp32 is updated in
     place; gate and u (batch, channels); returns h, the updated state in their type."""
+    _no_gradient_lost("gated_step", state, gate, u, h)
     if state.dim() != 2:
         raise ValueError("state must be (batch, channels)")
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), state.device, state.shape

@@ -117,3 +117,20 @@ def test_sizes_of_more_than_32_bits():
                                          meta(2 ** 32 + 1, 8))):
         with pytest.raises(ValueError, match="below 2\\^31"):
             call()
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """A call records no gradient, and would drop it unseen; without autograd the same tensors pass that check."""
+    plain = lambda *shape: torch.zeros(shape)
+    grad = lambda *shape: torch.zeros(shape, requires_grad=True)
+    x, s = plain(2, 3, 64), plain(2, 64)
+    calls = [lambda: ssdq.gated_scan(grad(2, 3, 64), x), lambda: ssdq.gated_scan(x, grad(2, 3, 64)),
+             lambda: ssdq.gated_scan(x, x, grad(2, 64)), lambda: ssdq.gated_scan(x, x, h=grad(2, 3, 64)),
+             lambda: ssdq.gated_scan_backward(grad(2, 3, 64), x, h=x), lambda: ssdq.gated_scan_backward(x, grad(2, 3, 64), h=x),
+             lambda: ssdq.gated_scan_backward(x, x, h=x, dh_final=grad(2, 64)),
+             lambda: ssdq.gated_step(grad(2, 64), s, s), lambda: ssdq.gated_step(s, s, grad(2, 64))]
+    for call in calls:
+        with pytest.raises(ValueError, match="records no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
+            call()

@@ -673,3 +673,38 @@ def test_overlapping_short_sequences_stay_inside_the_tensors():
         ssdq.gated_scan(d.gate, d.u, d.h0, torch.tensor(offsets, dtype=torch.int32, device=DEV), h=h)
         torch.cuda.synchronize()
         assert bool((room[:8] == 7.0).all()) and bool((room[8 + 600 * 67:] == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+def test_within_an_autograd_function(kind):
+    """The use in training: forward and backward as those of a torch.autograd.Function, on leaves that require a
+    gradient; the bits of the calls alone.  The calls on the leaves themselves are refused."""
+    ssdq = lib()
+    d = Draw(17, torch.bfloat16, kind, 2, 2 * 300, 72)
+
+    class Scan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, gate, u, h0):
+            saved = ssdq.checkpoint_empty(u)
+            h, final = ssdq.gated_scan(gate, u, h0, gate_kind=kind, checkpoint=saved)
+            ctx.save_for_backward(gate, u, h0, *saved)
+            return h, final
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dh, dh_final):
+            gate, u, h0, *saved = ctx.saved_tensors
+            return ssdq.gated_scan_backward(gate, dh, u=u, checkpoint=tuple(saved), h0=h0, dh_final=dh_final, gate_kind=kind)
+
+    leaves = [t.clone().requires_grad_() for t in (d.gate, d.u, d.h0)]
+    out = Scan.apply(*leaves)
+    torch.autograd.backward(out, (d.dh, d.dh_final))
+    saved = ssdq.checkpoint_empty(d.u)
+    want = ssdq.gated_scan(d.gate, d.u, d.h0, gate_kind=kind, checkpoint=saved)
+    grads = ssdq.gated_scan_backward(d.gate, d.dh, u=d.u, checkpoint=saved, h0=d.h0, dh_final=d.dh_final, gate_kind=kind)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(torch.equal(a.grad, b) for a, b in zip(leaves, grads))
+    with pytest.raises(ValueError, match="records no gradient"):
+        ssdq.gated_scan(*leaves, gate_kind=kind)
+    with torch.no_grad():
+        assert torch.equal(ssdq.gated_scan(*leaves, gate_kind=kind)[0], want[0])
