@@ -140,9 +140,17 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _public_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of torch.cuda.current_stream(index).  torch has it without building a Stream object (a step's call: 7.7 us
+# against 10), but not in its public interface: where a release lacks that function, the public one serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+
+
 def _stream(device: torch.device) -> ctypes.c_void_p:
-    # the raw handle of torch.cuda.current_stream(device), without building a Stream object
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return ctypes.c_void_p(_raw_stream(device.index))
 
 
 def _need(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple | None, device, optional=False):
@@ -585,10 +593,10 @@ def _call(function, where: str, device: torch.device, *args) -> None:
     """One library call on the current stream of `device`, with that device current."""
     index = device.index
     if index == torch.cuda.current_device():
-        status = function(*args, torch._C._cuda_getCurrentRawStream(index))
+        status = function(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = function(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = function(*args, _raw_stream(index))
     if status != SSDQ_SUCCESS:
         raise SSDQError(status, where)
 

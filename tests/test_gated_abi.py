@@ -134,3 +134,23 @@ def test_tensors_that_require_a_gradient_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
             call()
+
+
+def test_streams_without_the_private_function(monkeypatch):
+    """The binding loads and finds the current stream where torch lacks its private short cut."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("_ssdq_binding", ssdq.__file__)
+    binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(binding)
+
+    class Stream:
+        cuda_stream = 0x1230
+
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: asked.append(index) or Stream)
+    assert binding._stream(torch.device("cuda", 3)).value == 0x1230 and asked == [3]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    got = []
+    binding._call(lambda *args: got.extend(args) or binding.SSDQ_SUCCESS, "where", torch.device("cuda", 3), 5)
+    assert got == [5, 0x1230]

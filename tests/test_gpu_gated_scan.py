@@ -708,3 +708,12 @@ def test_within_an_autograd_function(kind):
         ssdq.gated_scan(*leaves, gate_kind=kind)
     with torch.no_grad():
         assert torch.equal(ssdq.gated_scan(*leaves, gate_kind=kind)[0], want[0])
+
+
+def test_both_ways_to_the_current_stream():
+    ssdq = lib()
+    s = torch.cuda.Stream()
+    for _ in range(2):
+        with torch.cuda.stream(s):
+            assert ssdq._raw_stream(0) == ssdq._public_raw_stream(0) == s.cuda_stream
+        assert ssdq._raw_stream(0) == ssdq._public_raw_stream(0) == torch.cuda.current_stream(0).cuda_stream
