@@ -601,10 +601,14 @@ def _call(function, where: str, device: torch.device, *args) -> None:
         raise SSDQError(status, where)
 
 
+def _some_channels(t: torch.Tensor, name: str) -> None:
+    if t.dim() < 1 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must have a last axis of at least one channel")
+
+
 def checkpoint_empty(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """Buffers for the 8-bit checkpoint of x (..., C): codes like x, int8, and scale (..., ceil(C/64)) fp32."""
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError("x must have a last axis of at least one channel")
+    _some_channels(x, "x")
     blocks = -(-x.shape[-1] // CHECKPOINT_BLOCK)
     return (torch.empty(x.shape, dtype=torch.int8, device=x.device),
             torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=x.device))
@@ -620,6 +624,7 @@ def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | No
     fp32 scale per 64 channels (..., ceil(C/64)) (ssdq_checkpoint_save).  Returns (codes, scale);
     `out` may give the two tensors."""
     dtype = _element_type(x, "x")
+    _some_channels(x, "x")
     shape, dev = x.shape, x.device
     _int32(shape[-1], "the channels of x")
     _expect(x, "x", x.dtype, shape, dev)
@@ -636,8 +641,7 @@ def checkpoint_save(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | No
 
 def checkpoint_load(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype, out: torch.Tensor | None = None):
     """The values codes * scale of an 8-bit checkpoint as a tensor of `dtype` (ssdq_checkpoint_load)."""
-    if codes.dim() < 1 or codes.shape[-1] == 0:
-        raise ValueError("codes must have a last axis of at least one channel")
+    _some_channels(codes, "codes")
     shape, dev = codes.shape, codes.device
     _int32(shape[-1], "the channels of codes")
     _expect_checkpoint(codes, scale, shape, dev)

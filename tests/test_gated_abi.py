@@ -154,3 +154,14 @@ def test_streams_without_the_private_function(monkeypatch):
     got = []
     binding._call(lambda *args: got.extend(args) or binding.SSDQ_SUCCESS, "where", torch.device("cuda", 3), 5)
     assert got == [5, 0x1230]
+
+
+def test_checkpoint_of_no_channels():
+    """Refused with its reason also where `out` is given (it divided by the number of channels)."""
+    for shape in ((), (0,), (3, 0)):
+        x = torch.zeros(shape)
+        out = (torch.zeros(shape, dtype=torch.int8), torch.zeros(shape))
+        for call in (lambda: ssdq.checkpoint_save(x), lambda: ssdq.checkpoint_save(x, out=out), lambda: ssdq.checkpoint_empty(x),
+                     lambda: ssdq.checkpoint_load(*out, torch.float32)):
+            with pytest.raises(ValueError, match="at least one channel"):
+                call()
