@@ -128,3 +128,29 @@ def test_the_longest_rows(channels):
     back = ssdq.checkpoint_load(codes, scale, torch.bfloat16)
     assert torch.equal(back[:, lo:], ssdq.checkpoint_load(want_codes, want_scale, torch.bfloat16))
     assert bool((back[:, :lo] == 0.5).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(8192, 1531), (2048, 4095)], ids=str)
+def test_large_activations_in_widths_that_no_vector_divides(shape, dtype):
+    g = torch.Generator(device=DEV).manual_seed(shape[1])
+    check(torch.randn(shape, generator=g, device=DEV).to(TYPES[dtype]))
+
+
+@pytest.mark.parametrize("channels", [1, 63, 65, 1531])
+def test_ragged_rows_leave_their_neighbours(channels):
+    """Codes, scales and values written inside larger buffers: nothing before or behind them changes."""
+    ssdq, rows = lib(), 77
+    blocks = -(-channels // 64)
+    for t in TYPES.values():
+        x = torch.randn(rows, channels, device=DEV).to(t)
+        edge = 1024
+        rooms = [torch.full((rows * w + 2 * edge,), 77, dtype=kind, device=DEV)
+                 for w, kind in ((channels, torch.int8), (blocks, torch.float32), (channels, t))]
+        codes, scale, back = (r[edge:-edge].view(rows, -1) for r in rooms)
+        ssdq.checkpoint_save(x, out=(codes, scale))
+        ssdq.checkpoint_load(codes, scale, t, out=back)
+        want = ssdq.checkpoint_save(x)
+        assert torch.equal(codes, want[0]) and torch.equal(scale, want[1])
+        assert torch.equal(back, ssdq.checkpoint_load(*want, t))
+        assert all(bool((r[:edge] == 77).all()) and bool((r[-edge:] == 77).all()) for r in rooms)

@@ -717,3 +717,142 @@ def test_both_ways_to_the_current_stream():
         with torch.cuda.stream(s):
             assert ssdq._raw_stream(0) == ssdq._public_raw_stream(0) == s.cuda_stream
         assert ssdq._raw_stream(0) == ssdq._public_raw_stream(0) == torch.cuda.current_stream(0).cuda_stream
+
+
+def saved_of_its_own(d, h, saved):
+    """`saved` (buffers filled with 77 and 7 before) is the checkpoint of h, and untouched in rows of no sequence."""
+    rows = torch.from_numpy(covered(d)).to(DEV)
+    codes, scale = lib().checkpoint_save(h)
+    got_codes, got_scale = saved[0].view(d.tokens, -1), saved[1].view(d.tokens, -1)
+    assert torch.equal(got_codes[rows], codes.view(d.tokens, -1)[rows])
+    assert torch.equal(got_scale[rows], scale.view(d.tokens, -1)[rows])
+    assert bool((got_codes[~rows] == 77).all()) and bool((got_scale[~rows] == 7.0).all())
+
+
+def filled_checkpoint(d):
+    codes, scale = lib().checkpoint_empty(d.u)
+    return codes.fill_(77), scale.fill_(7.0)
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("channels", [64, 75, 200])
+def test_checkpoints_that_waves_of_short_sequences_write(channels, dtype, kind):
+    """Packed sequences that share waves, and rows of none: the checkpoint of the h beside it, bit for bit, and the
+    gradient from it against the reference."""
+    rng = np.random.default_rng(channels + 1)
+    sizes = rng.integers(0, 20, 201)
+    sizes[rng.integers(0, 201, 30)] = rng.integers(30, 91, 30)
+    sizes[[7, 200]] = (700, 129)
+    offsets = np.concatenate([[3], 3 + np.cumsum(sizes)]).astype(np.int32)
+    d = Draw(111, TYPES[dtype], kind, 201, int(offsets[-1]) + 2, channels, offsets)
+    saved = filled_checkpoint(d)
+    h = torch.zeros(d.shape, dtype=d.dtype, device=DEV)
+    lib().gated_scan(d.gate, d.u, d.h0, d.offsets, gate_kind=kind, checkpoint=saved, h=h)
+    saved_of_its_own(d, h, saved)
+    assert torch.equal(h, check_forward(d).where(torch.from_numpy(covered(d)).to(DEV)[:, None], h))
+    check_backward(d, checkpoint=saved)
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(9, 9 * 33, 75), (130, 130 * 8, 64), (5, 15, 200), (3, 3 * 65, 130), (33, 33, 72),
+                                   (2, 2 * 300, 67), (3, 3 * 512, 64)], ids=str)
+def test_checkpoints_that_dense_calls_write(shape, dtype, kind):
+    """Dense sequences that share waves, that have a tile, and that have two."""
+    d = Draw(112 + shape[1], TYPES[dtype], kind, *shape)
+    saved = filled_checkpoint(d)
+    h, _ = lib().gated_scan(d.gate, d.u, d.h0, gate_kind=kind, checkpoint=saved)
+    saved_of_its_own(d, h, saved)
+    assert torch.equal(h, check_forward(d))
+    check_backward(d, checkpoint=saved)
+
+
+DISORDER = [[-50, 200, 5000, 600, 3, 7, 7, 9, 600], [400, 100, 600, 0, 10 ** 9, 10 ** 9, 5, 600, 2],
+            [0, 500, 3, 20, 5, 9, 600, 2, 4], [590, 600, -5, 7, 600, 600, 0, 12, 11], [599] * 9,
+            [0, 10 ** 9, 3, 2 ** 31 - 1, -2 ** 31, 4, 8, 600, 590]]
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("channels", [64, 67])
+def test_offsets_out_of_order_keep_every_output_inside(channels, dtype, kind):
+    """Forward with a checkpoint, and the gradient from h and from a checkpoint, for offsets that leave the tensors or
+    decrease: every output lies in a larger buffer whose other elements stay."""
+    ssdq, tokens = lib(), 600
+    d = Draw(113, TYPES[dtype], kind, 8, tokens, channels, np.arange(9, dtype=np.int32))
+    blocks = -(-channels // 64)
+
+    def room(width, dtype, fill):
+        edge = 64 * width                                # a multiple of 64 elements: the inner tensor stays aligned
+        buffer = torch.full((tokens * width + 2 * edge,), fill, dtype=dtype, device=DEV)
+        return buffer, buffer[edge:edge + tokens * width].view(tokens, width), edge
+
+    states = ssdq.checkpoint_save(d.u)
+    for offsets in DISORDER:
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        rooms = [room(channels, d.dtype, 7.0) for _ in range(3)] + [room(channels, torch.int8, 77),
+                                                                   room(blocks, torch.float32, 7.0)]
+        h, dgate, du, codes, scale = (r[1] for r in rooms)
+        u = d.u if kind == "logit" else None
+        for saved in (dict(h=d.u), dict(checkpoint=states)):
+            ssdq.gated_scan(d.gate, d.u, d.h0, off, gate_kind=kind, h=h, checkpoint=(codes, scale))
+            ssdq.gated_scan_backward(d.gate, d.dh, u=u, h0=d.h0, dh_final=d.dh_final, offsets=off, gate_kind=kind,
+                                     dgate=dgate, du=du, **saved)
+            torch.cuda.synchronize()
+            for buffer, _, edge in rooms:
+                fill = 77 if buffer.dtype == torch.int8 else 7.0
+                assert bool((buffer[:edge] == fill).all()) and bool((buffer[-edge:] == fill).all()), offsets
+
+
+@pytest.mark.parametrize("kind,seqlen", [("log", 512), ("logit", 256)])
+def test_large_batches_of_two_tiles(kind, seqlen):
+    """A batch of many sequences of two tiles each: some of them, in full, against the reference."""
+    ssdq, batch, channels = lib(), 64, 4096
+    g = torch.Generator(device=DEV).manual_seed(seqlen)
+    make = lambda *s: torch.randn(s, generator=g, device=DEV)
+    gate = (-make(batch, seqlen, channels).abs() * 0.1 if kind == "log" else make(batch, seqlen, channels) + 2).bfloat16()
+    u, dh = make(batch, seqlen, channels).bfloat16(), make(batch, seqlen, channels).bfloat16()
+    h0, dh_final = make(batch, channels), make(batch, channels)
+    saved = ssdq.checkpoint_empty(u)
+    h, final = ssdq.gated_scan(gate, u, h0, gate_kind=kind, checkpoint=saved)
+    grads = ssdq.gated_scan_backward(gate, dh, u=u, checkpoint=saved, h0=h0, dh_final=dh_final, gate_kind=kind)
+    full = ssdq.gated_scan_backward(gate, dh, u=u, h=h, h0=h0, dh_final=dh_final, gate_kind=kind)
+    codes, scale = ssdq.checkpoint_save(h)
+    assert torch.equal(saved[0], codes) and torch.equal(saved[1], scale)
+    host = lambda t: t.double().cpu().numpy().reshape(-1, channels)
+    bf16, f32 = torch.bfloat16, torch.float32
+    for s in (0, 31, 63):
+        one = slice(s, s + 1)
+        want, want_final, bound, final_bound = ref.forward(host(gate[s]), host(u[s]), host(h0[one]), kind, 1)
+        close(h[s], want, bound, bf16, "h")
+        close(final[one], want_final, final_bound, f32, "h_final")
+        values = ref.values(codes[s].cpu().numpy(), scale[s].cpu().numpy())
+        for got, states in ((grads, values), (full, host(h[s]))):
+            w = ref.backward(host(gate[s]), host(u[s]), states, host(h0[one]), host(dh[s]), host(dh_final[one]), kind, 1)
+            close(got[0][s], w[0], w[3], bf16, "dgate")
+            close(got[1][s], w[1], w[4], bf16, "du")
+            close(got[2][one], w[2], w[5], f32, "dh0")
+
+
+@pytest.mark.parametrize("kind", ["log", "logit"])
+def test_nan_stays_in_its_sequence_of_a_shared_wave(kind):
+    """Eight sequences to a wave, one with a NaN: the others keep their bits, forward and backward."""
+    ssdq = lib()
+    d = Draw(115, torch.bfloat16, kind, 48, 48 * 5, 72)
+
+    def run(u, dh):
+        h, final = ssdq.gated_scan(d.gate, u, d.h0, gate_kind=kind)
+        return (h, final, *ssdq.gated_scan_backward(d.gate, dh, u=u, h=h, h0=d.h0, dh_final=d.dh_final, gate_kind=kind))
+
+    clean = run(d.u, d.dh)
+    u, dh = d.u.clone(), d.dh.clone()
+    u[3, 2] = float("nan")
+    dh[20, 2] = float("inf")
+    others = torch.ones(48, dtype=torch.bool, device=DEV)
+    others[[3, 20]] = False
+    got = run(u, dh)
+    for a, b in zip(got, clean):
+        assert torch.equal(a[others], b[others])
+    assert bool(got[0][3, 2:].isnan().all()) and torch.equal(got[0][3, :2], clean[0][3, :2])
+    assert not got[4][20].isfinite().any()
