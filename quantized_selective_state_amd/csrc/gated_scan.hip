@@ -844,20 +844,21 @@ void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t strea
   }
 }
 
-// Non-temporal accesses, for rows of whole 128-byte lines (lines that two blocks share are worth keeping: packed 9001 x
-// 1531 bf16 30 against 38 us).  Loads, once a call touches more than the 256 MiB of the Infinity Cache, since what a
-// call reads is then gone before anything reads it again (forward 16384 x 5120 fp16 106 -> 97 us, backward 8192 x 4096
-// fp32 137 -> 121 us; below, 21 against 26 us); stores, once the outputs alone do (training step 32768 x 8192 bf16
-// forward 422 -> 346 us, backward 499 -> 428; a smaller output stays for what reads it: backward fp32 above 121 against
-// 132 us).  Not in the gradient of a logit gate, which reads four tensors: 298 us plain against 311 for 256 M
-// elements of bf16, 563 against 695 for as many of fp32.
+// Non-temporal accesses, for rows of whole 128-byte lines (lines that two blocks share are worth keeping: training
+// step 32768 x 8200 bf16 1254 us against 1585).  Loads, once a call touches more than the 256 MiB of the Infinity Cache, since what a
+// call reads is then gone before anything reads it again (forward 16384 x 5120 fp16 108 -> 99 us, backward 8192 x 4096
+// fp32 143 -> 123; below, 2 x 2048 x 4096 bf16, 23.6 us against 28.2 with them); stores, once the outputs alone do
+// (training step 32768 x 8192 bf16 902 -> 787 us with both; a smaller output stays for what reads it: backward fp32
+// above 123 against 135 us).  A logit gate's gradient too, which reads four tensors: 4 x 4096 x 8192 bf16 327 -> 307 us
+// from h and 306 -> 288 from a checkpoint, fp32 from h 600 -> 541.
 void choose_streams(const GatedArgs& g, int kind, bool back, int size, Plan* p) {
   constexpr int64_t kCache = int64_t(256) << 20;
   const int64_t tensor = g.tokens * g.channels * size, outputs = (back ? 2 : 1) * tensor;
-  const int64_t inputs = 2 * tensor + (!back ? 0 : g.codes ? tensor / size : tensor);
-  const bool lines = int64_t(g.channels) * size % 128 == 0, never = back && kind == SSDQ_GATE_LOGIT;
-  p->load_nt = lines && !never && inputs + outputs > kCache;
-  p->store_nt = lines && !never && outputs > kCache;
+  const int64_t saved = !back ? 0 : g.codes ? tensor / size : tensor;
+  const int64_t inputs = (back && kind == SSDQ_GATE_LOGIT ? 3 : 2) * tensor + saved;
+  const bool lines = int64_t(g.channels) * size % 128 == 0;
+  p->load_nt = lines && inputs + outputs > kCache;
+  p->store_nt = lines && outputs > kCache;
 }
 
 template <typename T, int KIND>

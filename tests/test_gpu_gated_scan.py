@@ -856,3 +856,25 @@ def test_nan_stays_in_its_sequence_of_a_shared_wave(kind):
         assert torch.equal(a[others], b[others])
     assert bool(got[0][3, 2:].isnan().all()) and torch.equal(got[0][3, :2], clean[0][3, :2])
     assert not got[4][20].isfinite().any()
+
+
+def test_large_logit_calls_equal_their_parts():
+    """As test_large_calls_equal_their_parts, for the gradient that reads four tensors."""
+    ssdq = lib()
+    g = torch.Generator(device=DEV).manual_seed(6)
+    shape = (4, 4000, 5120)
+    make = lambda: torch.randn(shape, generator=g, device=DEV).to(torch.float16)
+    gate, u, dh = make() + 2, make(), make()
+    h0 = torch.randn(4, 5120, generator=g, device=DEV)
+    saved = ssdq.checkpoint_empty(u)
+    h, final = ssdq.gated_scan(gate, u, h0, gate_kind="logit", checkpoint=saved)
+    back = lambda i, **states: ssdq.gated_scan_backward(gate[i], dh[i], u=u[i], h0=h0[i], dh_final=h0[i], gate_kind="logit",
+                                                        **states)
+    everything = slice(0, 4)
+    grads, full = back(everything, checkpoint=saved), back(everything, h=h)
+    for s in range(4):
+        one = slice(s, s + 1)
+        h1, final1 = ssdq.gated_scan(gate[one], u[one], h0[one], gate_kind="logit")
+        assert torch.equal(h1, h[one]) and torch.equal(final1, final[one])
+        for whole, states in ((grads, dict(checkpoint=(saved[0][one], saved[1][one]))), (full, dict(h=h[one]))):
+            assert all(torch.equal(a, b[one]) for a, b in zip(back(one, **states), whole))
