@@ -496,7 +496,8 @@ typedef enum {
 /*
  * 8-bit activation checkpoint: an activation kept between the forward and the backward pass as one
  * signed code per element and one binary32 scale per 64 consecutive channels of a row (1.0625
- * bytes per element), by the max/127 rule of the 8-bit decode state.
+ * bytes per element).  As in the 8-bit decode state the largest magnitude takes the code 127; its scale is
+ * a product here and the rounded quotient m / 127 there, so the two may differ in the last place.
  *
  *   m[r,k]     = max over i in block k of |x[r,i]|
  *   scale[r,k] = m * (1/127), one product of binary32 numbers, 1/127 rounded to binary32 (within
@@ -553,8 +554,10 @@ size_t ssdq_gated_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t
  *   workspace : device scratch of at least ssdq_gated_scan_workspace_size() bytes, owned by the
  *             caller, not shared with a concurrent call; it need not start at any value
  * Any sequences >= 1, tokens >= 0 and 1 <= channels <= 2^20 with tokens < 2^31 - 2^16 and
- * ceil(channels / 64) * (tokens / 128 + sequences) < 2^24 (else SSDQ_ERROR_UNSUPPORTED); dense
- * tokens must be a multiple of sequences.  With tokens == 0 the (tokens, ...) pointers are not looked at.
+ * ceil(channels / 64) * tiles < 2^24 (else SSDQ_ERROR_UNSUPPORTED), where tiles is, dense, sequences *
+ * max(1, ceil(L / 128)) and, packed, sequences, plus floor(tokens / 128) if tokens > 128; dense tokens must be
+ * a multiple of sequences.  With tokens == 0 the (tokens, ...) pointers are not looked at.  No output overlaps
+ * an input or another output, but for h_final on h0.
  * A NaN or infinity in gate, u or h0 makes the rows after it in its sequence and channel non-finite
  * or NaN (a = 0 does not clear it: 0 times infinity is NaN), and nothing else.  Products of a over up to
  * 256 neighbouring tokens of a sequence are formed on the way: where one is past binary32's range (only log
@@ -580,7 +583,8 @@ ssdq_status ssdq_gated_scan(int32_t dtype, int32_t gate_kind, const void* gate, 
  *   u       : (tokens, channels) of dtype; needed with SSDQ_GATE_LOGIT, not looked at otherwise
  *   h       : (tokens, channels) of dtype, or NULL with codes and scale given (exactly one of them)
  *   dh_final, dh0 : (sequences, channels) fp32 or NULL each; dh0 is written and may alias dh_final
- * Everything else as ssdq_gated_scan.
+ * Everything else as ssdq_gated_scan; no output overlaps an input (h0 among them) or another output, but for
+ * dh0 on dh_final.
  */
 ssdq_status ssdq_gated_scan_backward(int32_t dtype, int32_t gate_kind, const void* gate, const void* u, const void* h,
                                      const int8_t* codes, const float* scale, const float* h0, const void* dh,
@@ -592,7 +596,7 @@ ssdq_status ssdq_gated_scan_backward(int32_t dtype, int32_t gate_kind, const voi
  * One token of ssdq_gated_scan for every sequence of a decode batch, the state updated in place:
  *   state <- a state + b;   h = the updated state rounded to dtype
  *   state : (batch, channels) fp32, read and written     gate, u, h : (batch, channels) of dtype
- * batch, channels >= 1 with batch * channels < 2^36; no workspace.
+ * batch, channels >= 1 with batch * channels < 2^36; no workspace.  h and state overlap no other tensor.
  */
 ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, const void* gate, const void* u, void* h,
                             int32_t batch, int32_t channels, hipStream_t stream);

@@ -698,7 +698,8 @@ def gated_scan(gate: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None = No
     offsets (sequences + 1) int32 on the device, in fp32, fp16 or bf16; h0 and h_final (batch,
     channels) fp32.  gate_kind "log": a = exp(gate), b = u; "logit": a = sigmoid(gate), b = (1 - a) u.
     checkpoint: (codes, scale) as of checkpoint_empty(u), which then receive the 8-bit checkpoint
-    of h.  h, h_final and workspace may give those tensors.  Tensors that require a gradient are refused
+    of h.  h, h_final and workspace may give those tensors; only h_final may share memory with an input,
+    with h0.  Rows of no sequence are not written (in a tensor made here they hold anything).  Tensors that require a gradient are refused
     where autograd is on: the call records none (so are those of gated_scan_backward and gated_step)."""
     _no_gradient_lost("gated_scan", gate, u, h0, h, h_final)
     sequences, tokens, channels = _gated_sizes(gate, offsets)
@@ -732,7 +733,7 @@ def gated_scan_backward(gate: torch.Tensor, dh: torch.Tensor, u: torch.Tensor | 
     (None: zero), with the states of the forward pass given either as the saved h or as its 8-bit
     checkpoint (codes, scale) (ssdq_gated_scan_backward).  u is needed with gate_kind "logit" only;
     gate, offsets and h0 are those of the forward call.  dgate, du, dh0 and workspace may give those
-    tensors."""
+    tensors; only dh0 may share memory with an input, with dh_final."""
     _no_gradient_lost("gated_scan_backward", gate, dh, u, h, h0, dh_final, dgate, du, dh0)
     sequences, tokens, channels = _gated_sizes(gate, offsets)
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
@@ -772,7 +773,8 @@ def gated_scan_backward(gate: torch.Tensor, dh: torch.Tensor, u: torch.Tensor | 
 def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_kind: str = "log",
                h: torch.Tensor | None = None) -> torch.Tensor:
     """One decode token of gated_scan (ssdq_gated_step): state (batch, channels) fp32 is updated in
-    place; gate and u (batch, channels); returns h, the updated state in their type."""
+    place; gate and u (batch, channels); returns h, the updated state in their type, which shares memory
+    with none of them."""
     _no_gradient_lost("gated_step", state, gate, u, h)
     if state.dim() != 2:
         raise ValueError("state must be (batch, channels)")

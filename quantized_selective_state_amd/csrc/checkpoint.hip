@@ -1,7 +1,8 @@
 // 8-bit activation checkpoints: codes and one scale per 64 channels of a row, and their values.
 //
 // HBM-bound: 2 or 4 bytes in and 1 + 1/16 out per element, or the other way (8192 x 4096 bf16: both together 39 us,
-// 5.3 TB/s; one channel per lane and one block per wave took 158).  An item is one block of
+// 5.3 TB/s; one channel per lane and one block per wave took 158; a row length that 8 does not divide, one channel per
+// lane and four blocks in flight, takes 61 and 33 us at 8192 x 4095).  An item is one block of
 // 64 channels of a row.  Its 64 / V lanes hold V neighbouring channels each (16 bytes of x, where the
 // row length is a multiple of V: else one channel per lane), take the block's largest magnitude over the
 // lanes in registers, and a thread has the loads of kItems items in flight before it works on the first.

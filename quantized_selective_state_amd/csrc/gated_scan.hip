@@ -17,7 +17,7 @@
 // pass: enough bytes in flight (64 KB per block and four blocks per CU, hence raw inputs in the registers and the
 // gates formed in both passes; persistent blocks with prefetched tiles had half of that and took twice as long),
 // channels mapped to XCDs in runs, and non-temporal accesses for large calls.  Gates from logits cost a reciprocal
-// more per element and are near the vector units' limit as well (35 x 256 x 1536 bf16: 21 us, from logs 17).
+// more per element (4 x 2048 x 4096 bf16 forward: 52 us a call, from logs in tiles of the same size 50).
 #include <algorithm>
 
 #include "gated_types.h"
@@ -33,10 +33,12 @@ constexpr int kForward = 0, kForwardSave = 1;      // with the checkpoint of h w
 constexpr int kBackward = 2, kBackwardSaved = 3;   // from the saved h, from its checkpoint
 constexpr bool is_back(int mode) { return mode >= kBackward; }
 
-// Tokens of a tile.  A thread holds rows * 64 / 256 elements of each tensor, and no more of them than leaves three or
-// four blocks per CU: 256 tokens of a log gate in 16 bits (forward 8192 x 4096 bf16: 44 us, 47 with 128), 128 of 4
-// bytes (backward 8192 x 4096: 134 us, 138 with 256) and where a logit's sigmoids are kept too (backward 12345 x 2008
-// fp16: 76 us, 97 with 256).
+// Tokens of a tile.  A thread holds rows * 64 / 256 elements of each tensor, and no more of them than leaves four blocks
+// per CU forward (three in ragged rows with a checkpoint) and three or four backward (two: fp32 logit gates with the
+// saved h, and most 16-bit log gates where a block walks two tiles).  256 tokens of a log gate in 16 bits (calls: forward
+// 4 x 2048 x 4096 bf16 48 us, 50 with 128; 16384 x 5120 fp16 99 and 109); 128 where a logit's sigmoids are kept too
+// (backward 12345 x 2008 fp16 80 us, 92 with 256; 8192 x 4096 fp32 151 and 174) and for 4 bytes (log gates come out
+// even there: backward 8192 x 4096 123 and 122 us, 40 packed sequences of 9000 x 2048 74 and 77, 8192 x 1001 53 and 49).
 constexpr int tile_rows(int size, int kind) { return size == 4 || kind == SSDQ_GATE_LOGIT ? 128 : 256; }
 constexpr int kFewestRows = 128;   // the workspace is sized for any of them
 
@@ -99,10 +101,10 @@ bool plan_sizes(int32_t sequences, int64_t tokens, int32_t channels, bool packed
   if (tiles * p->chans >= (int64_t(1) << 24)) return false;   // a grid holds fewer than 2^32 threads
   const int64_t fits = rows / kWaves;
   if (packed) {
-    // The table of tiles is worth its launch where a block per sequence would be more blocks than run at once (60
-    // sequences, 200 tokens x 4096 bf16: 15.4 us against 17.6; 20 sequences: 14.6 against 12.3), and sharing where
-    // sequences are shorter than a tile on average (200 sequences, 8192 tokens x 4096: 55 us against 74; 37
-    // sequences, 9001 tokens x 1531: 33 against 31).
+    // The table of tiles is worth its launch where a block per sequence would be more blocks than run at once (200 tokens
+    // x 4096 bf16, a call with the table against one without: 60 sequences 15.9 and 17.9 us, 40 sequences 15.9 and
+    // 13.4, 20 sequences 15.6 and 12.9), and sharing where sequences are shorter than a tile on average (200 sequences,
+    // 8192 tokens x 4096: 63 us against 86; 150 sequences, 2000 tokens, training step: 59 against 144).
     p->chained = p->chained || int64_t(sequences) * p->chans > kManyBlocks;
     p->sharing = p->chained && tokens / rows < sequences;
     const int64_t most = std::min(int64_t(sequences), tokens / (fits + 1));   // sequences that do not fit in a wave
@@ -628,7 +630,9 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
   __shared__ Shared sh;
   // A block's channels go by its number, so that neighbouring channels of the same rows run on one XCD: its
   // blocks then use all channels of its L2.  (With the 8 XCDs' blocks interleaved, each XCD met only the
-  // lines of one residue mod 1 KB: 118 us against 109 at 16384 x 5120 fp16.)
+  // lines of one residue mod 1 KB: forward 16384 x 5120 fp16 108 us against 99, training step 8 x 4096 x 8192 bf16 868
+  // against 787, packed 12345 x 2008 91 against 80; of the cases measured only backward 8192 x 4096 fp32 had it the other
+  // way, 120 against 124.)
   const int32_t blk = xcd_remap(int32_t(blockIdx.x % uint32_t(p.chans)), p.chans);
   int32_t index = int32_t(blockIdx.x / uint32_t(p.chans));
   if (p.chained) {
@@ -702,6 +706,9 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs g, Plan p) {
 // Before chained tiles: the tickets to 0, every map to "not yet", and for packed sequences the table of
 // tiles, by the last block: those of the sequences that do not fit in a wave, then those of waves of short ones (of 8,
 // 4 or 2 sequences whose number starts at a multiple of that, if they fit in a wave together, or of one).
+//
+// 4 to 6 us, bound by the launch, up to some hundred sequences; the one block that makes the table then takes 4.1 us per
+// 1000 sequences (10,000 sequences of 8 tokens x 256 bf16: 43 of the call's 110 us, as a dense call 34 us).
 __global__ void __launch_bounds__(256) gated_clear_kernel(GatedArgs g, Plan p, int64_t zeros, int64_t words,
                                                           int rows, int runs) {
   const bool packed = p.per_sequence == 0;
@@ -845,12 +852,12 @@ void launch_mode(const GatedArgs& g, const Plan& p, bool back, hipStream_t strea
 }
 
 // Non-temporal accesses, for rows of whole 128-byte lines (lines that two blocks share are worth keeping: training
-// step 32768 x 8200 bf16 1254 us against 1585).  Loads, once a call touches more than the 256 MiB of the Infinity Cache, since what a
-// call reads is then gone before anything reads it again (forward 16384 x 5120 fp16 108 -> 99 us, backward 8192 x 4096
-// fp32 143 -> 123; below, 2 x 2048 x 4096 bf16, 23.6 us against 28.2 with them); stores, once the outputs alone do
-// (training step 32768 x 8192 bf16 902 -> 787 us with both; a smaller output stays for what reads it: backward fp32
-// above 123 against 135 us).  A logit gate's gradient too, which reads four tensors: 4 x 4096 x 8192 bf16 327 -> 307 us
-// from h and 306 -> 288 from a checkpoint, fp32 from h 600 -> 541.
+// step 32768 x 8200 bf16 1254 us against 1585).  Loads, once a call touches more than the 256 MiB of the Infinity Cache,
+// since what a call reads is then gone before anything reads it again (forward 16384 x 5120 fp16 108 -> 99 us, backward
+// 8192 x 4096 fp32 143 -> 123; below, 2 x 2048 x 4096 bf16, 23.6 us against 28.2 with them); stores, once the outputs
+// alone do (training step 32768 x 8192 bf16 902 -> 787 us with both; a smaller output stays for what reads it: backward
+// fp32 above 123 against 135 us).  A logit gate's gradient too, which reads four tensors: 4 x 4096 x 8192 bf16 327 -> 307
+// us from h and 306 -> 288 from a checkpoint, fp32 from h 600 -> 541.
 void choose_streams(const GatedArgs& g, int kind, bool back, int size, Plan* p) {
   constexpr int64_t kCache = int64_t(256) << 20;
   const int64_t tensor = g.tokens * g.channels * size, outputs = (back ? 2 : 1) * tensor;
@@ -868,8 +875,10 @@ struct Scan {
     Plan p = {};
     if (!plan_sizes(g->sequences, g->tokens, g->channels, g->offsets != nullptr, rows, runs_of(sizeof(T)), &p))
       return hipErrorInvalidValue;
-    // Two tiles: one block for both, and no maps.  (1 x 512 x 4096 bf16: 10.2 us against 7.5 and 5 for clearing the
-    // maps; three tiles would take 15 against 14.)
+    // Two tiles: one block for both, and no maps to clear.  Calls of 1, 8, 64 sequences walked, and chained through maps:
+    // 512 tokens x 4096 bf16 log, forward 13.0, 22.5, 141 and 15.6, 23.1, 144 us, training step 36, 70, 425 and 41, 76,
+    // 423 (4 sequences are the one loss: 45.5 and 40.8); 256 tokens, logit, training step 35, 46.5, 260 and 39, 47.5, 265;
+    // fp32 log, backward 15.7, 38, 258 and 18, 43, 269.  One sequence of three tiles would take 15 walked, 14 chained.
     const bool walk = p.per_sequence == 2;
     if (walk) p.chained = false, p.tiles = g->sequences;
     if (p.chained) {

@@ -42,7 +42,9 @@ __device__ __forceinline__ float logit_pair(float g) {
   const float e = exp_f32<EXACT>(-fabsf(g)), sum = 1.f + e;
   float inv = __builtin_amdgcn_rcpf(sum);
   // The hardware reciprocal is within 1.6 of 2^-24 and low by 0.1 of it on average.  For binary32 tensors one Newton
-  // step follows; beside the rounding of 16-bit ones it is not seen (a state of 1000 tokens is 6e-6 low).
+  // step follows; beside the rounding of 16-bit ones it is not seen: the smaller sigmoid is low by 6e-9 of itself, and the
+  // other one, 1 - that, high by as many parts of the smaller.  A state of memory 1 / (1 - a), which adds (1 - a) u, is
+  // moved by less than 6e-9 of the magnitudes in it, however long it is.
   if constexpr (EXACT) inv = fmaf(fmaf(-sum, inv, 1.f), inv, inv);
   return copysignf(e * inv, g);
 }
