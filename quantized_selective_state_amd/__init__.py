@@ -699,8 +699,9 @@ def gated_scan(gate: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None = No
     channels) fp32.  gate_kind "log": a = exp(gate), b = u; "logit": a = sigmoid(gate), b = (1 - a) u.
     checkpoint: (codes, scale) as of checkpoint_empty(u), which then receive the 8-bit checkpoint
     of h.  h, h_final and workspace may give those tensors; only h_final may share memory with an input,
-    with h0.  Rows of no sequence are not written (in a tensor made here they hold anything).  Tensors that require a gradient are refused
-    where autograd is on: the call records none (so are those of gated_scan_backward and gated_step)."""
+    with h0.  Rows of no sequence are not written (in a tensor made here they hold anything).  Tensors that
+    require a gradient are refused where autograd is on: the call records none (gated_scan_backward and
+    gated_step do the same)."""
     _no_gradient_lost("gated_scan", gate, u, h0, h, h_final)
     sequences, tokens, channels = _gated_sizes(gate, offsets)
     dtype, kind, dev, shape = _element_type(gate, "gate"), _kind(gate_kind), gate.device, gate.shape
