@@ -1,7 +1,7 @@
 // Element types, gates and 8-bit codes shared by the gated-scan and checkpoint kernels.
 #pragma once
 
-#include "ssdq_internal.h"
+#include "gated_internal.h"
 
 namespace ssdq {
 

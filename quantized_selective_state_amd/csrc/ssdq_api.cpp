@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "gated_internal.h"
 #include "ssdq_internal.h"
 
 using namespace ssdq;
