@@ -483,7 +483,7 @@ ssdq_status ssdq_frontend_step(void* conv_state, const void* xbc, const float* c
                                int32_t batch, int32_t nheads, int32_t headdim, int32_t dstate, int32_t ngroups,
                                hipStream_t stream);
 
-/* Element types of the gated scan and of activation checkpoints. */
+/* Element types of the gated scan, of activation checkpoints, of the norms and of the selective scan. */
 typedef enum {
   SSDQ_DTYPE_F32 = 0,   /* binary32 */
   SSDQ_DTYPE_F16 = 1,   /* IEEE binary16 */
@@ -600,6 +600,158 @@ ssdq_status ssdq_gated_scan_backward(int32_t dtype, int32_t gate_kind, const voi
  */
 ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, const void* gate, const void* u, void* h,
                             int32_t batch, int32_t channels, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of rows, the step ahead of a block's projections, with its output rounded to dtype or as
+ * 8-bit codes (the W8A8 projections of the Quamba project page and of the Quamba2 rebuttal).
+ *
+ *   v[r,c] = x[r,c]                                       plain
+ *            x[r,c] + residual[r,c]                       with residual (residual_out receives v, rounded)
+ *            x[r,c] * z / (1 + exp(-z)), z = gate[r,c]    with gate
+ *   n[r,c] = v[r,c] * weight[c] / sqrt(mean over the group of c of v[r,:]^2 + eps)
+ *
+ * in binary32; groups equal parts of a row's channels are normalized each by itself.  v is not rounded to dtype
+ * before it is squared and scaled.  The output is one of
+ *   out          : (rows, channels) of dtype = n, rounded to nearest even
+ *   codes, scale : (rows, channels) int8 and (rows) fp32: the row's scale is m * (1/127) with m = max |n[r,:]| (0, with
+ *                  zero codes, when m < 127 * 2^-126), a code the integer nearest to n / scale, ties to even
+ *   codes, static_scale : static_scale [1] fp32, device, positive and normal; a code is the integer nearest to
+ *                  n / static_scale, within [-127, 127] (NaN gives 0); scale is NULL then
+ * -128 is never produced.  A row whose sum of squares is not finite in binary32 (a NaN or an infinity in it, or
+ * magnitudes near 2^64) is NaN: out is NaN throughout, the scale is NaN and the codes 0, so that the fault is not hidden;
+ * with a static scale its codes are 0.  (With groups: out is NaN in that group, scale and codes over the row; under
+ * a static scale the codes are 0 in that group.)
+ *   dtype    : ssdq_dtype of x, gate and out     x, gate, out : (rows, channels)
+ *   residual_dtype : ssdq_dtype of residual and residual_out: dtype, or SSDQ_DTYPE_F32
+ *   residual, residual_out : (rows, channels) or both NULL; residual_out may be residual
+ *   gate     : (rows, channels) or NULL; not together with residual
+ *   weight   : (channels) fp32, device           eps : not negative, finite
+ * Any rows >= 0 (0 = no-op, pointers not looked at) below 2^31; 1 <= channels <= 16384, or 32768 with one group;
+ * 1 <= groups <= 256 and channels % groups == 0 (a remainder: SSDQ_ERROR_INVALID_VALUE; sizes beyond:
+ * SSDQ_ERROR_UNSUPPORTED).  No output overlaps an input or another output, but residual_out on residual.
+ */
+ssdq_status ssdq_rms_norm(int32_t dtype, int32_t residual_dtype, const void* x, const void* residual, const void* gate,
+                          const float* weight, const float* static_scale, void* out, int8_t* codes, float* scale,
+                          void* residual_out, int64_t rows, int32_t channels, int32_t groups, float eps,
+                          hipStream_t stream);
+
+/*
+ * Rows as 8-bit codes with one scale each: activations per token, or weights per output channel, as the operands of
+ * ssdq_matmul_i8.  Codes and scales are those of ssdq_rms_norm for n = x, bit-exact: scale = m * (1/127), codes the
+ * integers nearest to the exact quotient x / scale, ties to even.  A row that holds a NaN or an infinity gets the scale
+ * NaN and zero codes.
+ *   x : (rows, channels) of dtype     codes : (rows, channels) int8, written     scale : (rows) fp32, written
+ * Any rows >= 0 (0 = no-op) below 2^31 and 1 <= channels <= 32768 (else SSDQ_ERROR_UNSUPPORTED).
+ */
+ssdq_status ssdq_quantize_rows(int32_t dtype, const void* x, int8_t* codes, float* scale, int64_t rows,
+                               int32_t channels, hipStream_t stream);
+
+/*
+ * The values of such rows: x[r,c] = codes[r,c] * scale[r], formed in binary32 and rounded once to dtype.  Any codes
+ * (-128 reads as such) and any channels >= 1; everything else as ssdq_quantize_rows.
+ */
+ssdq_status ssdq_dequantize_rows(int32_t dtype, const int8_t* codes, const float* scale, void* x, int64_t rows,
+                                 int32_t channels, hipStream_t stream);
+
+/*
+ * Matrix product of 8-bit codes, the block's projections in W8A8:
+ *
+ *   out[m,n] = (float(sum_k a[m,k] b[n,k]) * a_scale[m]) * b_scale[n] + bias[n]
+ *
+ * The sum is exact in int32; the conversion, the two products and the sum with the bias are binary32 operations, each
+ * rounded to nearest even (the last product and the sum may be one fused operation), and out is rounded once more.
+ *   dtype   : ssdq_dtype of out
+ *   a       : (m, k) int8, a row per token            b    : (n, k) int8, a row per output channel
+ *   a_scale : (m) fp32 with a_scale_per_row nonzero, else [1]     b_scale : (n) fp32
+ *   bias    : (n) fp32 or NULL                         out  : (m, n) of dtype, written
+ * Any codes, -128 among them.  Any m >= 0 (0 = no-op, pointers not looked at), n >= 1, 1 <= k <= 131071 (above, a
+ * sum could leave int32) with m < 2^31 - 2^16 and ceil(m/128) * ceil(n/128) < 2^24 (else SSDQ_ERROR_UNSUPPORTED).  A NaN
+ * or an infinity in a scale or in bias makes the outputs that it enters non-finite or NaN, and no others.  out overlaps
+ * no input.
+ */
+ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale, int32_t a_scale_per_row,
+                           const int8_t* b, const float* b_scale, const float* bias, void* out, int64_t m, int32_t k,
+                           int32_t n, hipStream_t stream);
+
+/*
+ * Short causal convolution along the tokens of every channel, ahead of the selective scan (the convolution of the
+ * Mamba block; ssdq_frontend holds the Mamba-2 block's, fused with its quantizer):
+ *
+ *   a[t,c] = bias[c] + sum_k weight[c,k] x[t - width + 1 + k, c];    out = a, or a / (1 + exp(-a)) with silu nonzero
+ *
+ * in binary32, rounded once to dtype; rows before a sequence's first token are those of its state (or 0).
+ *   x, out    : (tokens, channels) of dtype; dense or packed by offsets exactly as in ssdq_gated_scan
+ *   weight    : (channels, width) fp32, tap width - 1 multiplies the token itself     bias : (channels) fp32 or NULL
+ *   state     : (sequences, width - 1, channels) of dtype or NULL (= 0): the inputs ahead of the first token, oldest
+ *               first
+ *   state_out : (sequences, width - 1, channels) of dtype or NULL, written: the inputs of each sequence's last width - 1
+ *               tokens, oldest first (of state where it has fewer); it must not be state
+ * width 2, 3 or 4; sequences, channels >= 1; tokens >= 0, dense a multiple of sequences; tokens < 2^31 - 2^16,
+ * sequences < 2^24, channels <= 2^20 and ceil(channels / 64) * (sequences + tokens / 16) < 2^31 (else
+ * SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of order give
+ * unspecified results but no access outside the tensors.  No output overlaps an input.
+ */
+ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, const float* bias, const void* state,
+                             const int32_t* offsets, void* out, void* state_out, int32_t sequences, int64_t tokens,
+                             int32_t channels, int32_t width, int32_t silu, hipStream_t stream);
+
+/*
+ * One token of ssdq_causal_conv for every sequence of a decode batch, the state updated in place:
+ *   state : (batch, width - 1, channels) of dtype, read and written     x, out : (batch, channels) of dtype
+ * batch, channels >= 1 with batch * channels < 2^31 (else SSDQ_ERROR_UNSUPPORTED).  No output overlaps an input.
+ */
+ssdq_status ssdq_causal_conv_step(int32_t dtype, void* state, const void* x, const float* weight, const float* bias,
+                                  void* out, int32_t batch, int32_t channels, int32_t width, int32_t silu,
+                                  hipStream_t stream);
+
+/* Bytes of workspace that ssdq_selective_scan needs (host; packed is nonzero for calls with offsets; 0 on invalid or
+ * unsupported sizes, else at least 256). */
+size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate,
+                                          int32_t packed);
+
+/*
+ * Selective state space scan with a decay for every channel and state and a step size for every channel (the recurrence
+ * h_t = Abar_t h_{t-1} + Bbar_t x_t of Ternary Mamba, Section 1, in the form of the first Mamba block, which the Quamba
+ * project page quantizes beside the second):
+ *
+ *   d_t[c]   = softplus(delta_t[c] + delta_bias[c])      (softplus nonzero; else delta_t[c] + delta_bias[c])
+ *   h_t[c,n] = exp(d_t[c] A[c,n]) h_{t-1}[c,n] + d_t[c] u_t[c] B_t[n],        h_{-1} = h0 (or 0)
+ *   y_t[c]   = (sum_n C_t[n] h_t[c,n] + D[c] u_t[c]) * z_t[c] / (1 + exp(-z_t[c]))      (without z: the bracket)
+ *
+ * over every token of every sequence, in binary32 whatever the types; y is rounded once.
+ *   dtype        : ssdq_dtype of u, delta, B, C, z and y
+ *   u, delta, y  : (tokens, channels); z the same or NULL     B, C : (tokens, dstate)
+ *   A            : (channels, dstate) fp32     D, delta_bias : (channels) fp32 or NULL (= 0) each
+ *   offsets      : NULL (dense) or (sequences + 1) int32, exactly as in ssdq_gated_scan
+ *   h0, h_final  : (sequences, channels, dstate) fp32 or NULL each; h_final is the state after each sequence's last token
+ *                  (h0, or 0, for one without tokens) and must not be h0
+ *   workspace    : device scratch of at least ssdq_selective_scan_workspace_size() bytes, owned by the caller, not
+ *                  shared with a concurrent call; it need not start at any value
+ * sequences >= 1, tokens >= 0, channels >= 1, 1 <= dstate <= 64; dense tokens a multiple of sequences (else
+ * SSDQ_ERROR_INVALID_VALUE); tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20, fewer than 2^23 chunks of 256 tokens
+ * (dense: of each sequence) and a workspace below 2^40 bytes (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 the (tokens, ...) pointers are not looked
+ * at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence and
+ * channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
+ * products of it over 256 neighbouring tokens stay finite.  The result does not depend on timing: calls with the same
+ * arguments give the same bits.
+ */
+ssdq_status ssdq_selective_scan(int32_t dtype, const void* u, const void* delta, const float* A, const void* B,
+                                const void* C, const float* D, const void* z, const float* delta_bias, const float* h0,
+                                const int32_t* offsets, void* y, float* h_final, int32_t sequences, int64_t tokens,
+                                int32_t channels, int32_t dstate, int32_t softplus, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of ssdq_selective_scan for every sequence of a decode batch, the state updated in place:
+ *   state : (batch, channels, dstate) fp32, read and written     u, delta, z, y : (batch, channels)
+ *   B, C  : (batch, dstate)
+ * batch, channels >= 1, 1 <= dstate <= 64, batch * channels < 2^31 (else SSDQ_ERROR_UNSUPPORTED); no workspace.  No
+ * output overlaps another tensor.
+ */
+ssdq_status ssdq_selective_step(int32_t dtype, float* state, const void* u, const void* delta, const float* A,
+                                const void* B, const void* C, const float* D, const void* z, const float* delta_bias,
+                                void* y, int32_t batch, int32_t channels, int32_t dstate, int32_t softplus,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -790,3 +790,11 @@ def gated_step(state: torch.Tensor, gate: torch.Tensor, u: torch.Tensor, gate_ki
         _expect(h, "h", gate.dtype, shape, dev)
     _call(lib.ssdq_gated_step, "ssdq_gated_step", dev, dtype, kind, _at(state), _at(gate), _at(u), _at(h), *shape)
     return h
+
+
+# ---------------------------------------------------------------------------------------------
+# the block around the scans: norms, 8-bit product, convolution and selective scan
+
+from .block import (causal_conv, causal_conv_step, dequantize_rows, gated_rms_norm,  # noqa: E402,F401
+                    gated_rms_norm_i8, matmul_i8, quantize_rows, rms_norm, rms_norm_i8, selective_scan,
+                    selective_scan_workspace_size, selective_step)

@@ -1,0 +1,302 @@
+// Root-mean-square norm of rows with the residual's addition or a gate, output in the inputs' type or as 8-bit codes
+// with a scale per row; rows as codes without a norm; and their values.
+//
+// One pass: n = (v w) / sqrt(mean(v^2) + eps), and since multiplying by the positive root is monotone in binary32,
+// max |n| is max |v w| times it.  So the sum of squares and the largest |v w| are reduced together, the row stays in
+// registers between, and a block has one barrier per row (none where a row fits one wave).
+#include "block_internal.h"
+#include "gated_types.h"
+
+namespace ssdq {
+namespace {
+
+constexpr int V = 8;              // neighbouring channels of a lane
+constexpr int kMostThreads = 1024;
+enum Source { kPlain, kResidual, kGate };
+enum Output { kValues, kDynamic, kStatic };
+
+template <typename T>
+struct Eight { T e[V]; };
+
+// Rows start at any element, so the loads and stores are of 16 bytes (or 32, or 8) at any alignment; the last channels
+// of a group one by one.
+template <typename T>
+__device__ __forceinline__ void load_some(const T* __restrict__ p, int count, float (&v)[V]) {
+  Eight<T> raw = {};
+  if (count >= V) {
+    __builtin_memcpy(&raw, p, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < count) raw.e[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = to_f32(raw.e[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* __restrict__ p, int count, const Eight<T>& raw) {
+  if (count >= V) {
+    __builtin_memcpy(p, &raw, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < count) p[i] = raw.e[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ Eight<T> rounded(const float (&v)[V]) {
+  Eight<T> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.e[i] = from_f32<T>(v[i]);
+  return r;
+}
+
+__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + exp_f32<true>(-v)); }
+
+struct NormKernelArgs {
+  const void* x;
+  const void* other;        // residual or gate
+  const float* weight;
+  const float* static_scale;
+  void* out;
+  int8_t* codes;
+  float* scale;
+  void* residual_out;
+  int64_t rows;
+  int32_t channels, groups, size;   // size = channels / groups
+  int32_t lanes;                    // threads of a group, a power of two
+  int32_t per_block;                // rows of a block
+  float eps, inverse_size;
+};
+
+// sum and most over the `lanes` (at most 64) neighbouring lanes of a group, in all of them
+__device__ __forceinline__ void reduce_lanes(float& sum, uint32_t& most, int lanes) {
+  for (int d = 1; d < lanes && d < kWave; d <<= 1) {
+    sum += __shfl_xor(sum, d);
+    most = max(most, uint32_t(__shfl_xor(int(most), d)));
+  }
+}
+
+__device__ __forceinline__ float root(float sum, const NormKernelArgs& a) {
+  return sum < __builtin_inff() ? 1.f / sqrtf(fmaf(sum, a.inverse_size, a.eps)) : __builtin_nanf("");
+}
+
+template <typename T, typename R, int SOURCE, bool NORM, int OUT, int SLOTS>
+__global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
+  __shared__ float sums[2][kMostThreads];       // of a wave, or of a group with fewer lanes; two rows in turn
+  __shared__ uint32_t mosts[2][kMostThreads];
+  const int sub = int(threadIdx.x) / a.lanes, lane = int(threadIdx.x) % a.lanes;
+  const int in_block = sub / a.groups, group = sub % a.groups;
+  const int unit = a.lanes < kWave ? a.lanes : kWave;            // threads that share one entry of sums
+  const int entry = int(threadIdx.x) / unit;
+  const int per_group = a.lanes / unit;
+  const int first = in_block * a.groups * per_group;             // the row's entries
+  const bool alone = a.groups == 1 && per_group == 1;
+  const int start = group * a.size;
+
+  float w[SLOTS][V];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int c = (s * a.lanes + lane) * V;
+      load_some(a.weight + start + c, in_block < a.per_block ? a.size - c : 0, w[s]);
+    }
+  }
+  int parity = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * a.per_block; row0 < a.rows; row0 += int64_t(gridDim.x) * a.per_block) {
+    const int64_t row = row0 + in_block;
+    const bool live = in_block < a.per_block && row < a.rows;
+    const int64_t at = row * a.channels + start;
+    float v[SLOTS][V], sum = 0.f;
+    uint32_t most = 0;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int c = (s * a.lanes + lane) * V, count = live ? a.size - c : 0;
+      load_some(static_cast<const T*>(a.x) + at + c, count, v[s]);
+      if constexpr (SOURCE != kPlain) {
+        float o[V];
+        load_some(static_cast<const R*>(a.other) + at + c, count, o);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[s][i] = SOURCE == kResidual ? v[s][i] + o[i] : v[s][i] * silu(o[i]);
+        if constexpr (SOURCE == kResidual)
+          store_some(static_cast<R*>(a.residual_out) + at + c, count, rounded<R>(v[s]));
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (NORM) {
+          sum = fmaf(v[s][i], v[s][i], sum);
+          v[s][i] *= w[s][i];
+        }
+        if constexpr (OUT == kDynamic) most = max(most, __float_as_uint(fabsf(v[s][i])));
+      }
+    }
+    reduce_lanes(sum, most, a.lanes);
+    float r = 1.f;
+    if (alone) {
+      if constexpr (NORM) {
+        r = root(sum, a);
+        most = __float_as_uint(fabsf(__uint_as_float(most) * r));
+      }
+    } else {
+      sums[parity][entry] = sum;
+      mosts[parity][entry] = most;
+      __syncthreads();
+      const int entries = a.groups * per_group;
+      most = 0;
+      for (int g = 0, e = 0; e < entries; ++g) {   // every group's root, for the row's largest value
+        float total = 0.f;
+        uint32_t top = 0;
+        for (int k = 0; k < per_group; ++k, ++e) {
+          total += sums[parity][first + e];
+          top = max(top, mosts[parity][first + e]);
+        }
+        if constexpr (NORM) {
+          const float its = root(total, a);
+          if (g == group) r = its;
+          top = __float_as_uint(fabsf(__uint_as_float(top) * its));
+        }
+        most = max(most, top);
+      }
+      parity ^= 1;
+    }
+    float s = 0.f;
+    if constexpr (OUT == kDynamic) {
+      s = checkpoint_scale(most);
+      if (live && group == 0 && lane == 0) a.scale[row] = s;
+    } else if constexpr (OUT == kStatic) {
+      s = a.static_scale[0];
+    }
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int c = (k * a.lanes + lane) * V, count = live ? a.size - c : 0;
+      float n[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        n[i] = NORM ? v[k][i] * r : v[k][i];
+        // beyond 127 scales a code is 127, and a NaN has the code 0; the bound is within a rounding of 127 s
+        if constexpr (OUT == kStatic) n[i] = n[i] != n[i] ? 0.f : fminf(fmaxf(n[i], -127.f * s), 127.f * s);
+      }
+      if constexpr (OUT == kValues) {
+        store_some(static_cast<T*>(a.out) + at + c, count, rounded<T>(n));
+      } else {
+        const auto packed = codes_of<V>(n, s);
+        store_some(a.codes + at + c, count, __builtin_bit_cast(Eight<int8_t>, packed));
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __restrict__ codes,
+                                                              const float* __restrict__ scale, T* __restrict__ x,
+                                                              int64_t rows, int32_t channels, int32_t lanes) {
+  const int per_block = 256 / lanes, lane = int(threadIdx.x) % lanes;
+  for (int64_t row = int64_t(blockIdx.x) * per_block + threadIdx.x / lanes; row < rows;
+       row += int64_t(gridDim.x) * per_block) {
+    const float s = scale[row];
+    for (int64_t c = int64_t(lane) * V; c < channels; c += int64_t(lanes) * V) {
+      const int count = int(min(int64_t(V), channels - c));
+      float v[V];
+      load_some(codes + row * channels + c, count, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= s;
+      store_some(x + row * channels + c, count, rounded<T>(v));
+    }
+  }
+}
+
+int32_t multiprocessors() {
+  int device = 0, cus = 256;
+  if (hipGetDevice(&device) == hipSuccess)
+    (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+  return cus > 0 ? cus : 256;
+}
+
+int32_t power_of_two(int32_t n) {
+  int32_t p = 1;
+  while (p < n) p <<= 1;
+  return p;
+}
+
+template <typename T, typename R, int SOURCE, bool NORM, int OUT>
+hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
+  NormKernelArgs a = {};
+  a.x = n.x;
+  a.other = SOURCE == kResidual ? n.residual : n.gate;
+  a.weight = n.weight;
+  a.static_scale = n.static_scale;
+  a.out = n.out;
+  a.codes = n.codes;
+  a.scale = n.scale;
+  a.residual_out = n.residual_out;
+  a.rows = n.rows;
+  a.channels = n.channels;
+  a.groups = n.groups;
+  a.size = n.channels / n.groups;
+  a.eps = n.eps;
+  a.inverse_size = 1.f / float(a.size);
+  const int32_t packs = (a.size + V - 1) / V;
+  // up to four packs a lane, eight where the block would else be too large (the limits on sizes make that enough)
+  a.lanes = power_of_two((packs + 3) / 4);
+  if (a.lanes * a.groups > kMostThreads) a.lanes = power_of_two((packs + 7) / 8);
+  const int32_t threads = a.lanes * a.groups;
+  if (threads > kMostThreads) return hipErrorInvalidValue;
+  a.per_block = threads >= 256 ? 1 : 256 / threads;
+  const int32_t block = (threads * a.per_block + kWave - 1) / kWave * kWave;
+  const int64_t items = (a.rows + a.per_block - 1) / a.per_block;
+  const int64_t most = int64_t(multiprocessors()) * (2048 / block);
+  const dim3 grid(uint32_t(items < most ? items : most));
+  const int32_t slots = (packs + a.lanes - 1) / a.lanes;
+  if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1><<<grid, block, 0, stream>>>(a);
+  else if (slots <= 2) norm_kernel<T, R, SOURCE, NORM, OUT, 2><<<grid, block, 0, stream>>>(a);
+  else if (slots <= 4) norm_kernel<T, R, SOURCE, NORM, OUT, 4><<<grid, block, 0, stream>>>(a);
+  else norm_kernel<T, R, SOURCE, NORM, OUT, 8><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, typename R, int SOURCE>
+hipError_t launch_output(const NormArgs& a, hipStream_t stream) {
+  if (a.out != nullptr) return launch_slots<T, R, SOURCE, true, kValues>(a, stream);
+  if (a.scale != nullptr) return launch_slots<T, R, SOURCE, true, kDynamic>(a, stream);
+  return launch_slots<T, R, SOURCE, true, kStatic>(a, stream);
+}
+
+template <typename T>
+hipError_t launch_source(const NormArgs& a, hipStream_t stream) {
+  if (a.weight == nullptr) return launch_slots<T, T, kPlain, false, kDynamic>(a, stream);
+  if (a.gate != nullptr) return launch_output<T, T, kGate>(a, stream);
+  if (a.residual == nullptr) return launch_output<T, T, kPlain>(a, stream);
+  if (a.residual_dtype == a.dtype) return launch_output<T, T, kResidual>(a, stream);
+  return launch_output<T, float, kResidual>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  switch (a.dtype) {
+    case SSDQ_DTYPE_F32: return launch_source<float>(a, stream);
+    case SSDQ_DTYPE_F16: return launch_source<_Float16>(a, stream);
+    default: return launch_source<__bf16>(a, stream);
+  }
+}
+
+hipError_t launch_dequantize_rows(int32_t dtype, const int8_t* codes, const float* scale, void* x, int64_t rows,
+                                  int32_t channels, hipStream_t stream) {
+  const int32_t packs = int32_t((int64_t(channels) + V - 1) / V);
+  const int32_t lanes = packs >= 256 ? 256 : power_of_two(packs);
+  const int64_t items = (rows + 256 / lanes - 1) / (256 / lanes), most = int64_t(multiprocessors()) * 16;
+  const dim3 grid(uint32_t(items < most ? items : most));
+  switch (dtype) {
+    case SSDQ_DTYPE_F32:
+      dequantize_rows_kernel<<<grid, 256, 0, stream>>>(codes, scale, static_cast<float*>(x), rows, channels, lanes);
+      break;
+    case SSDQ_DTYPE_F16:
+      dequantize_rows_kernel<<<grid, 256, 0, stream>>>(codes, scale, static_cast<_Float16*>(x), rows, channels, lanes);
+      break;
+    default:
+      dequantize_rows_kernel<<<grid, 256, 0, stream>>>(codes, scale, static_cast<__bf16*>(x), rows, channels, lanes);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ssdq
