@@ -16,20 +16,38 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 16;            // rows of B and C in LDS at a time
+constexpr int kGroup = 4;            // rows whose values are loaded together, one group ahead
 constexpr float kLog2e = 1.44269502e+00f;
 
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), to a few 2^-24 of itself also where it is small: there by the
-// series of log(1 + e), else by the hardware's logarithm of w = 1 + e with the rounding of that sum put back.
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|); log(1 + e) = e P(e) with a polynomial fitted to it on [0, 1] (within
+// 2.3 half places of itself in binary32), so that also small step sizes keep their relative precision.  -inf gives 0.
+template <bool EXACT>
 __device__ __forceinline__ float softplus(float v) {
-  const float e = exp_f32<true>(-fabsf(v));
-  const float w = 1.f + e, lost = e - (w - 1.f);
-  const float large = fmaf(__builtin_amdgcn_logf(w), 0.693147182f, lost * __builtin_amdgcn_rcpf(w));
-  const float small = e * fmaf(-e, fmaf(-e, fmaf(-e, 0.25f, 0.333333343f), 0.5f), 1.f);
-  const float log1p = e < 0.015625f ? small : large;
-  return fmaxf(v, 0.f) + log1p;
+  const float e = exp_f32<EXACT>(fmaxf(-fabsf(v), -104.f));
+  float p = 0.0051058256f;
+  p = fmaf(p, e, -0.028991956f);
+  p = fmaf(p, e, 0.077380739f);
+  p = fmaf(p, e, -0.135905996f);
+  p = fmaf(p, e, 0.190713093f);
+  p = fmaf(p, e, -0.248339459f);
+  p = fmaf(p, e, 0.333179355f);
+  p = fmaf(p, e, -0.499994367f);
+  p = fmaf(p, e, 0.99999994f);
+  return fmaf(p, e, v < 0.f ? 0.f : v);   // (a NaN stays one)
 }
-__device__ __forceinline__ float gated(float y, float z) {
-  return y * z * __builtin_amdgcn_rcpf(1.f + exp_f32<true>(-z));
+template <bool EXACT>
+__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + exp_f32<EXACT>(-z)); }
+
+// One element of a lane at `lane` bytes, `row` bytes (the same for all lanes) into a buffer.
+template <typename T>
+__device__ __forceinline__ T load_element(Rsrc r, uint32_t lane, uint32_t row) {
+  if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, int(lane), int(row), 0));
+  else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, int(lane), int(row), 0));
+}
+template <typename T>
+__device__ __forceinline__ void store_element(Rsrc r, uint32_t lane, uint32_t row, T v) {
+  if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, int(lane), int(row), 0);
+  else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(u16, v), r, int(lane), int(row), 0);
 }
 
 struct ScanKernelArgs {
@@ -63,17 +81,30 @@ __device__ __forceinline__ Span chunk_rows(const ScanKernelArgs& a, int32_t k) {
   return Span{span.begin + i * a.chunk, int32_t(min(int64_t(span.begin) + int64_t(i + 1) * a.chunk, int64_t(span.end)))};
 }
 
-template <typename T, int N, bool OUTPUT>
-__global__ void __launch_bounds__(kThreads) chunk_kernel(ScanKernelArgs a) {
-  __shared__ float Bs[kRows][N], Cs[OUTPUT ? kRows : 1][N];
-  const int32_t c = int32_t(blockIdx.y) * kThreads + int32_t(threadIdx.x);
+// The first kernel (OUTPUT false) forms what leaves a chunk by itself, the third one y and the final states.
+//
+// Of a block's four waves G share 64 channels, with N of the states each; their parts of C . h meet in LDS.  The products
+// d u B[n] and their sum with exp(d A) h come from the matrix unit: one 4 x 4 x 1 instruction of 16 blocks is, for the 64
+// channels of the lanes, an outer product of 4 states of B and d u, added to 4 registers of each lane.
+template <typename T, int N, int G, bool OUTPUT>
+__global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKernelArgs a) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr int kChannels = kThreads / G, kStates = N * G;
+  constexpr int kPer = (kRows * kStates + kThreads - 1) / kThreads;   // values of B, and of C, that a thread stages
+  __shared__ __attribute__((aligned(16))) float Bs[2][kRows][G][4][N / 4];   // state 4 q + i of a wave at [i][q]
+  __shared__ __attribute__((aligned(16))) float Cs[OUTPUT ? 2 : 1][OUTPUT ? kRows : 1][kStates];
+  __shared__ float parts[OUTPUT && G > 1 ? kRows : 1][G][OUTPUT && G > 1 ? kChannels : 1];
+  const int lane = int(threadIdx.x) % kWave, wave = int(threadIdx.x) / kWave;
+  const int group = wave % G, first_state = group * N;
+  const int32_t block_channel = int32_t(blockIdx.y) * kChannels, c = block_channel + wave / G * kWave + lane;
   const bool live = c < a.channels;
-  if (int32_t(blockIdx.x) >= a.chunks) {   // sequences without rows: their state passes through
+  const int32_t cc = min(c, a.channels - 1);   // lanes past the last channel compute it too and store nothing
+  if (int32_t(blockIdx.x) >= a.chunks) {       // sequences without rows: their state passes through
     const int32_t step = int32_t(gridDim.x) - a.chunks;
     for (int32_t s = int32_t(blockIdx.x) - a.chunks; s < a.seq.sequences; s += step) {
       const Span span = a.seq.span(s);
       if (span.begin < span.end || !live) continue;
-      for (int n = 0; n < a.dstate; ++n) {
+      for (int n = first_state; n < min(a.dstate, first_state + N); ++n) {
         const int64_t at = (int64_t(s) * a.channels + c) * a.dstate + n;
         a.h_final[at] = a.h0 != nullptr ? a.h0[at] : 0.f;
       }
@@ -93,88 +124,223 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(ScanKernelArgs a) {
       ++s;
     }
     const bool leaves = s < a.seq.sequences && span.begin < rows.end;
-    if (c == 0) a.resets[k] = !leaves || span.begin >= rows.begin;
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.resets[k] = !leaves || span.begin >= rows.begin;
     if (!leaves) return;
     from = max(from, span.begin);
   }
-  float A2[N], h[N], sum = 0.f;
+  float A2[N], sum = 0.f;
+  v4f h[N / 4];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    A2[n] = live && n < a.dstate ? a.A[int64_t(c) * a.dstate + n] * kLog2e : 0.f;
-    h[n] = 0.f;
+    A2[n] = first_state + n < a.dstate ? a.A[int64_t(cc) * a.dstate + first_state + n] * kLog2e : 0.f;
+    h[n / 4][n % 4] = 0.f;
   }
-  const float bias = live && a.delta_bias != nullptr ? a.delta_bias[c] : 0.f;
-  const float skip = OUTPUT && live && a.D != nullptr ? a.D[c] : 0.f;
-  const T* u = static_cast<const T*>(a.u);
-  const T* delta = static_cast<const T*>(a.delta);
-  const T* z = static_cast<const T*>(a.z);
+  const float bias = a.delta_bias != nullptr ? a.delta_bias[cc] : 0.f;
+  const float skip = OUTPUT && a.D != nullptr ? a.D[cc] : 0.f;
+  // the chunk's rows of u, delta, z and y; lanes past the last channel store nowhere
+  const int64_t base = int64_t(rows.begin) * a.channels;
+  const uint32_t pitch = uint32_t(a.channels) * sizeof(T), bytes = uint32_t(rows.end - rows.begin) * pitch;
+  const uint32_t at_lane = uint32_t(cc) * sizeof(T), store_lane = live ? at_lane : kOutOfRange;
+  const bool has_z = OUTPUT && a.z != nullptr;
+  const Rsrc ru = make_rsrc(static_cast<const T*>(a.u) + base, bytes), rd = make_rsrc(static_cast<const T*>(a.delta) + base, bytes);
+  const Rsrc rz = make_rsrc(static_cast<const T*>(has_z ? a.z : a.u) + base, bytes);
+  const Rsrc ry = make_rsrc(static_cast<T*>(a.y) + base, OUTPUT ? bytes : 0u);
   const T* B = static_cast<const T*>(a.B);
   const T* C = static_cast<const T*>(a.C);
-  T* y = static_cast<T*>(a.y);
 
   const auto enter = [&](int32_t row) {   // the state ahead of `row`, which is in sequence s
-    if (!live) return;
-    if (row == span.begin) {
+    if (row != span.begin && !(OUTPUT && k > 0)) return;   // (k is 0 here only with offsets out of order)
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        h[n] = a.h0 != nullptr && n < a.dstate ? a.h0[(int64_t(s) * a.channels + c) * a.dstate + n] : 0.f;
-    } else if (OUTPUT && k > 0) {   // (k is 0 here only with offsets out of order)
+    for (int n = 0; n < N; ++n) {
+      const int32_t state = first_state + n;
+      float v = 0.f;
+      if (state < a.dstate) {
+        if (row != span.begin) v = a.states[(int64_t(k - 1) * a.dstate + state) * a.channels + cc];
+        else if (a.h0 != nullptr) v = a.h0[(int64_t(s) * a.channels + cc) * a.dstate + state];
+      }
+      h[n / 4][n % 4] = v;
+    }
+  };
+  const auto leave = [&]() {
+    if (!OUTPUT || !live || a.h_final == nullptr) return;
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        h[n] = n < a.dstate ? a.states[(int64_t(k - 1) * a.dstate + n) * a.channels + c] : 0.f;
+    for (int n = 0; n < N; ++n)
+      if (first_state + n < a.dstate)
+        a.h_final[(int64_t(s) * a.channels + c) * a.dstate + first_state + n] = h[n / 4][n % 4];
+  };
+  // a row of B and C as a token needs it
+  struct Row { float b[N / 4]; v4f c[OUTPUT ? N / 4 : 1]; };
+  const auto read_row = [&](int buffer, int r) __attribute__((always_inline)) {
+    Row t;
+    __builtin_memcpy(t.b, __builtin_assume_aligned(&Bs[buffer][r][group][lane % 4][0], N), N);
+    if constexpr (OUTPUT) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) t.c[q] = *reinterpret_cast<const v4f*>(&Cs[buffer][r][first_state + 4 * q]);
+    }
+    return t;
+  };
+  // one token: d its step size, v its u; returns C . h
+  const auto token = [&](float d, float v, const Row& t) __attribute__((always_inline)) {
+    const float dv = d * v;
+    float out[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[q][i] *= __builtin_amdgcn_exp2f(d * A2[4 * q + i]);
+      h[q] = __builtin_amdgcn_mfma_f32_4x4x1f32(t.b[q], dv, h[q], 0, 0, 0);
+    }
+    if constexpr (OUTPUT) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = q == 0 ? t.c[q][i] * h[q][i] : fmaf(t.c[q][i], h[q][i], out[i]);
+      }
+    }
+    if constexpr (!OUTPUT) sum += d;
+    return (out[0] + out[1]) + (out[2] + out[3]);
+  };
+
+  // The values of a group of rows, loaded a group ahead (rows past the chunk: the last one's again)
+  struct Group { T u[kGroup], delta[kGroup], z[OUTPUT && G == 1 ? kGroup : 1]; };
+  const auto load_group = [&](int32_t row) {
+    Group g;
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) {
+      const uint32_t at = uint32_t(min(row + r, rows.end - 1) - rows.begin) * pitch;
+      g.u[r] = load_element<T>(ru, at_lane, at);
+      g.delta[r] = load_element<T>(rd, at_lane, at);
+      if constexpr (OUTPUT && G == 1) g.z[r] = load_element<T>(rz, at_lane, at);
+    }
+    return g;
+  };
+  // B and C of a tile of rows, by way of registers into one of the two buffers
+  float staged_b[kPer], staged_c[OUTPUT ? kPer : 1];
+  const auto load_tile = [&](int32_t tile) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
+      const bool some = r < kRows && tile + r < rows.end && n < a.dstate;
+      const int64_t at = int64_t(tile + r) * a.dstate + n;
+      staged_b[i] = some ? to_f32(B[at]) : 0.f;
+      if constexpr (OUTPUT) staged_c[i] = some ? to_f32(C[at]) : 0.f;
+    }
+  };
+  const auto put_tile = [&](int buffer) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
+      if (r < kRows) {
+        Bs[buffer][r][n / N][n % 4][n % N / 4] = staged_b[i];
+        if constexpr (OUTPUT) Cs[buffer][r][n] = staged_c[i];
+      }
+    }
+  };
+  // with G waves to a channel: the sum of a tile's parts, and y
+  const auto join = [&](int32_t tile, uint32_t walked) {
+    const int32_t cj = block_channel + int32_t(threadIdx.x) % kChannels;
+    if (cj >= a.channels) return;
+    const float skip_j = a.D != nullptr ? a.D[cj] : 0.f;
+    for (int r = int(threadIdx.x) / kChannels; r < kRows; r += G) {
+      if (!(walked >> r & 1u)) continue;
+      const uint32_t at = uint32_t(tile + r - rows.begin) * pitch + uint32_t(cj) * sizeof(T);
+      float out = skip_j * to_f32(load_element<T>(ru, at, 0));
+#pragma unroll
+      for (int g = 0; g < G; ++g) out += parts[r][g][int(threadIdx.x) % kChannels];
+      if (has_z) out *= silu<EXACT>(to_f32(load_element<T>(rz, at, 0)));
+      store_element(ry, at, 0, from_f32<T>(out));
     }
   };
   bool inside = false;
-  for (int32_t tile = from; tile < rows.end; tile += kRows) {
-    __syncthreads();
-    const int32_t count = min(kRows, rows.end - tile);
-    for (int i = threadIdx.x; i < kRows * N; i += kThreads) {
-      const int r = i / N, n = i % N;
-      const bool some = r < count && n < a.dstate;
-      Bs[r][n] = some ? to_f32(B[int64_t(tile + r) * a.dstate + n]) : 0.f;
-      if constexpr (OUTPUT) Cs[r][n] = some ? to_f32(C[int64_t(tile + r) * a.dstate + n]) : 0.f;
-    }
-    __syncthreads();
-    for (int r = 0; r < count; ++r) {
-      const int32_t row = tile + r;
-      while (s < a.seq.sequences && span.end <= row) {
-        if (++s < a.seq.sequences) span = a.seq.span(s);
-        inside = false;
-      }
-      if (s >= a.seq.sequences || row < span.begin) continue;
-      if (!inside) {
-        enter(row);
-        inside = true;
-      }
-      if (live) {
-        const int64_t at = int64_t(row) * a.channels + c;
-        float d = to_f32(delta[at]) + bias;
-        if (a.softplus) d = softplus(d);
-        const float v = to_f32(u[at]), dv = d * v;
-        float out = skip * v;
+  load_tile(from);
+  put_tile(0);
+  Group ahead = load_group(from);
+  int buffer = 0;
+  for (int32_t tile = from; tile < rows.end; tile += kRows, buffer ^= 1) {
+    __syncthreads();   // the tile is in LDS, and the buffer of the one before is free
+    const bool more = tile + kRows < rows.end;
+    if (more) load_tile(tile + kRows);
+    uint32_t walked = 0;   // the tile's rows that are in a sequence
+#pragma unroll 1
+    for (int part = 0; part < kRows && tile + part < rows.end; part += kGroup) {
+      const int32_t row0 = tile + part;
+      const Group now = ahead;
+      if (row0 + kGroup < rows.end) ahead = load_group(row0 + kGroup);
+      float d[kGroup], v[kGroup], gate[OUTPUT ? kGroup : 1];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], dv * Bs[r][n]);
-          if constexpr (OUTPUT) out = fmaf(Cs[r][n], h[n], out);
+      for (int r = 0; r < kGroup; ++r) {
+        v[r] = to_f32(now.u[r]);
+        d[r] = to_f32(now.delta[r]) + bias;
+        if constexpr (OUTPUT) gate[r] = 1.f;
+      }
+      if (a.softplus) {
+#pragma unroll
+        for (int r = 0; r < kGroup; ++r) d[r] = softplus<EXACT>(d[r]);
+      }
+      if constexpr (OUTPUT && G == 1) {
+        if (has_z) {
+#pragma unroll
+          for (int r = 0; r < kGroup; ++r) gate[r] = silu<EXACT>(to_f32(now.z[r]));
         }
-        sum += d;
-        if constexpr (OUTPUT) y[at] = from_f32<T>(z != nullptr ? gated(out, to_f32(z[at])) : out);
       }
-      if (OUTPUT && live && row + 1 == span.end && a.h_final != nullptr) {
+      const auto row_of = [&](int r, float dr, float vr, float gr, const Row& t) __attribute__((always_inline)) {
+        const float read = token(dr, vr, t);
+        if constexpr (OUTPUT && G == 1)
+          store_element(ry, store_lane, uint32_t(row0 + r - rows.begin) * pitch, from_f32<T>(fmaf(skip, vr, read) * gr));
+        if constexpr (OUTPUT && G > 1) parts[part + r][group][wave / G * kWave + lane] = read;
+      };
+      if (inside && row0 + kGroup <= min(span.end, rows.end)) {
+        Row t = read_row(buffer, part);
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (n < a.dstate) a.h_final[(int64_t(s) * a.channels + c) * a.dstate + n] = h[n];
+        for (int r = 0; r < kGroup; ++r) {
+          const Row next = read_row(buffer, part + (r + 1 < kGroup ? r + 1 : r));
+          row_of(r, d[r], v[r], gate[OUTPUT ? r : 0], t);
+          t = next;
+        }
+        walked |= ((1u << kGroup) - 1u) << part;
+        if (row0 + kGroup == span.end) leave();
+        continue;
+      }
+#pragma unroll 1
+      for (int r = 0; r < kGroup && row0 + r < rows.end; ++r) {   // where sequences begin or end
+        const int32_t row = row0 + r;
+        while (s < a.seq.sequences && span.end <= row) {
+          if (++s < a.seq.sequences) span = a.seq.span(s);
+          inside = false;
+        }
+        if (s >= a.seq.sequences || row < span.begin) continue;
+        if (!inside) {
+          enter(row);
+          inside = true;
+        }
+        float dr = d[0], vr = v[0], gr = gate[0];
+#pragma unroll
+        for (int i = 1; i < kGroup; ++i) {
+          dr = r == i ? d[i] : dr;
+          vr = r == i ? v[i] : vr;
+          if constexpr (OUTPUT) gr = r == i ? gate[i] : gr;
+        }
+        row_of(r, dr, vr, gr, read_row(buffer, part + r));
+        walked |= 1u << (part + r);
+        if (row + 1 == span.end) leave();
       }
     }
+    if constexpr (OUTPUT && G > 1) {
+      __syncthreads();
+      join(tile, walked);
+    }
+    if (more) put_tile(buffer ^ 1);
   }
   if constexpr (!OUTPUT) {
     if (!live) return;
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (n < a.dstate) a.states[(int64_t(k) * a.dstate + n) * a.channels + c] = h[n];
-    a.sums[int64_t(k) * a.channels + c] = sum;
+      if (first_state + n < a.dstate)
+        a.states[(int64_t(k) * a.dstate + first_state + n) * a.channels + c] = h[n / 4][n % 4];
+    if (group == 0) a.sums[int64_t(k) * a.channels + c] = sum;
   }
 }
+
+constexpr int kCarried = 8;
 
 // chunk by chunk along every chain (a dense sequence, or all packed rows), one thread per channel and state
 __global__ void __launch_bounds__(kThreads) carry_kernel(ScanKernelArgs a) {
@@ -184,13 +350,25 @@ __global__ void __launch_bounds__(kThreads) carry_kernel(ScanKernelArgs a) {
   const float A2 = a.A[int64_t(c) * a.dstate + n] * kLog2e;
   for (int32_t first = int32_t(blockIdx.z) * a.per_sequence; first < a.chunks;
        first += int32_t(gridDim.z) * a.per_sequence) {
-    const int32_t last = first + a.per_sequence - 1;
+    const int32_t last = first + a.per_sequence - 1;   // nothing enters a chain's first chunk; nothing reads its last's
+    const int64_t pitch = int64_t(a.dstate) * a.channels;
+    float* at = a.states + (int64_t(first) * a.dstate + n) * a.channels + c;
     float h = 0.f;
-    for (int32_t k = first; k < last; ++k) {   // nothing enters a chain's first chunk; nothing reads what leaves its last
-      float* at = a.states + (int64_t(k) * a.dstate + n) * a.channels + c;
-      const float own = *at;
-      h = a.resets[k] ? own : fmaf(__builtin_amdgcn_exp2f(a.sums[int64_t(k) * a.channels + c] * A2), h, own);
-      *at = h;
+    for (int32_t k = first; k < last; k += kCarried, at += kCarried * pitch) {   // loads of several chunks at a time
+      float own[kCarried], sum[kCarried];
+      int32_t reset[kCarried];
+#pragma unroll
+      for (int i = 0; i < kCarried; ++i) {
+        const int32_t j = min(k + i, last - 1);
+        own[i] = at[(j - k) * pitch];
+        sum[i] = a.sums[int64_t(j) * a.channels + c];
+        reset[i] = a.resets[j];
+      }
+#pragma unroll
+      for (int i = 0; i < kCarried; ++i) {
+        h = reset[i] ? own[i] : fmaf(__builtin_amdgcn_exp2f(sum[i] * A2), h, own[i]);
+        if (k + i < last) at[i * pitch] = h;
+      }
     }
   }
 }
@@ -210,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(float* __restrict__ stat
     const int64_t s = item / channels;
     const int32_t c = int32_t(item - s * channels);
     float d = to_f32(delta[item]) + (delta_bias != nullptr ? delta_bias[c] : 0.f);
-    if (use_softplus) d = softplus(d);
+    if (use_softplus) d = softplus<sizeof(T) == 4>(d);
     const float v = to_f32(u[item]), dv = d * v;
     float out = 0.f;
 #pragma unroll
@@ -226,62 +404,79 @@ __global__ void __launch_bounds__(kThreads) step_kernel(float* __restrict__ stat
     for (int k = 1; k < lanes; k <<= 1) out += __shfl_xor(out, k);
     if (threadIdx.x % lanes == 0) {
       if (D != nullptr) out = fmaf(D[c], v, out);
-      y[item] = from_f32<T>(z != nullptr ? gated(out, to_f32(z[item])) : out);
+      y[item] = from_f32<T>(z != nullptr ? out * silu<sizeof(T) == 4>(to_f32(z[item])) : out);
     }
   }
 }
 
 // ---- host ----
 
-constexpr int32_t kChunk = 256;
-
 struct Plan {
   int32_t chunk, per_sequence, chunks;
   size_t sums, resets, bytes;   // byte offsets behind the states, and the total
 };
 
+constexpr int64_t kSimds = 1024;   // of a whole chip; the workspace's size does not depend on the device
+
+constexpr int state_groups(int32_t dstate) { return dstate <= 16 ? 1 : dstate <= 32 ? 2 : 4; }
+
+// How long a chunk is.  Where the sequences and channels alone give every SIMD a wave they are walked whole, in one pass.
+// Otherwise the walk is made twice, in as many chunks as fill the three waves that a SIMD holds an even number of times; a
+// chunk has 32 to 256 rows (carried states are traffic, and the sum of d is kept precise).
 bool make_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed, Plan* p) {
-  p->chunk = kChunk;
-  const int64_t length = packed ? tokens : tokens / sequences;
-  const int64_t per = (length + p->chunk - 1) / p->chunk, chunks = packed ? per : per * sequences;
+  const int64_t length = packed ? tokens : tokens / sequences, chains = packed ? 1 : sequences;
+  const int64_t waves = chains * ((int64_t(channels) + kWave - 1) / kWave) * state_groups(dstate);
+  const bool reach = length * channels < (int64_t(1) << 29);   // a chunk's rows are addressed in 32 bits
+  int64_t chunk = std::max<int64_t>(length, 1);
+  if (waves < kSimds || !reach) {
+    const int64_t least = (length + 255) / 256, rounds = (least * waves + 3 * kSimds - 1) / (3 * kSimds);
+    const int64_t number = std::max(least, rounds * 3 * kSimds / waves);
+    chunk = number > 0 ? (length + number - 1) / number : 1;
+    chunk = std::min<int64_t>(256, std::max<int64_t>(32, (chunk + kGroup - 1) / kGroup * kGroup));
+  }
+  const int64_t per = (length + chunk - 1) / chunk, chunks = per * chains;
   if (chunks >= int64_t(1) << 23) return false;   // a grid's threads along x in 32 bits
+  p->chunk = int32_t(chunk);
   p->per_sequence = int32_t(per);
   p->chunks = int32_t(chunks);
   const double need = double(chunks) * channels * (dstate + 1) * 4.0;
   if (need >= double(int64_t(1) << 40)) return false;
   const auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
-  p->sums = round(size_t(chunks) * dstate * channels * 4);
-  p->resets = p->sums + round(size_t(chunks) * channels * 4);
-  p->bytes = std::max<size_t>(256, p->resets + round(size_t(chunks) * 4));
+  const size_t carried = per > 1 ? size_t(chunks) : 0;
+  p->sums = round(carried * dstate * channels * 4);
+  p->resets = p->sums + round(carried * channels * 4);
+  p->bytes = std::max<size_t>(256, p->resets + round(carried * 4));
   return true;
 }
 
-template <typename T, int N>
+template <typename T, int N, int G>
 hipError_t launch_states(const ScanKernelArgs& a, hipStream_t stream) {
-  const uint32_t blocks = uint32_t((a.channels + kThreads - 1) / kThreads);
-  // grid.x: the chunks, and where packed sequences may have no rows some blocks that look for those
+  const uint32_t blocks = uint32_t((a.channels + kThreads / G - 1) / (kThreads / G));
+  // grid.x: the chunks, and where sequences may have no rows some blocks that look for those
   const bool empty = a.h_final != nullptr && (a.seq.offsets != nullptr || a.seq.tokens == 0);
   const uint32_t extra = empty ? uint32_t(std::min(a.seq.sequences, 64)) : 0u;
   if (a.per_sequence > 1) {
-    chunk_kernel<T, N, false><<<dim3(a.chunks, blocks), kThreads, 0, stream>>>(a);
+    chunk_kernel<T, N, G, false><<<dim3(a.chunks, blocks), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const uint32_t chains = uint32_t(std::min(a.chunks / a.per_sequence, 32768));
-    carry_kernel<<<dim3(blocks, a.dstate, chains), kThreads, 0, stream>>>(a);
+    carry_kernel<<<dim3((a.channels + kThreads - 1) / kThreads, a.dstate, chains), kThreads, 0, stream>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.chunks + extra == 0) return hipSuccess;
-  chunk_kernel<T, N, true><<<dim3(a.chunks + extra, blocks), kThreads, 0, stream>>>(a);
+  chunk_kernel<T, N, G, true><<<dim3(a.chunks + extra, blocks), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_scan(const ScanKernelArgs& a, hipStream_t stream) {
-  if (a.dstate <= 8) return launch_states<T, 8>(a, stream);
-  if (a.dstate <= 16) return launch_states<T, 16>(a, stream);
-  if (a.dstate <= 32) return launch_states<T, 32>(a, stream);
-  return launch_states<T, 64>(a, stream);
+  if (a.dstate <= 8) return launch_states<T, 8, 1>(a, stream);
+  switch (state_groups(a.dstate)) {
+    case 1: return launch_states<T, 16, 1>(a, stream);
+    case 2: return launch_states<T, 16, 2>(a, stream);
+    default: return launch_states<T, 16, 4>(a, stream);
+  }
 }
 
 template <typename T>
