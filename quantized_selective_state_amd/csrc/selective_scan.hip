@@ -373,39 +373,75 @@ __global__ void __launch_bounds__(kThreads) carry_kernel(ScanKernelArgs a) {
   }
 }
 
+// Up to four neighbouring elements at any alignment; those past `count` are 0.
 template <typename T>
+__device__ __forceinline__ void load_four(const T* __restrict__ p, int count, float (&v)[4]) {
+  struct { T e[4]; } raw = {};
+  if (count >= 4) {
+    __builtin_memcpy(&raw, p, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) raw.e[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = to_f32(raw.e[i]);
+}
+
+// One token for every sequence.  HBM-bound by the states: `lanes` neighbouring lanes take a channel, four states each, and
+// K sequences one after another, whose loads are all under way together and share A.
+template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) step_kernel(float* __restrict__ state, const T* __restrict__ u,
                                                         const T* __restrict__ delta, const float* __restrict__ A,
                                                         const T* __restrict__ B, const T* __restrict__ C,
                                                         const float* __restrict__ D, const T* __restrict__ z,
                                                         const float* __restrict__ delta_bias, T* __restrict__ y,
-                                                        int64_t items, int32_t channels, int32_t dstate, int32_t lanes,
-                                                        bool use_softplus) {
-  // `lanes` neighbouring lanes per channel, four states each
-  const int64_t step = int64_t(gridDim.x) * (kThreads / lanes);
-  const int first = int(threadIdx.x % lanes) * 4, count = dstate - first;
-  for (int64_t item = int64_t(blockIdx.x) * (kThreads / lanes) + threadIdx.x / lanes; item < items; item += step) {
-    const int64_t s = item / channels;
-    const int32_t c = int32_t(item - s * channels);
-    float d = to_f32(delta[item]) + (delta_bias != nullptr ? delta_bias[c] : 0.f);
-    if (use_softplus) d = softplus<sizeof(T) == 4>(d);
-    const float v = to_f32(u[item]), dv = d * v;
+                                                        int32_t batch, int32_t channels, int32_t dstate, int32_t lanes,
+                                                        int32_t channel_blocks, bool use_softplus) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  const int32_t s0 = int32_t(blockIdx.x) / channel_blocks * K;
+  const int32_t c0 = int32_t(blockIdx.x) % channel_blocks * (kThreads / lanes) + int32_t(threadIdx.x) / lanes;
+  const bool live = c0 < channels;   // (all lanes of a channel are, or none: the others keep the sums' lanes filled)
+  const int32_t c = min(c0, channels - 1);
+  const int first = int(threadIdx.x) % lanes * 4, count = dstate - first;
+  float a[4], h[K][4], b[K][4], cs[K][4], d[K], v[K], gate[K];
+  load_four(A + int64_t(c) * dstate + first, count, a);
+  const float bias = delta_bias != nullptr ? delta_bias[c] : 0.f, skip = D != nullptr ? D[c] : 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t s = min(s0 + k, batch - 1), at = s * channels + c;
+    load_four(state + at * dstate + first, count, h[k]);
+    d[k] = to_f32(delta[at]) + bias;
+    v[k] = to_f32(u[at]);
+    gate[k] = z != nullptr ? to_f32(z[at]) : 0.f;
+    load_four(B + s * dstate + first, count, b[k]);
+    load_four(C + s * dstate + first, count, cs[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (s0 + k >= batch) break;
+    const int64_t at = int64_t(s0 + k) * channels + c;
+    if (use_softplus) d[k] = softplus<EXACT>(d[k]);
     float out = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i < count) {
-        const int n = first + i;
-        float* at = state + item * dstate + n;
-        const float h = fmaf(__builtin_amdgcn_exp2f(d * A[int64_t(c) * dstate + n] * kLog2e), *at, dv * to_f32(B[s * dstate + n]));
-        *at = h;
-        out = fmaf(to_f32(C[s * dstate + n]), h, out);
+      h[k][i] = fmaf(__builtin_amdgcn_exp2f(d[k] * a[i] * kLog2e), h[k][i], d[k] * v[k] * b[k][i]);
+      out = i < count ? fmaf(cs[k][i], h[k][i], out) : out;
+    }
+    if (live) {
+      float* to = state + at * dstate + first;
+      if (count >= 4) {
+        __builtin_memcpy(to, h[k], 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < count) to[i] = h[k][i];
       }
     }
-    for (int k = 1; k < lanes; k <<= 1) out += __shfl_xor(out, k);
-    if (threadIdx.x % lanes == 0) {
-      if (D != nullptr) out = fmaf(D[c], v, out);
-      y[item] = from_f32<T>(z != nullptr ? out * silu<sizeof(T) == 4>(to_f32(z[item])) : out);
-    }
+    for (int n = 1; n < lanes; n <<= 1) out += __shfl_xor(out, n);
+    out = fmaf(skip, v[k], out);
+    if (z != nullptr) out *= silu<EXACT>(gate[k]);
+    if (live && first == 0) y[at] = from_f32<T>(out);
   }
 }
 
@@ -485,12 +521,16 @@ hipError_t launch_step(float* state, const void* u, const void* delta, const flo
                        int32_t dstate, bool softplus, hipStream_t stream) {
   int32_t lanes = 1;
   while (lanes * 4 < dstate) lanes *= 2;
-  const int64_t items = int64_t(batch) * channels, per = kThreads / lanes;
-  const int64_t blocks = std::min<int64_t>((items + per - 1) / per, 1 << 20);
-  step_kernel<T><<<dim3(uint32_t(blocks)), kThreads, 0, stream>>>(
-      state, static_cast<const T*>(u), static_cast<const T*>(delta), A, static_cast<const T*>(B),
-      static_cast<const T*>(C), D, static_cast<const T*>(z), delta_bias, static_cast<T*>(y), items, channels, dstate,
-      lanes, softplus);
+  const int32_t channel_blocks = (channels + kThreads / lanes - 1) / (kThreads / lanes);
+  // four sequences a lane once they leave a block for every compute unit
+  const bool many = int64_t(channel_blocks) * (batch / 4) >= 256;
+  const int64_t blocks = int64_t(channel_blocks) * (many ? (batch + 3) / 4 : batch);
+  if (blocks >= int64_t(1) << 24) return hipErrorInvalidValue;   // (the limit on batch * channels keeps below it)
+  const dim3 grid = dim3(uint32_t(blocks));
+  const T *in = static_cast<const T*>(u), *steps = static_cast<const T*>(delta), *gate = static_cast<const T*>(z);
+  const T *b = static_cast<const T*>(B), *c = static_cast<const T*>(C);
+  if (many) step_kernel<T, 4><<<grid, kThreads, 0, stream>>>(state, in, steps, A, b, c, D, gate, delta_bias, static_cast<T*>(y), batch, channels, dstate, lanes, channel_blocks, softplus);
+  else step_kernel<T, 1><<<grid, kThreads, 0, stream>>>(state, in, steps, A, b, c, D, gate, delta_bias, static_cast<T*>(y), batch, channels, dstate, lanes, channel_blocks, softplus);
   return hipGetLastError();
 }
 

@@ -13,17 +13,17 @@ def silu(v):
 
 def norm(x, weight, residual=None, gate=None, groups=1, eps=1e-5):
     """(n, v, bound of n)."""
-    v, extra = x, 1.0                                  # roundings of v
+    v, extra = x, np.ones_like(x)                      # roundings of v
     if residual is not None:
         v = x + residual
-    if gate is not None:
-        v, extra = x * silu(gate), 10.0                # exp within 3, 1 + e, the reciprocal within 2, two products
+    if gate is not None:                               # exp within |z| + 3, 1 + e, the reciprocal within 2, two products
+        v, extra = x * silu(gate), 8.0 + np.abs(gate)
     parts = v.reshape(v.shape[0], groups, -1)
     n = parts / np.sqrt((parts ** 2).mean(-1, keepdims=True) + eps)
     n = n.reshape(v.shape) * weight
     # The sum of squares: up to 64 of them one after another in a lane, then 10 levels of halves and 16 waves; a squared
     # v carries its roundings twice, and the root halves all of it.  Then mean, root and quotient, and two products.
-    return n, v, np.abs(n) * E * (extra + (64 + 10 + 16 + 2 * extra) / 2 + 3 + 2)
+    return n, v, np.abs(n) * E * (extra + (64 + 10 + 16 + 2 * extra.max()) / 2 + 3 + 2)
 
 
 def row_scale(most):
@@ -89,8 +89,8 @@ def scan(u, delta, A, B, C, D, z, delta_bias, h0, sequences, offsets, positive=T
     raw = delta + (0.0 if delta_bias is None else delta_bias)
     d = softplus(raw) if positive else raw
     # d: the sum with the bias rounded once, moved on by a slope of at most 1 (but relatively never more than |raw| times);
-    # then the exponential, the logarithm or its series and the sum, 8 roundings of d
-    wrong_d = E * (np.abs(raw) * np.minimum(1.0, np.abs(d) if positive else 1.0) + 8 * np.abs(d))
+    # then exp(-|raw|), which may be off by |raw| + 3, and log(1 + that), of at most its size, within 5 more
+    wrong_d = E * (2 * np.abs(raw) * np.minimum(1.0, np.abs(d) if positive else 1.0) + 8 * np.abs(d))
     for s, (lo, hi) in enumerate(spans(sequences, tokens, offsets)):
         h, size, wrong = final[s].copy(), np.abs(final[s]), np.zeros((channels, n))
         for t in range(lo, hi):
@@ -115,7 +115,7 @@ def scan(u, delta, A, B, C, D, z, delta_bias, h0, sequences, offsets, positive=T
             if z is not None:
                 g = silu(z[t])
                 y[t] = read * g
-                wrong_y[t] = wrong_read * np.abs(g) + np.abs(y[t]) * 10 * E
+                wrong_y[t] = wrong_read * np.abs(g) + np.abs(y[t]) * (np.abs(z[t]) + 10) * E   # exp within |z| + 3
             else:
                 y[t], wrong_y[t] = read, wrong_read
         final[s] = h
