@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
   }
 }
 
-constexpr int kCarried = 8;
+constexpr int kCarried = 16;
 
 // chunk by chunk along every chain (a dense sequence, or all packed rows), one thread per channel and state
 __global__ void __launch_bounds__(kThreads) carry_kernel(ScanKernelArgs a) {
