@@ -76,7 +76,7 @@ def _code_buffers(x, scale, out):
     _some_channels(x, "x")
     codes, row_scale = (None, None) if out is None else out
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.int8)
     else:
         _expect(codes, "codes", torch.int8, x.shape, x.device)
     if scale is not None:
@@ -85,7 +85,7 @@ def _code_buffers(x, scale, out):
         _expect(scale, "scale", torch.float32, (1,), x.device)
         return codes, None, scale
     if row_scale is None:
-        row_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        row_scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     else:
         _expect(row_scale, "scale of out", torch.float32, x.shape[:-1], x.device)
     return codes, row_scale, None
@@ -161,7 +161,7 @@ def dequantize_rows(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype
     _expect(codes, "codes", torch.int8, codes.shape, codes.device)
     _expect(scale, "scale", torch.float32, codes.shape[:-1], codes.device)
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        out = torch.empty_like(codes, dtype=dtype)
     else:
         _expect(out, "out", dtype, codes.shape, codes.device)
     _call(lib.ssdq_dequantize_rows, "ssdq_dequantize_rows", codes.device, _element_type(out, "out"), _at(codes),
@@ -191,7 +191,7 @@ def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
     _expect(b_scale, "b_scale", torch.float32, (n,), dev)
     _expect(bias, "bias", torch.float32, (n,), dev, optional=True)
     if out is None:
-        out = torch.empty((*a.shape[:-1], n), dtype=dtype, device=dev)
+        out = a.new_empty((*a.shape[:-1], n), dtype=dtype)
     else:
         _expect(out, "out", dtype, (*a.shape[:-1], n), dev)
     _call(lib.ssdq_matmul_i8, "ssdq_matmul_i8", dev, _element_type(out, "out"), _at(a), _at(a_scale), int(per_row), _at(b),
@@ -251,7 +251,7 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None
     if state_out is not None:
         _expect(state_out, "state_out", x.dtype, states, dev)
     elif want_final_state and width > 1:
-        state_out = torch.empty(states, dtype=x.dtype, device=dev)
+        state_out = x.new_empty(states)
     _call(lib.ssdq_causal_conv, "ssdq_causal_conv", dev, dtype, _at(x), _at(weight), _at(bias), _at(state), _at(offsets),
           _at(out), _at(state_out), sequences, tokens, channels, width, int(silu))
     return out, state_out
@@ -328,12 +328,12 @@ def selective_scan(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
     if h_final is not None:
         _expect(h_final, "h_final", torch.float32, states, dev)
     elif want_final_state:
-        h_final = torch.empty(states, dtype=torch.float32, device=dev)
+        h_final = u.new_empty(states, dtype=torch.float32)
     need = selective_scan_workspace_size(sequences, tokens, channels, dstate, offsets is not None)
     if need == 0:
         raise SSDQError(SSDQ_ERROR_UNSUPPORTED, "ssdq_selective_scan")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = u.new_empty(need, dtype=torch.uint8)
     else:
         _need(workspace, "workspace", torch.uint8, None, dev)
     _call(lib.ssdq_selective_scan, "ssdq_selective_scan", dev, dtype, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(D),

@@ -5,6 +5,18 @@
 
 #include "block_internal.h"
 
+namespace ssdq {
+
+int32_t compute_units() {
+  int device = 0, count = 0;
+  if (hipGetDevice(&device) != hipSuccess ||
+      hipDeviceGetAttribute(&count, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || count <= 0)
+    return 256;
+  return count;
+}
+
+}  // namespace ssdq
+
 using namespace ssdq;
 
 namespace {

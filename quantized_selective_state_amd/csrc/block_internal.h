@@ -5,6 +5,9 @@
 
 namespace ssdq {
 
+// Compute units of the current device.
+int32_t compute_units();
+
 // ssdq_rms_norm, ssdq_quantize_rows after validation (weight null: no norm).
 struct NormArgs {
   int32_t dtype, residual_dtype;

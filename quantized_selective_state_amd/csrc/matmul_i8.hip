@@ -467,18 +467,11 @@ __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restric
   }
 }
 
-// the device's, a multiple of the 8 XCDs
-int32_t compute_units() {
-  int device = 0, count = 256;
-  if (hipGetDevice(&device) == hipSuccess)
-    (void)hipDeviceGetAttribute(&count, hipDeviceAttributeMultiprocessorCount, device);
-  return std::max(8, count / 8 * 8);
-}
-
 template <int TM, int TN>
 TileArgs tile_args(const MatmulArgs& a, const Epilogue& ep, int per_unit, uint32_t* blocks) {
   const uint32_t m_tiles = uint32_t((a.m + TM - 1) / TM), n_tiles = uint32_t((int64_t(a.n) + TN - 1) / TN);
-  *blocks = std::min(m_tiles * n_tiles, uint32_t(compute_units() * per_unit));
+  const int32_t units = std::max(8, compute_units() / 8 * 8);   // the same number on every XCD
+  *blocks = std::min(m_tiles * n_tiles, uint32_t(units * per_unit));
   return TileArgs{a.a, a.b, ep, a.m, a.k, a.n, m_tiles, n_tiles};
 }
 
@@ -523,7 +516,7 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   // Few tokens: up to 8 the tokens' bytes are nothing beside the weights'; up to 32 where tiles of 64 channels would leave
   // half of the compute units idle (16 x 8192 x 4096: 11.0 us against 20.5; 16 x 4096 x 18560: 23.2 against 20.9).
   const bool narrow = (int64_t(a.n) + 63) / 64 * 2 <= compute_units();
-  if (a.m <= 8 || (a.m <= 16 && narrow)) return launch_stream<T, 1, 1>(a, ep, stream);
+  if ((a.m <= 8 && a.n <= 1 << 24) || (a.m <= 16 && narrow)) return launch_stream<T, 1, 1>(a, ep, stream);
   if (a.m <= 32 && narrow) return launch_stream<T, 2, 1>(a, ep, stream);
   switch (choose(a)) {
     case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(a, ep, kCandidates[0].per_unit, stream);

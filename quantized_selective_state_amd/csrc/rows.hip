@@ -231,13 +231,6 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __re
   }
 }
 
-int32_t multiprocessors() {
-  int device = 0, cus = 256;
-  if (hipGetDevice(&device) == hipSuccess)
-    (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
-  return cus > 0 ? cus : 256;
-}
-
 int32_t power_of_two(int32_t n) {
   int32_t p = 1;
   while (p < n) p <<= 1;
@@ -275,7 +268,7 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   a.per_block = threads >= 256 ? 1 : 256 / threads;
   const int32_t block = (threads * a.per_block + kWave - 1) / kWave * kWave;
   const int64_t items = (a.rows + a.per_block - 1) / a.per_block;
-  const int64_t most = int64_t(multiprocessors()) * (2048 / block);
+  const int64_t most = int64_t(compute_units()) * (2048 / block);
   const dim3 grid(uint32_t(items < most ? items : most));
   const int32_t slots = (packs + a.lanes - 1) / a.lanes;
   if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1, PAST><<<grid, block, 0, stream>>>(a);
@@ -314,7 +307,7 @@ hipError_t launch_values(const int8_t* codes, const float* scale, void* x, int64
                          hipStream_t stream) {
   const int32_t packs = int32_t((int64_t(channels) + V - 1) / V);
   const int32_t lanes = packs >= 256 ? 256 : power_of_two(packs);
-  const int64_t items = (rows + 256 / lanes - 1) / (256 / lanes), most = int64_t(multiprocessors()) * 16;
+  const int64_t items = (rows + 256 / lanes - 1) / (256 / lanes), most = int64_t(compute_units()) * 16;
   const dim3 grid(uint32_t(items < most ? items : most));
   T* to = static_cast<T*>(x);
   if (rows * channels * int64_t(1 + sizeof(T)) > kInfinityCache)
