@@ -192,14 +192,18 @@ struct Loader {
   const Walk<TM, TN>& walk;
   int wave;
   uint32_t tile, piece, row_at;
-  int32_t slab, first, left, slabs;
+  int32_t slab, low, high, first, left, slabs;   // slabs [low, high) of a tile, from `first` on and round
   Rsrc ra, rb;
-  __device__ __forceinline__ Loader(const TileArgs& a, const Walk<TM, TN>& walk, int lane, int wave)
+  // part `group` of `groups` equal ones of the slabs (the last may end in slabs past k, which load as zero)
+  __device__ __forceinline__ Loader(const TileArgs& a, const Walk<TM, TN>& walk, int lane, int wave, int group, int groups)
       : a(a), walk(walk), wave(wave), tile(blockIdx.x / 8), piece(place_of_piece(lane / kPieces, lane % kPieces) * 16),
-        row_at((uint32_t(wave) * kRows + lane / kPieces) * uint32_t(a.k)), slabs((a.k + kSlab - 1) / kSlab) {
+        row_at((uint32_t(wave) * kRows + lane / kPieces) * uint32_t(a.k)),
+        slabs(((a.k + kSlab - 1) / kSlab + groups - 1) / groups) {
+    low = group * slabs;
+    high = low + slabs;
     // XCDs begin at different slabs: rows of many codes are often a power of two apart, and the same line of all rows
     // would lie in few of the memory's channels.
-    first = int32_t(blockIdx.x % 8) * slabs / 8;
+    first = low + int32_t(blockIdx.x % 8) * slabs / 8;
     aim();
   }
   __device__ __forceinline__ void aim() {
@@ -222,7 +226,7 @@ struct Loader {
     for (int i = 0; i < LA; ++i) load_to_lds(ra, to + i * kWaves * 1024, from + i * step);
 #pragma unroll
     for (int i = 0; i < LB; ++i) load_to_lds(rb, to + TM * kSlab + i * kWaves * 1024, from + i * step);
-    if (++slab == slabs) slab = 0;
+    if (++slab == high) slab = low;
     if (--left == 0) {
       tile += walk.stride;
       aim();
@@ -363,22 +367,26 @@ struct Store {
   }
 };
 
-// WM x WN waves, kStages slabs in LDS.  Between two barriers every wave reads a slab's operands and multiplies them.
-template <typename T, int TM, int TN, int WM, int WN, int kStages>
-__global__ void __launch_bounds__(WM * WN * kWave) tile_kernel(TileArgs args, T* __restrict__ out) {
+// WM x WN waves, kStages slabs in LDS.  Between two barriers every wave reads a slab's operands and multiplies them.  With
+// kSplit 2 there are twice the waves, and the halves of them walk half of the inner axis each: two waves on every SIMD for
+// tiles that are too few to give a compute unit a second one.
+template <typename T, int TM, int TN, int WM, int WN, int kStages, int kSplit>
+__global__ void __launch_bounds__(WM * WN * kSplit * kWave) tile_kernel(TileArgs args, T* __restrict__ out) {
   constexpr int kWaves = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
   typedef Loader<TM, TN, kWaves> Load;
   typedef Store<T, FM, FN> Put;
   constexpr int kAhead = (kStages - 2) * Load::kLoads;
   constexpr int kAheadStored = kAhead + Put::kStores < 63 ? kAhead + Put::kStores : 63;
-  __shared__ __attribute__((aligned(16))) int8_t lds[kStages][(TM + TN) * kSlab];
+  __shared__ __attribute__((aligned(16))) int8_t lds[kSplit][kStages][(TM + TN) * kSlab];
   __shared__ __attribute__((aligned(16))) int8_t results[kWaves][Put::kRoom];
-  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  __shared__ v4i sums[kSplit > 1 ? kWaves : 1][kSplit > 1 ? FM * FN : 1][kWave];
+  const int lane = threadIdx.x % kWave, of_block = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const int group = of_block / kWaves, wave = of_block % kWaves;
   const Walk<TM, TN> walk(args);
-  Load load(args, walk, lane, wave);
+  Load load(args, walk, lane, wave, group, kSplit);
   const int wm = (wave % WM) * (TM / WM), wn = (wave / WM) * (TN / WN);
 #pragma unroll
-  for (int i = 0; i + 1 < kStages; ++i) load(lds[i]);
+  for (int i = 0; i + 1 < kStages; ++i) load(lds[group][i]);
   int stage = 0;
   bool stored = false;   // whether the newest operations in memory are the stores of a whole tile
   for (uint32_t t = blockIdx.x / 8; t < walk.run; t += walk.stride) {
@@ -390,11 +398,26 @@ __global__ void __launch_bounds__(WM * WN * kWave) tile_kernel(TileArgs args, T*
       if (stored && slab < kStages - 1) wait_loads<kAheadStored>();
       else wait_loads<kAhead>();
       barrier();
-      load(lds[stage == 0 ? kStages - 1 : stage - 1]);
+      load(lds[group][stage == 0 ? kStages - 1 : stage - 1]);
       Operands<FM, FN> o;
-      o.read(lds[stage] + wm * kSlab, lds[stage] + (TM + wn) * kSlab, lane);
+      o.read(lds[group][stage] + wm * kSlab, lds[group][stage] + (TM + wn) * kSlab, lane);
       o.multiply(acc);
       stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if constexpr (kSplit > 1) {
+      if (group == 1) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int i = 0; i < FM; ++i) sums[wave][j * FM + i][lane] = acc[j][i];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      barrier();
+      if (group == 1) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[j][i] += sums[wave][j * FM + i][lane];
     }
     int64_t m0;
     int32_t n0;
@@ -476,11 +499,11 @@ TileArgs tile_args(const MatmulArgs& a, const Epilogue& ep, int per_unit, uint32
 }
 
 // `per_unit` blocks on a compute unit
-template <typename T, int TM, int TN, int WM, int WN, int kStages>
+template <typename T, int TM, int TN, int WM, int WN, int kStages, int kSplit = 1>
 hipError_t launch_tiles(const MatmulArgs& a, const Epilogue& ep, int per_unit, hipStream_t stream) {
   uint32_t blocks;
   const TileArgs args = tile_args<TM, TN>(a, ep, per_unit, &blocks);
-  tile_kernel<T, TM, TN, WM, WN, kStages><<<dim3(blocks), WM * WN * kWave, 0, stream>>>(args, static_cast<T*>(a.out));
+  tile_kernel<T, TM, TN, WM, WN, kStages, kSplit><<<dim3(blocks), WM * WN * kSplit * kWave, 0, stream>>>(args, static_cast<T*>(a.out));
   return hipGetLastError();
 }
 
@@ -522,8 +545,13 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(a, ep, kCandidates[0].per_unit, stream);
     case 1: return launch_tiles<T, 128, 128, 2, 2, 2>(a, ep, kCandidates[1].per_unit, stream);
     case 2: return launch_tiles<T, 128, 64, 2, 2, 3>(a, ep, kCandidates[2].per_unit, stream);
-    default: return launch_tiles<T, 64, 64, 2, 2, 4>(a, ep, kCandidates[3].per_unit, stream);
+    default: break;
   }
+  // no more tiles than compute units: two halves of the inner axis in each (256 x 4096 x 4096 12.9 us and 11.2 so;
+  // 64 x 4096 x 18560, 290 tiles, 24.0 and 24.5)
+  const int64_t tiles = (a.m + 63) / 64 * ((int64_t(a.n) + 63) / 64);
+  if (tiles <= compute_units()) return launch_tiles<T, 64, 64, 2, 2, 4, 2>(a, ep, 1, stream);
+  return launch_tiles<T, 64, 64, 2, 2, 4>(a, ep, kCandidates[3].per_unit, stream);
 }
 
 }  // namespace
