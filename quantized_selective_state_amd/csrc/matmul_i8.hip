@@ -23,10 +23,26 @@ __device__ __forceinline__ float finish(int32_t sum, float sa, float sb, float b
   return fmaf(float(sum) * sa, sb, bias);
 }
 
+// 16 codes of a row of k, at any byte; those past the row's end are 0 and not read.
+__device__ __forceinline__ v4i load_codes(const int8_t* __restrict__ row, int32_t at, int32_t k) {
+  v4i r = {0, 0, 0, 0};
+  if (at + 16 <= k) {
+    __builtin_memcpy(&r, row + at, 16);
+  } else if (at < k) {
+    int8_t e[16] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (at + i < k) e[i] = row[at + i];
+    __builtin_memcpy(&r, e, 16);
+  }
+  return r;
+}
+
 // Few tokens: the time is the weights' bytes.  A wave reads its part of 16 NT weight rows straight into the matrix
 // instructions' operands, a whole 128-byte line of a row at a time, without LDS: four lanes per row take 32 bytes each, and
 // the two halves of them enter two instructions (the sum does not mind which codes meet in which instruction, as long as
-// both operands agree).  The waves of a block share the lines of the inner axis, and their sums meet in LDS.
+// both operands agree).  The waves of a block share the lines of the inner axis, and their sums meet in LDS.  kAny: rows
+// may start at any byte.
 constexpr int kLine = 128, kLinesAhead = 4;
 constexpr int kMostSums = 64;   // of 1 KB each, in LDS
 constexpr uint32_t kNowhere = 0x80000000u;    // an offset that no buffer reaches: loads as zero
@@ -35,7 +51,7 @@ __device__ __forceinline__ v4i load_piece(Rsrc r, uint32_t offset) { return __bu
 
 constexpr int stream_waves(int tiles) { return tiles <= 2 ? 16 : 8; }   // at most: more tiles take more registers
 
-template <typename T, int MT, int NT>
+template <typename T, int MT, int NT, bool kAny>
 __global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, Epilogue ep,
                                                       T* __restrict__ out, int32_t m, int32_t k, int32_t n) {
   extern __shared__ v4i sums[];   // [waves][NT][MT][64]
@@ -67,10 +83,18 @@ __global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(c
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool in = at + h * 16 < uint32_t(k);
+        if constexpr (kAny) {   // (rows past the last one: the last one's again, into results that are not stored)
+          const int32_t from = in ? int32_t(at) + h * 16 : k;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb[l][j][h] = load_piece(rb, in ? row_at[j] + at + h * 16 : kNowhere);
+          for (int j = 0; j < NT; ++j) fb[l][j][h] = load_codes(b + int64_t(min(n0 + 16 * j + lane % 16, n - 1)) * k, from, k);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) fa[l][i][h] = load_piece(ra, in ? row_at[i] + at + h * 16 : kNowhere);
+          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_codes(a + int64_t(min(m0 + 16 * i + lane % 16, m - 1)) * k, from, k);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) fb[l][j][h] = load_piece(rb, in ? row_at[j] + at + h * 16 : kNowhere);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_piece(ra, in ? row_at[i] + at + h * 16 : kNowhere);
+        }
       }
     }
 #pragma unroll
@@ -118,7 +142,7 @@ __global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(c
   }
 }
 
-template <typename T, int MT, int NT>
+template <typename T, int MT, int NT, bool kAny = false>
 hipError_t launch_stream(const MatmulArgs& a, const Epilogue& ep, hipStream_t stream) {
   const uint32_t n_tiles = uint32_t((int64_t(a.n) + 16 * NT - 1) / (16 * NT)), m_tiles = uint32_t((a.m + 16 * MT - 1) / (16 * MT));
   const uint32_t blocks = (n_tiles + 7) / 8 * 8 * m_tiles;
@@ -126,7 +150,7 @@ hipError_t launch_stream(const MatmulArgs& a, const Epilogue& ep, hipStream_t st
   int32_t waves = 4;
   while (waves < stream_waves(MT * NT) && waves * kLinesAhead < lines && blocks * waves < 4096) waves *= 2;
   const size_t lds = size_t(std::min(waves * NT * MT, kMostSums)) * kWave * sizeof(v4i);
-  stream_kernel<T, MT, NT><<<dim3(blocks), waves * kWave, lds, stream>>>(a.a, a.b, ep, static_cast<T*>(a.out),
+  stream_kernel<T, MT, NT, kAny><<<dim3(blocks), waves * kWave, lds, stream>>>(a.a, a.b, ep, static_cast<T*>(a.out),
                                                                          int32_t(a.m), a.k, a.n);
   return hipGetLastError();
 }
@@ -428,62 +452,61 @@ __global__ void __launch_bounds__(WM * WN * kSplit * kWave) tile_kernel(TileArgs
 }
 
 // Inner sizes of any number of codes: rows may start at any byte, so the pieces pass through registers, those of the next
-// slab while the current one is multiplied, and the last codes of a row are loaded one by one.  64 x 64 tiles, 4 waves.
-constexpr int kRaggedTile = 64;
-
-__device__ __forceinline__ v4i load_codes(const int8_t* __restrict__ row, int32_t at, int32_t k) {
-  v4i r = {0, 0, 0, 0};
-  if (at + 16 <= k) {
-    __builtin_memcpy(&r, row + at, 16);
-  } else if (at < k) {
-    int8_t e[16] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (at + i < k) e[i] = row[at + i];
-    __builtin_memcpy(&r, e, 16);
-  }
-  return r;
-}
-
-template <typename T>
+// slabs while the current one is multiplied (loads of 16 bytes at any address; the aligned words that hold them, shifted,
+// take longer: 777 x 1531 x 1000 18.2 us against 15.3).  A row's last slab is loaded code by code.  Square tiles, 4 waves.
+template <typename T, int kSide>
 __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restrict__ out) {
-  constexpr int TM = kRaggedTile, TN = kRaggedTile, kThreads = 256, kPieces = (TM + TN) * kSlab / 16 / kThreads;
-  typedef Store<T, 2, 2> Put;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2][(TM + TN) * kSlab];
+  constexpr int kThreads = 256, kPieces = 2 * kSide * kSlab / 16 / kThreads, F = kSide / 32;
+  constexpr int kSets = kSide == 64 ? 2 : 1;   // slabs in registers
+  typedef Store<T, F, F> Put;
+  __shared__ __attribute__((aligned(16))) int8_t lds[2][2 * kSide * kSlab];
   __shared__ __attribute__((aligned(16))) int8_t results[4][Put::kRoom];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const Walk<TM, TN> walk(args);
-  const int wm = (wave % 2) * 32, wn = (wave / 2) * 32, piece = threadIdx.x % 8;
+  const Walk<kSide, kSide> walk(args);
+  const int wm = (wave % 2) * (kSide / 2), wn = (wave / 2) * (kSide / 2), piece = threadIdx.x % 8;
   const int32_t slabs = (args.k + kSlab - 1) / kSlab;
   for (uint32_t t = blockIdx.x / 8; t < walk.run; t += walk.stride) {
     int64_t m0;
     int32_t n0;
     walk.place(t, m0, n0);
-    v4i pieces[kPieces];
-    const auto load = [&](int32_t slab) {
+    const int8_t* row[kPieces];
+    v4i pieces[kSets][kPieces];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int r = int(threadIdx.x) / 8 + i * (kThreads / 8);   // the tokens' rows, then the channels'
-        const int8_t* row = r < TM ? args.a + min(m0 + r, args.m - 1) * args.k
-                                   : args.b + int64_t(min(n0 + r - TM, args.n - 1)) * args.k;
-        pieces[i] = load_codes(row, slab * kSlab + piece * 16, args.k);
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = int(threadIdx.x) / 8 + i * (kThreads / 8);   // the tokens' rows, then the channels'
+      row[i] = r < kSide ? args.a + min(m0 + r, args.m - 1) * args.k
+                         : args.b + int64_t(min(n0 + r - kSide, args.n - 1)) * args.k;
+    }
+    const auto load = [&](int32_t slab, int set) __attribute__((always_inline)) {
+      if ((slab + 1) * kSlab <= args.k) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) __builtin_memcpy(&pieces[set][i], row[i] + slab * kSlab + piece * 16, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) pieces[set][i] = load_codes(row[i], slab * kSlab + piece * 16, args.k);
       }
     };
-    v4i acc[2][2] = {};
-    load(0);
-    for (int32_t slab = 0; slab < slabs; ++slab) {
+    v4i acc[F][F] = {};
+    const auto multiply = [&](int32_t slab, int set) __attribute__((always_inline)) {
       int8_t* rows = lds[slab & 1];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int r = int(threadIdx.x) / 8 + i * (kThreads / 8);
-        *reinterpret_cast<v4i*>(rows + r * kSlab + place_of_piece(r, piece) * 16) = pieces[i];
+        *reinterpret_cast<v4i*>(rows + r * kSlab + place_of_piece(r, piece) * 16) = pieces[set][i];
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       barrier();
-      if (slab + 1 < slabs) load(slab + 1);
-      Operands<2, 2> o;
-      o.read(rows + wm * kSlab, rows + (TM + wn) * kSlab, lane);
+      if (slab + kSets < slabs) load(slab + kSets, set);
+      Operands<F, F> o;
+      o.read(rows + wm * kSlab, rows + (kSide + wn) * kSlab, lane);
       o.multiply(acc);
+    };
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      if (i < slabs) load(i, i);
+    for (int32_t slab = 0; slab < slabs; slab += kSets) {
+      multiply(slab, 0);
+      if (kSets > 1 && slab + 1 < slabs) multiply(slab + 1, kSets - 1);
     }
     Put::run(acc, args, out, results[wave], lane, m0 + wm, n0 + wn);
     barrier();   // the next tile's first slab goes over one that other waves may still read
@@ -531,9 +554,15 @@ template <typename T>
 hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   const Epilogue ep = {a.a_scale, a.b_scale, a.bias, a.per_row};
   if (a.k % 16 != 0) {
+    if (a.m <= 16 && a.n <= 1 << 24) return launch_stream<T, 1, 1, true>(a, ep, stream);
     uint32_t blocks;
-    const TileArgs args = tile_args<kRaggedTile, kRaggedTile>(a, ep, 3, &blocks);
-    ragged_kernel<T><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+    if ((a.m + 127) / 128 * ((int64_t(a.n) + 127) / 128) >= compute_units()) {
+      const TileArgs args = tile_args<128, 128>(a, ep, 2, &blocks);
+      ragged_kernel<T, 128><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+    } else {
+      const TileArgs args = tile_args<64, 64>(a, ep, 3, &blocks);
+      ragged_kernel<T, 64><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+    }
     return hipGetLastError();
   }
   // Few tokens: up to 8 the tokens' bytes are nothing beside the weights'; up to 32 where tiles of 64 channels would leave

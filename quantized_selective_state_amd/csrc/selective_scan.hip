@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
       store_element(ry, at, 0, from_f32<T>(out));
     }
   };
-  bool inside = false;
+  bool inside = s < a.seq.sequences && span.begin <= from && from < span.end;
+  if (inside) enter(from);
   load_tile(from);
   put_tile(0);
   Group ahead = load_group(from);
@@ -458,7 +459,7 @@ constexpr int state_groups(int32_t dstate) { return dstate <= 16 ? 1 : dstate <=
 
 // How long a chunk is.  Where the sequences and channels alone give every SIMD a wave they are walked whole, in one pass.
 // Otherwise the walk is made twice, in as many chunks as fill the three waves that a SIMD holds an even number of times; a
-// chunk has 32 to 256 rows (carried states are traffic, and the sum of d is kept precise).
+// chunk has 16 to 256 rows (carried states are traffic, and the sum of d is kept precise).
 bool make_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed, Plan* p) {
   const int64_t length = packed ? tokens : tokens / sequences, chains = packed ? 1 : sequences;
   const int64_t waves = chains * ((int64_t(channels) + kWave - 1) / kWave) * state_groups(dstate);
@@ -468,7 +469,7 @@ bool make_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dsta
     const int64_t least = (length + 255) / 256, rounds = (least * waves + 3 * kSimds - 1) / (3 * kSimds);
     const int64_t number = std::max(least, rounds * 3 * kSimds / waves);
     chunk = number > 0 ? (length + number - 1) / number : 1;
-    chunk = std::min<int64_t>(256, std::max<int64_t>(32, (chunk + kGroup - 1) / kGroup * kGroup));
+    chunk = std::min<int64_t>(256, std::max<int64_t>(16, (chunk + kGroup - 1) / kGroup * kGroup));
   }
   const int64_t per = (length + chunk - 1) / chunk, chunks = per * chains;
   if (chunks >= int64_t(1) << 23) return false;   // a grid's threads along x in 32 bits

@@ -44,7 +44,8 @@ SIZES = [(1, 1, 1), (1, 16, 16), (1, 4096, 512), (1, 1531, 1000), (2, 64, 130), 
          (15, 64, 64), (16, 128, 256), (17, 192, 250), (31, 320, 1000), (32, 8192, 96), (33, 4096, 2048), (48, 65, 129),
          (64, 1024, 1024), (65, 1008, 1030), (100, 2048, 8512), (127, 127, 127), (128, 4096, 512), (129, 129, 129),
          (200, 8192, 520), (256, 256, 256), (257, 2048, 4096), (300, 1531, 999), (512, 640, 2000), (777, 1531, 1000),
-         (1000, 4096, 1000), (1024, 4096, 4096), (2048, 64, 2560), (2500, 2560, 2570), (4096, 192, 4100)]
+         (1000, 4096, 1000), (1024, 4096, 4096), (2048, 64, 2560), (2500, 2560, 2570), (4096, 192, 4100),
+         (16, 5003, 700), (700, 8192, 130), (3000, 333, 2800), (8200, 1040, 4200), (20, 131071, 40), (6, 131056, 300)]
 
 
 @pytest.mark.parametrize("m,k,n", SIZES)
