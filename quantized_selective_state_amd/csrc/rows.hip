@@ -260,8 +260,9 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   a.eps = n.eps;
   a.inverse_size = 1.f / float(a.size);
   const int32_t packs = (a.size + V - 1) / V;
-  // up to four packs a lane, eight where the block would else be too large (the limits on sizes make that enough)
-  a.lanes = power_of_two((packs + 3) / 4);
+  // up to four packs a lane, one where there is not a row for every compute unit, eight where the block would else be too
+  // large (the limits on sizes make that enough)
+  a.lanes = power_of_two(a.rows < compute_units() && power_of_two(packs) * a.groups <= kMostThreads ? packs : (packs + 3) / 4);
   if (a.lanes * a.groups > kMostThreads) a.lanes = power_of_two((packs + 7) / 8);
   const int32_t threads = a.lanes * a.groups;
   if (threads > kMostThreads) return hipErrorInvalidValue;

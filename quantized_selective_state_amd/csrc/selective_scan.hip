@@ -354,21 +354,27 @@ __global__ void __launch_bounds__(kThreads) carry_kernel(ScanKernelArgs a) {
     const int32_t last = first + a.per_sequence - 1;   // nothing enters a chain's first chunk; nothing reads its last's
     const int64_t pitch = int64_t(a.dstate) * a.channels;
     float* at = a.states + (int64_t(first) * a.dstate + n) * a.channels + c;
-    float h = 0.f;
-    for (int32_t k = first; k < last; k += kCarried, at += kCarried * pitch) {   // loads of several chunks at a time
-      float own[kCarried], sum[kCarried];
-      int32_t reset[kCarried];
+    struct Group { float own[kCarried], sum[kCarried]; int32_t reset[kCarried]; };
+    const auto load = [&](int32_t k) {   // (past the last: its values again)
+      Group g;
 #pragma unroll
       for (int i = 0; i < kCarried; ++i) {
         const int32_t j = min(k + i, last - 1);
-        own[i] = at[(j - k) * pitch];
-        sum[i] = a.sums[int64_t(j) * a.channels + c];
-        reset[i] = a.resets[j];
+        g.own[i] = at[(j - first) * pitch];
+        g.sum[i] = a.sums[int64_t(j) * a.channels + c];
+        g.reset[i] = a.resets[j];
       }
+      return g;
+    };
+    float h = 0.f;
+    Group ahead = load(first);
+    for (int32_t k = first; k < last; k += kCarried) {   // the loads of one group of chunks ahead of the other's sums
+      const Group now = ahead;
+      if (k + kCarried < last) ahead = load(k + kCarried);
 #pragma unroll
       for (int i = 0; i < kCarried; ++i) {
-        h = reset[i] ? own[i] : fmaf(__builtin_amdgcn_exp2f(sum[i] * A2), h, own[i]);
-        if (k + i < last) at[i * pitch] = h;
+        h = now.reset[i] ? now.own[i] : fmaf(__builtin_amdgcn_exp2f(now.sum[i] * A2), h, now.own[i]);
+        if (k + i < last) at[(k + i - first) * pitch] = h;
       }
     }
   }
