@@ -619,8 +619,8 @@ ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, cons
  *                  n / static_scale, within [-127, 127] (NaN gives 0); scale is NULL then
  * -128 is never produced.  A row whose sum of squares is not finite in binary32 (a NaN or an infinity in it, or
  * magnitudes near 2^64) is NaN: out is NaN throughout, the scale is NaN and the codes 0, so that the fault is not hidden;
- * with a static scale its codes are 0.  (With groups: out is NaN in that group, scale and codes over the row; under
- * a static scale the codes are 0 in that group.)
+ * with a static scale its codes are 0.  So is a row of zeros with eps 0.  (With groups: out is NaN in that group, scale
+ * and codes over the row; under a static scale the codes are 0 in that group.)
  *   dtype    : ssdq_dtype of x, gate and out     x, gate, out : (rows, channels)
  *   residual_dtype : ssdq_dtype of residual and residual_out: dtype, or SSDQ_DTYPE_F32
  *   residual, residual_out : (rows, channels) or both NULL; residual_out may be residual
@@ -686,10 +686,10 @@ ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale,
  *               first
  *   state_out : (sequences, width - 1, channels) of dtype or NULL, written: the inputs of each sequence's last width - 1
  *               tokens, oldest first (of state where it has fewer); it must not be state
- * width 2, 3 or 4; sequences, channels >= 1; tokens >= 0, dense a multiple of sequences; tokens < 2^31 - 2^16,
- * sequences < 2^24, channels <= 2^20 and ceil(channels / 64) * (sequences + tokens / 16) < 2^31 (else
- * SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of order give
- * unspecified results but no access outside the tensors.  No output overlaps an input.
+ * width 2, 3 or 4; sequences, channels >= 1; tokens >= 0, dense a multiple of sequences (else SSDQ_ERROR_INVALID_VALUE);
+ * tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20 and ceil(channels / 256) * (sequences + tokens / 16 + 1) < 2^25
+ * (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of order
+ * give unspecified results but no access outside the tensors.  No output overlaps an input.
  */
 ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, const float* bias, const void* state,
                              const int32_t* offsets, void* out, void* state_out, int32_t sequences, int64_t tokens,
@@ -728,9 +728,10 @@ size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int
  *   workspace    : device scratch of at least ssdq_selective_scan_workspace_size() bytes, owned by the caller, not
  *                  shared with a concurrent call; it need not start at any value
  * sequences >= 1, tokens >= 0, channels >= 1, 1 <= dstate <= 64; dense tokens a multiple of sequences (else
- * SSDQ_ERROR_INVALID_VALUE); tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20, fewer than 2^23 chunks of 256 tokens
- * (dense: of each sequence) and a workspace below 2^40 bytes (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 the (tokens, ...) pointers are not looked
- * at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence and
+ * SSDQ_ERROR_INVALID_VALUE); tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20, a workspace below 2^40 bytes and
+ * fewer than 2^23 pieces that the kernels walk the sequences in: up to 256 tokens of a sequence each, or a whole one where
+ * sequences and channels alone fill the device (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With
+ * tokens == 0 the (tokens, ...) pointers are not looked at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence and
  * channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
  * products of it over 256 neighbouring tokens stay finite.  The result does not depend on timing: calls with the same
  * arguments give the same bits.
@@ -745,8 +746,8 @@ ssdq_status ssdq_selective_scan(int32_t dtype, const void* u, const void* delta,
  * One token of ssdq_selective_scan for every sequence of a decode batch, the state updated in place:
  *   state : (batch, channels, dstate) fp32, read and written     u, delta, z, y : (batch, channels)
  *   B, C  : (batch, dstate)
- * batch, channels >= 1, 1 <= dstate <= 64, batch * channels < 2^31 (else SSDQ_ERROR_UNSUPPORTED); no workspace.  No
- * output overlaps another tensor.
+ * batch, channels >= 1; 1 <= dstate <= 64 and batch * ceil(channels / 16) < 2^24 (else SSDQ_ERROR_UNSUPPORTED); no
+ * workspace.  No output overlaps another tensor.
  */
 ssdq_status ssdq_selective_step(int32_t dtype, float* state, const void* u, const void* delta, const float* A,
                                 const void* B, const void* C, const float* D, const void* z, const float* delta_bias,

@@ -134,7 +134,8 @@ ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, 
   if (!ok_dtype(dtype) || width < 2 || width > 4) return SSDQ_ERROR_INVALID_VALUE;
   const ssdq_status st = check_sequences(sequences, tokens, channels, offsets != nullptr);
   if (st != SSDQ_SUCCESS) return st;
-  if (((int64_t(channels) + 63) / 64) * (sequences + tokens / 16) >= (int64_t(1) << 31)) return SSDQ_ERROR_UNSUPPORTED;
+  // a grid's threads in 31 bits, at 64 for each 16 rows x 256 channels and for each sequence's state
+  if ((int64_t(channels) + 255) / 256 * (sequences + tokens / 16 + 1) >= int64_t(1) << 25) return SSDQ_ERROR_UNSUPPORTED;
   if (!ok_ptr(weight) || !ok_opt(bias) || !ok_opt(state) || !ok_opt(offsets) || !ok_opt(state_out))
     return SSDQ_ERROR_INVALID_VALUE;
   if (tokens > 0 && (!ok_ptr(x) || !ok_ptr(out))) return SSDQ_ERROR_INVALID_VALUE;
@@ -185,7 +186,8 @@ ssdq_status ssdq_selective_step(int32_t dtype, float* state, const void* u, cons
                                 void* y, int32_t batch, int32_t channels, int32_t dstate, int32_t softplus,
                                 hipStream_t stream) {
   if (!ok_dtype(dtype) || batch <= 0 || channels <= 0 || dstate <= 0) return SSDQ_ERROR_INVALID_VALUE;
-  if (dstate > 64 || int64_t(batch) * channels >= (int64_t(1) << 31)) return SSDQ_ERROR_UNSUPPORTED;
+  // a grid's threads in 32 bits, at up to 256 for each 16 channels
+  if (dstate > 64 || (int64_t(channels) + 15) / 16 * batch >= int64_t(1) << 24) return SSDQ_ERROR_UNSUPPORTED;
   if (!ok_ptr(state) || !ok_ptr(u) || !ok_ptr(delta) || !ok_ptr(A) || !ok_ptr(B) || !ok_ptr(C) || !ok_opt(D) ||
       !ok_opt(z) || !ok_opt(delta_bias) || !ok_ptr(y))
     return SSDQ_ERROR_INVALID_VALUE;

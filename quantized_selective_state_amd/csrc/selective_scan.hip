@@ -532,7 +532,6 @@ hipError_t launch_step(float* state, const void* u, const void* delta, const flo
   // four sequences a lane once they leave a block for every compute unit
   const bool many = int64_t(channel_blocks) * (batch / 4) >= 256;
   const int64_t blocks = int64_t(channel_blocks) * (many ? (batch + 3) / 4 : batch);
-  if (blocks >= int64_t(1) << 24) return hipErrorInvalidValue;   // (the limit on batch * channels keeps below it)
   const dim3 grid = dim3(uint32_t(blocks));
   const T *in = static_cast<const T*>(u), *steps = static_cast<const T*>(delta), *gate = static_cast<const T*>(z);
   const T *b = static_cast<const T*>(B), *c = static_cast<const T*>(C);

@@ -69,7 +69,9 @@ def test_matmul_refusals(over, status):
     (dict(offsets=ODD), INVALID), (dict(out=None), INVALID), (dict(state_out=ODD), INVALID),
     (dict(state_out=A), INVALID), (dict(tokens=1 << 31, sequences=1), UNSUPPORTED),
     (dict(channels=(1 << 20) + 1), UNSUPPORTED), (dict(sequences=1 << 24, tokens=1 << 24), UNSUPPORTED),
-    (dict(channels=1 << 20, tokens=1 << 30, sequences=1), UNSUPPORTED)])
+    (dict(channels=1 << 20, tokens=1 << 30, sequences=1), UNSUPPORTED),
+    (dict(channels=64, tokens=(1 << 29) - 32, sequences=1), UNSUPPORTED),   # 2^25 - 2 runs of 16 rows, a state, one more
+    (dict(channels=64, tokens=(1 << 29) - 48, sequences=1, x=None), INVALID)])
 def test_conv_refusals(over, status):
     a = dict(dtype=1, x=A, weight=A, bias=A, state=A, offsets=None, out=A, state_out=2 * A, sequences=2, tokens=8,
              channels=64, width=4, silu=1)
@@ -113,6 +115,7 @@ def test_selective_step_refusals():
                  dict(z=ODD), dict(b=ODD), dict(y=None), dict(n=0), dict(c=0), dict(k=0)):
         assert call(**over) == INVALID, over
     assert call(k=65) == UNSUPPORTED and call(n=1 << 20, c=1 << 11) == UNSUPPORTED
+    assert call(n=1 << 24, c=1) == UNSUPPORTED and call(n=1 << 20, c=241) == UNSUPPORTED   # 2^24 blocks of 16 channels
 
 
 # ---- the binding: tensors on the CPU are refused before anything else could happen ----
