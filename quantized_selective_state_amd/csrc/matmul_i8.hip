@@ -3,6 +3,11 @@
 // Both operands have their inner axis contiguous, as the matrix instructions take them (a lane's 16 codes are
 // neighbours).  The weights are the instruction's first operand, so that a lane of the result holds 4 neighbouring output
 // channels of one token and stores them together.
+//
+// Three kernels: few tokens are bound by the weights' bytes and streamed (1 x 4096 x 18560 15 us, 5.0 TB/s); many tokens
+// by the matrix units, whose clock the card's power limits on codes that are not zeros (32768 x 4096 x 18560 2.05 ms, 2.4
+// POP/s; out of registers alone random codes reach 3.4 to 4.0, zeros 4.8); inner sizes that no 16 divides by their unaligned
+// loads (777 x 1531 x 1000 15 us).
 #include <algorithm>
 
 #include "block_internal.h"
@@ -38,41 +43,36 @@ __device__ __forceinline__ v4i load_codes(const int8_t* __restrict__ row, int32_
   return r;
 }
 
-// Few tokens: the time is the weights' bytes.  A wave reads its part of 16 NT weight rows straight into the matrix
+// Few tokens: the time is the weights' bytes.  A wave reads its part of 16 weight rows straight into the matrix
 // instructions' operands, a whole 128-byte line of a row at a time, without LDS: four lanes per row take 32 bytes each, and
 // the two halves of them enter two instructions (the sum does not mind which codes meet in which instruction, as long as
-// both operands agree).  The waves of a block share the lines of the inner axis, and their sums meet in LDS.  kAny: rows
-// may start at any byte.
+// both operands agree).  The waves of a block share the lines of the inner axis, and their sums meet in LDS.  Up to 16 MT
+// tokens.  kAny: rows may start at any byte (1 x 8190 x 4096 19 us; by tiles 63).
 constexpr int kLine = 128, kLinesAhead = 4;
-constexpr int kMostSums = 64;   // of 1 KB each, in LDS
+constexpr int kStreamWaves = 16;              // at most
 constexpr uint32_t kNowhere = 0x80000000u;    // an offset that no buffer reaches: loads as zero
 
 __device__ __forceinline__ v4i load_piece(Rsrc r, uint32_t offset) { return __builtin_bit_cast(v4i, buf_load16(r, offset)); }
 
-constexpr int stream_waves(int tiles) { return tiles <= 2 ? 16 : 8; }   // at most: more tiles take more registers
-
-template <typename T, int MT, int NT, bool kAny>
-__global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, Epilogue ep,
-                                                      T* __restrict__ out, int32_t m, int32_t k, int32_t n) {
-  extern __shared__ v4i sums[];   // [waves][NT][MT][64]
+template <typename T, int MT, bool kAny>
+__global__ void __launch_bounds__(kStreamWaves* kWave)
+    stream_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, Epilogue ep, T* __restrict__ out, int32_t m,
+                  int32_t k, int32_t n) {
+  extern __shared__ v4i sums[];   // [waves][MT][64]
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
-  // the token tiles of the same weights on neighbouring blocks of one XCD
-  const uint32_t m_tiles = uint32_t(m + 16 * MT - 1) / (16 * MT);
-  const uint32_t tile = blockIdx.x / 8, n_tile = tile / m_tiles * 8 + blockIdx.x % 8;
-  const int32_t n0 = int32_t(n_tile) * 16 * NT, m0 = int32_t(tile % m_tiles) * 16 * MT;
-  if (n0 >= n) return;
-  const Rsrc ra = make_rsrc(a + int64_t(m0) * k, uint32_t(min(m - m0, 16 * MT)) * uint32_t(k));
-  const Rsrc rb = make_rsrc(b + int64_t(n0) * k, uint32_t(min(n - n0, 16 * NT)) * uint32_t(k));
+  const int32_t n0 = int32_t(blockIdx.x) * 16;
+  const Rsrc ra = make_rsrc(a, uint32_t(m) * uint32_t(k));
+  const Rsrc rb = make_rsrc(b + int64_t(n0) * k, uint32_t(min(n - n0, 16)) * uint32_t(k));
   const int32_t lines = (k + kLine - 1) / kLine;
-  v4i acc[NT][MT] = {};
-  uint32_t row_at[NT > MT ? NT : MT];
+  v4i acc[MT] = {};
+  uint32_t row_at[MT];
 #pragma unroll
-  for (int i = 0; i < (NT > MT ? NT : MT); ++i) row_at[i] = uint32_t(lane % 16 + 16 * i) * uint32_t(k);
+  for (int i = 0; i < MT; ++i) row_at[i] = uint32_t(lane % 16 + 16 * i) * uint32_t(k);
   // Blocks begin at different lines: rows of many codes are often a power of two apart, and the same line of all rows
-  // would lie in few of the memory's channels.
-  const int32_t turn = int32_t(n_tile * 5 % uint32_t(lines));
+  // would lie in few of the memory's channels (1 x 4096 x 18560: 22 us, and 16 so).
+  const int32_t turn = int32_t(blockIdx.x * 5 % uint32_t(lines));
   for (int32_t line0 = wave; line0 < lines; line0 += waves * kLinesAhead) {
-    v4i fa[kLinesAhead][MT][2], fb[kLinesAhead][NT][2];
+    v4i fa[kLinesAhead][MT][2], fb[kLinesAhead][2];
 #pragma unroll
     for (int l = 0; l < kLinesAhead; ++l) {
       int32_t line = line0 + l * waves;
@@ -85,13 +85,11 @@ __global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(c
         const bool in = at + h * 16 < uint32_t(k);
         if constexpr (kAny) {   // (rows past the last one: the last one's again, into results that are not stored)
           const int32_t from = in ? int32_t(at) + h * 16 : k;
+          fb[l][h] = load_codes(b + int64_t(min(n0 + lane % 16, n - 1)) * k, from, k);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) fb[l][j][h] = load_codes(b + int64_t(min(n0 + 16 * j + lane % 16, n - 1)) * k, from, k);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_codes(a + int64_t(min(m0 + 16 * i + lane % 16, m - 1)) * k, from, k);
+          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_codes(a + int64_t(min(16 * i + lane % 16, m - 1)) * k, from, k);
         } else {
-#pragma unroll
-          for (int j = 0; j < NT; ++j) fb[l][j][h] = load_piece(rb, in ? row_at[j] + at + h * 16 : kNowhere);
+          fb[l][h] = load_piece(rb, in ? row_at[0] + at + h * 16 : kNowhere);
 #pragma unroll
           for (int i = 0; i < MT; ++i) fa[l][i][h] = load_piece(ra, in ? row_at[i] + at + h * 16 : kNowhere);
         }
@@ -102,62 +100,40 @@ __global__ void __launch_bounds__(stream_waves(MT * NT) * kWave) stream_kernel(c
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[l][j][h], fa[l][i][h], acc[j][i], 0, 0, 0);
+        for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[l][h], fa[l][i][h], acc[i], 0, 0, 0);
   }
-  const auto put = [&](int place) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < MT; ++i) sums[((place * NT + j) * MT + i) * kWave + lane] = acc[j][i];
-  };
-  int parts = waves;
-  while (parts * NT * MT > kMostSums) {   // more than LDS is taken for: one half of the waves' sums joins the other
-    parts /= 2;
-    if (wave >= parts && wave < 2 * parts) put(wave - parts);
-    __syncthreads();
-    if (wave < parts) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[j][i] += sums[((wave * NT + j) * MT + i) * kWave + lane];
-    }
-    __syncthreads();
-  }
-  if (wave < parts) put(wave);
+  for (int i = 0; i < MT; ++i) sums[(wave * MT + i) * kWave + lane] = acc[i];
   __syncthreads();
-  for (int part = wave; part < NT * MT; part += waves) {
-    v4i sum = {0, 0, 0, 0};
-    for (int w = 0; w < parts; ++w) sum += sums[(w * NT * MT + part) * kWave + lane];
-    const int32_t row = m0 + (part % MT) * 16 + lane % 16, col = n0 + (part / MT) * 16 + (lane / 16) * 4;
-    if (row >= m) continue;
-    const float sa = ep.a_scale[ep.per_row ? row : 0];
-    T* to = out + int64_t(row) * n + col;
+  if (wave >= MT) return;   // one wave for each 16 tokens
+  v4i sum = {0, 0, 0, 0};
+  for (int w = 0; w < waves; ++w) sum += sums[(w * MT + wave) * kWave + lane];
+  const int32_t row = wave * 16 + lane % 16, col = n0 + (lane / 16) * 4;
+  if (row >= m) return;
+  const float sa = ep.a_scale[ep.per_row ? row : 0];
+  T* to = out + int64_t(row) * n + col;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n)
-        to[e] = from_f32<T>(finish(sum[e], sa, ep.b_scale[col + e], ep.bias != nullptr ? ep.bias[col + e] : 0.f));
-  }
+  for (int e = 0; e < 4; ++e)
+    if (col + e < n)
+      to[e] = from_f32<T>(finish(sum[e], sa, ep.b_scale[col + e], ep.bias != nullptr ? ep.bias[col + e] : 0.f));
 }
 
-template <typename T, int MT, int NT, bool kAny = false>
+template <typename T, int MT, bool kAny = false>
 hipError_t launch_stream(const MatmulArgs& a, const Epilogue& ep, hipStream_t stream) {
-  const uint32_t n_tiles = uint32_t((int64_t(a.n) + 16 * NT - 1) / (16 * NT)), m_tiles = uint32_t((a.m + 16 * MT - 1) / (16 * MT));
-  const uint32_t blocks = (n_tiles + 7) / 8 * 8 * m_tiles;
+  const uint32_t blocks = uint32_t((int64_t(a.n) + 15) / 16);
   const int32_t lines = (a.k + kLine - 1) / kLine;
   int32_t waves = 4;
-  while (waves < stream_waves(MT * NT) && waves * kLinesAhead < lines && blocks * waves < 4096) waves *= 2;
-  const size_t lds = size_t(std::min(waves * NT * MT, kMostSums)) * kWave * sizeof(v4i);
-  stream_kernel<T, MT, NT, kAny><<<dim3(blocks), waves * kWave, lds, stream>>>(a.a, a.b, ep, static_cast<T*>(a.out),
-                                                                         int32_t(a.m), a.k, a.n);
+  while (waves < kStreamWaves && waves * kLinesAhead < lines && blocks * waves < 4096) waves *= 2;
+  const size_t lds = size_t(waves) * MT * kWave * sizeof(v4i);
+  stream_kernel<T, MT, kAny><<<dim3(blocks), waves * kWave, lds, stream>>>(a.a, a.b, ep, static_cast<T*>(a.out),
+                                                                          int32_t(a.m), a.k, a.n);
   return hipGetLastError();
 }
 
 // Many tokens: tiles of TM tokens x TN output channels for inner sizes of whole 16-byte pieces.  Slabs of 128 codes of both
 // operands, a whole line of every row, go from memory to LDS without passing registers and ahead of the products, into
-// the next tile too: a block walks several tiles, and its loads do not stop between them.
+// the next tile too: a block walks several tiles, and its loads do not stop between them (32768 x 4096 x 18560: through
+// registers 4771 us, into LDS 3126, with the loads running on 2565, with the reads of LDS below 2046).
 constexpr int kSlab = 128;
 
 __device__ __forceinline__ void load_to_lds(Rsrc r, void* lds, uint32_t offset) {
@@ -391,7 +367,9 @@ struct Store {
   }
 };
 
-// WM x WN waves, kStages slabs in LDS.  Between two barriers every wave reads a slab's operands and multiplies them.  With
+// WM x WN waves, kStages slabs in LDS.  Between two barriers every wave reads a slab's operands and multiplies them.  The
+// largest tiles read the fewest bytes of LDS per product: 256 x 256 in 8 waves has matrix units and LDS busy for about as
+// long, 64 x 64 is bound by LDS and by what a compute unit can load (256 x 8192 x 4096 17 to 21 us, 0.9 POP/s).  With
 // kSplit 2 there are twice the waves, and the halves of them walk half of the inner axis each: two waves on every SIMD for
 // tiles that are too few to give a compute unit a second one.
 template <typename T, int TM, int TN, int WM, int WN, int kStages, int kSplit>
@@ -453,7 +431,8 @@ __global__ void __launch_bounds__(WM * WN * kSplit * kWave) tile_kernel(TileArgs
 
 // Inner sizes of any number of codes: rows may start at any byte, so the pieces pass through registers, those of the next
 // slabs while the current one is multiplied (loads of 16 bytes at any address; the aligned words that hold them, shifted,
-// take longer: 777 x 1531 x 1000 18.2 us against 15.3).  A row's last slab is loaded code by code.  Square tiles, 4 waves.
+// take longer: 777 x 1531 x 1000 18.2 us against 15.3).  A row's last slab is loaded code by code.  Square tiles, 4 waves,
+// of 128 once there is one for every compute unit (8192 x 4097 x 8192 501 us, 862 with 64), else of 64.
 template <typename T, int kSide>
 __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restrict__ out) {
   constexpr int kThreads = 256, kPieces = 2 * kSide * kSlab / 16 / kThreads, F = kSide / 32;
@@ -526,7 +505,8 @@ template <typename T, int TM, int TN, int WM, int WN, int kStages, int kSplit = 
 hipError_t launch_tiles(const MatmulArgs& a, const Epilogue& ep, int per_unit, hipStream_t stream) {
   uint32_t blocks;
   const TileArgs args = tile_args<TM, TN>(a, ep, per_unit, &blocks);
-  tile_kernel<T, TM, TN, WM, WN, kStages, kSplit><<<dim3(blocks), WM * WN * kSplit * kWave, 0, stream>>>(args, static_cast<T*>(a.out));
+  tile_kernel<T, TM, TN, WM, WN, kStages, kSplit>
+      <<<dim3(blocks), WM * WN * kSplit * kWave, 0, stream>>>(args, static_cast<T*>(a.out));
   return hipGetLastError();
 }
 
@@ -540,7 +520,8 @@ int choose(const MatmulArgs& a) {
   double least = 0.;
   for (int i = 0; i < 4; ++i) {
     const Candidate& c = kCandidates[i];
-    const int64_t tiles = (a.m + c.tm - 1) / c.tm * ((int64_t(a.n) + c.tn - 1) / c.tn), slots = compute_units() * c.per_unit;
+    const int64_t tiles = (a.m + c.tm - 1) / c.tm * ((int64_t(a.n) + c.tn - 1) / c.tn);
+    const int64_t slots = int64_t(compute_units()) * c.per_unit;
     const double time = double((tiles + slots - 1) / slots) * c.slab_us;
     if (i == 0 || time < least) {
       best = i;
@@ -554,7 +535,7 @@ template <typename T>
 hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   const Epilogue ep = {a.a_scale, a.b_scale, a.bias, a.per_row};
   if (a.k % 16 != 0) {
-    if (a.m <= 16 && a.n <= 1 << 24) return launch_stream<T, 1, 1, true>(a, ep, stream);
+    if (a.m <= 16 && a.n <= 1 << 24) return launch_stream<T, 1, true>(a, ep, stream);
     uint32_t blocks;
     if ((a.m + 127) / 128 * ((int64_t(a.n) + 127) / 128) >= compute_units()) {
       const TileArgs args = tile_args<128, 128>(a, ep, 2, &blocks);
@@ -568,8 +549,8 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   // Few tokens: up to 8 the tokens' bytes are nothing beside the weights'; up to 32 where tiles of 64 channels would leave
   // half of the compute units idle (16 x 8192 x 4096: 11.0 us against 20.5; 16 x 4096 x 18560: 23.2 against 20.9).
   const bool narrow = (int64_t(a.n) + 63) / 64 * 2 <= compute_units();
-  if ((a.m <= 8 && a.n <= 1 << 24) || (a.m <= 16 && narrow)) return launch_stream<T, 1, 1>(a, ep, stream);
-  if (a.m <= 32 && narrow) return launch_stream<T, 2, 1>(a, ep, stream);
+  if ((a.m <= 8 && a.n <= 1 << 24) || (a.m <= 16 && narrow)) return launch_stream<T, 1>(a, ep, stream);
+  if (a.m <= 32 && narrow) return launch_stream<T, 2>(a, ep, stream);
   switch (choose(a)) {
     case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(a, ep, kCandidates[0].per_unit, stream);
     case 1: return launch_tiles<T, 128, 128, 2, 2, 2>(a, ep, kCandidates[1].per_unit, stream);

@@ -4,6 +4,11 @@
 // One pass: n = (v w) / sqrt(mean(v^2) + eps), and since multiplying by the positive root is monotone in binary32,
 // max |n| is max |v w| times it.  So the sum of squares and the largest |v w| are reduced together, the row stays in
 // registers between, and a block has one barrier per row (none where a row fits one wave).
+//
+// HBM-bound: every tensor once (32768 x 4096 bf16: norm 82 us, 6.5 TB/s; to codes 73, with a residual in bf16 to codes 172,
+// 5.5 TB/s; 32768 x 8192 fp16 gated to codes 256, 5.2 TB/s; rows as codes 70 and back 61 at 32768 x 4096).  A lane's 16
+// bytes are neighbours and a lane holds up to four such pieces, so that a row has some waves and a compute unit many
+// rows: their loads cover each other's latency, and no row is loaded ahead by its own block.
 #include "block_internal.h"
 #include "gated_types.h"
 
@@ -128,7 +133,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
         float o[V];
         load_some(static_cast<const R*>(a.other) + at + c, count, o);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[s][i] = SOURCE == kResidual ? v[s][i] + o[i] : v[s][i] * silu<sizeof(T) == 4>(o[i]);
+        for (int i = 0; i < V; ++i)
+          v[s][i] = SOURCE == kResidual ? v[s][i] + o[i] : v[s][i] * silu<sizeof(T) == 4>(o[i]);
         if constexpr (SOURCE == kResidual)
           store_some<false>(static_cast<R*>(a.residual_out) + at + c, count, rounded<R>(v[s]));
       }
@@ -207,7 +213,7 @@ template <typename T, bool PAST>
 __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __restrict__ codes,
                                                               const float* __restrict__ scale, T* __restrict__ x,
                                                               int64_t rows, int32_t channels, int32_t lanes) {
-  // kAtOnce rows of a thread, so that their loads are under way together
+  // kAtOnce rows of a thread, so that their loads are under way together (32768 x 8192 fp16 121 us, 230 with one)
   constexpr int kAtOnce = 4;
   const int per_block = 256 / lanes, lane = int(threadIdx.x) % lanes;
   const int64_t step = int64_t(gridDim.x) * per_block;
@@ -237,8 +243,9 @@ int32_t power_of_two(int32_t n) {
   return p;
 }
 
-// Stores pass the caches by once a call touches more than the 256 MiB of the Infinity Cache (32768 x 4096 bf16: norm 98 us
-// and 82 with it, norm to codes 86 and 72, values of codes 82 and 61; below, 100000 x 256 fp16 gated to codes, 29 and 44).
+// Stores pass the caches by once a call touches more than the 256 MiB of the Infinity Cache (32768 x 4096 bf16: norm 98
+// us and 82 with it, norm to codes 86 and 72, values of codes 82 and 61; below, 100000 x 256 fp16 gated to codes, 29
+// and 44).
 // The residual stays an ordinary store (fp32 residual to codes, 32768 x 4096: 275 us, 285 with all stores).
 constexpr int64_t kInfinityCache = int64_t(256) << 20;
 
@@ -260,12 +267,11 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   a.eps = n.eps;
   a.inverse_size = 1.f / float(a.size);
   const int32_t packs = (a.size + V - 1) / V;
-  // up to four packs a lane, one where there is not a row for every compute unit, eight where the block would else be too
-  // large (the limits on sizes make that enough)
-  a.lanes = power_of_two(a.rows < compute_units() && power_of_two(packs) * a.groups <= kMostThreads ? packs : (packs + 3) / 4);
-  if (a.lanes * a.groups > kMostThreads) a.lanes = power_of_two((packs + 7) / 8);
+  // Up to four packs a lane, so that a compute unit has several rows (the limits on sizes keep all groups within
+  // kMostThreads); one where there is not a row for every compute unit.
+  const bool few = a.rows < compute_units() && power_of_two(packs) * a.groups <= kMostThreads;
+  a.lanes = power_of_two(few ? packs : (packs + 3) / 4);
   const int32_t threads = a.lanes * a.groups;
-  if (threads > kMostThreads) return hipErrorInvalidValue;
   a.per_block = threads >= 256 ? 1 : 256 / threads;
   const int32_t block = (threads * a.per_block + kWave - 1) / kWave * kWave;
   const int64_t items = (a.rows + a.per_block - 1) / a.per_block;
@@ -274,8 +280,7 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   const int32_t slots = (packs + a.lanes - 1) / a.lanes;
   if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1, PAST><<<grid, block, 0, stream>>>(a);
   else if (slots <= 2) norm_kernel<T, R, SOURCE, NORM, OUT, 2, PAST><<<grid, block, 0, stream>>>(a);
-  else if (slots <= 4) norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST><<<grid, block, 0, stream>>>(a);
-  else norm_kernel<T, R, SOURCE, NORM, OUT, 8, PAST><<<grid, block, 0, stream>>>(a);
+  else norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
