@@ -729,8 +729,8 @@ size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int
  *                  shared with a concurrent call; it need not start at any value
  * sequences >= 1, tokens >= 0, channels >= 1, 1 <= dstate <= 64; dense tokens a multiple of sequences (else
  * SSDQ_ERROR_INVALID_VALUE); tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20, a workspace below 2^40 bytes and
- * fewer than 2^23 pieces that the kernels walk the sequences in: up to 256 tokens of a sequence each, or a whole one where
- * sequences and channels alone fill the device (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With
+ * fewer than 2^23 pieces that the kernels walk the sequences in: 16 to 256 tokens of a sequence each, or a whole one
+ * (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With
  * tokens == 0 the (tokens, ...) pointers are not looked at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence and
  * channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
  * products of it over 256 neighbouring tokens stay finite.  The result does not depend on timing: calls with the same

@@ -26,6 +26,8 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-result",
 ]
+# Pairs of 16-bit values that are still being loaded would be packed into one register, and the packing waits for them.
+EXTRA = {"selective_scan.hip": ["-fno-slp-vectorize"]}
 
 
 def sources() -> list[str]:
@@ -34,9 +36,10 @@ def sources() -> list[str]:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *COMMON, "-c", src, "-o", obj]
+    flags = [*COMMON, *EXTRA.get(os.path.basename(src), [])]
+    cmd = [HIPCC, *flags, "-c", src, "-o", obj]
     if src.endswith(".cpp"):
-        cmd = [HIPCC, *COMMON, "-x", "hip", "-c", src, "-o", obj]
+        cmd = [HIPCC, *flags, "-x", "hip", "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     # hipcc's host pass warns that it does not know the packed-fp32 feature: harmless
     err = "\n".join(line for line in r.stderr.splitlines() if "packed-fp32-ops" not in line)

@@ -3,16 +3,17 @@
 //
 //   d = softplus(delta + bias);  h[n] = exp(d A[n]) h[n] + d u B[n];  y = (sum_n C[n] h[n] + D u) silu(z)
 //
-// A lane holds one channel with up to 16 of its states in registers and walks rows; B and C, the same for all channels,
-// are staged as binary32 in LDS for the block's channels.  Where sequences and channels alone fill the device, each is
-// walked whole, in one pass (16 x 2048 x 8192 bf16 1300 us).  Otherwise chunks of rows run side by side: a first kernel
-// forms what every chunk makes of a zero state, a second one carries states from chunk to chunk, h <- exp(A sum d) h +
-// that, and a third walks the chunks again from the states that enter them and writes y.
+// Two ways to walk. Dense sequences whole, by four lanes a channel with a quarter of its states each (quad_kernel): one
+// pass, where sequences and channels give the device enough waves or the sequences are short.  Otherwise, and packed, in
+// chunks of rows side by side (chunk_kernel), a lane holding one channel with up to 16 states: a first kernel forms what
+// every chunk makes of a zero state, a second one carries states from chunk to chunk, h <- exp(A sum d) h + that, and a
+// third walks the chunks again from the states that enter them and writes y.  B and C, the same for all channels, are
+// staged as binary32 in LDS.
 //
-// Bound by the vector units, not by memory: a token, channel and state costs an exp2 (a quarter of the rate of an fma), two
-// products, an fma into the state and in the last pass one into y.  4 x 2048 x 4096 bf16, 16 states: 277 us, of them 129
-// the first kernel, 11 the second, 170 the third less their overlap, vector units at work in 73 to 76% of the cycles; its
-// bytes would take 54.  16384 x 5120 fp16 634 us.
+// Bound by the vector units, not by memory: a token, channel and state costs an exp2 (a third of the rate of an fma), two
+// products, an fma into the state and one into y.  With 16 states, bf16: 4 x 2048 x 4096 223 us (its bytes would take 54; in
+// chunks 257), 16 x 2048 x 8192 1071 us (4.0e12 tokens x channels x states a second).  16384 x 5120 fp16, in chunks, 584 us.
+// 4 x 2048 x 4096 with 64 states 535 us (in chunks 1255).
 #include "block_internal.h"
 #include "gated_types.h"
 #include "sequences.h"
@@ -54,6 +55,15 @@ template <typename T>
 __device__ __forceinline__ void store_element(Rsrc r, uint32_t lane, uint32_t row, T v) {
   if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, int(lane), int(row), 0);
   else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(u16, v), r, int(lane), int(row), 0);
+}
+
+// N states from `first` on, `pitch` elements apart, all loaded before the first is looked at; those past dstate are 0.
+template <int N>
+__device__ __forceinline__ void load_states(const float* __restrict__ p, int64_t pitch, int first, int dstate, float (&v)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = p[min(first + n, dstate - 1) * pitch];
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = first + n < dstate ? v[n] : 0.f;
 }
 
 struct ScanKernelArgs {
@@ -137,12 +147,10 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
     from = max(from, span.begin);
   }
   float A2[N], sum = 0.f;
-  v4f h[N / 4];
+  v4f h[N / 4] = {};
+  load_states<N>(a.A + int64_t(cc) * a.dstate, 1, first_state, a.dstate, A2);
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    A2[n] = first_state + n < a.dstate ? a.A[int64_t(cc) * a.dstate + first_state + n] * kLog2e : 0.f;
-    h[n / 4][n % 4] = 0.f;
-  }
+  for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
   const float bias = a.delta_bias != nullptr ? a.delta_bias[cc] : 0.f;
   const float skip = OUTPUT && a.D != nullptr ? a.D[cc] : 0.f;
   // the chunk's rows of u, delta, z and y; lanes past the last channel store nowhere
@@ -153,21 +161,19 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
   const Rsrc ru = make_rsrc(static_cast<const T*>(a.u) + base, bytes), rd = make_rsrc(static_cast<const T*>(a.delta) + base, bytes);
   const Rsrc rz = make_rsrc(static_cast<const T*>(has_z ? a.z : a.u) + base, bytes);
   const Rsrc ry = make_rsrc(static_cast<T*>(a.y) + base, OUTPUT ? bytes : 0u);
-  const T* B = static_cast<const T*>(a.B);
-  const T* C = static_cast<const T*>(a.C);
+  const uint32_t row_bytes = uint32_t(a.dstate) * sizeof(T), bc_bytes = uint32_t(rows.end - rows.begin) * row_bytes;
+  const Rsrc rB = make_rsrc(static_cast<const T*>(a.B) + int64_t(rows.begin) * a.dstate, bc_bytes);
+  const Rsrc rC = make_rsrc(static_cast<const T*>(a.C) + int64_t(rows.begin) * a.dstate, bc_bytes);
 
   const auto enter = [&](int32_t row) {   // the state ahead of `row`, which is in sequence s
     if (row != span.begin && !(OUTPUT && k > 0)) return;   // (k is 0 here only with offsets out of order)
+    float v[N] = {};
+    if (row != span.begin)
+      load_states<N>(a.states + int64_t(k - 1) * a.dstate * a.channels + cc, a.channels, first_state, a.dstate, v);
+    else if (a.h0 != nullptr)
+      load_states<N>(a.h0 + (int64_t(s) * a.channels + cc) * a.dstate, 1, first_state, a.dstate, v);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int32_t state = first_state + n;
-      float v = 0.f;
-      if (state < a.dstate) {
-        if (row != span.begin) v = a.states[(int64_t(k - 1) * a.dstate + state) * a.channels + cc];
-        else if (a.h0 != nullptr) v = a.h0[(int64_t(s) * a.channels + cc) * a.dstate + state];
-      }
-      h[n / 4][n % 4] = v;
-    }
+    for (int n = 0; n < N; ++n) h[n / 4][n % 4] = v[n];
   };
   const auto leave = [&]() {
     if (!OUTPUT || !live || a.h_final == nullptr) return;
@@ -222,15 +228,14 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
     return g;
   };
   // B and C of a tile of rows, by way of registers into one of the two buffers
-  float staged_b[kPer], staged_c[OUTPUT ? kPer : 1];
+  T staged_b[kPer], staged_c[OUTPUT ? kPer : 1];   // (past the chunk's rows or the states: zeros)
   const auto load_tile = [&](int32_t tile) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
-      const bool some = r < kRows && tile + r < rows.end && n < a.dstate;
-      const int64_t at = int64_t(tile + r) * a.dstate + n;
-      staged_b[i] = some ? to_f32(B[at]) : 0.f;
-      if constexpr (OUTPUT) staged_c[i] = some ? to_f32(C[at]) : 0.f;
+      const uint32_t at = n < a.dstate ? uint32_t(tile - rows.begin + r) * row_bytes + uint32_t(n) * sizeof(T) : kOutOfRange;
+      staged_b[i] = load_element<T>(rB, at, 0);
+      if constexpr (OUTPUT) staged_c[i] = load_element<T>(rC, at, 0);
     }
   };
   const auto put_tile = [&](int buffer) {
@@ -238,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
     for (int i = 0; i < kPer; ++i) {
       const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
       if (r < kRows) {
-        Bs[buffer][r][n / N][n % 4][n % N / 4] = staged_b[i];
-        if constexpr (OUTPUT) Cs[buffer][r][n] = staged_c[i];
+        Bs[buffer][r][n / N][n % 4][n % N / 4] = to_f32(staged_b[i]);
+        if constexpr (OUTPUT) Cs[buffer][r][n] = to_f32(staged_c[i]);
       }
     }
   };
@@ -347,6 +352,177 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
         a.states[(int64_t(k) * a.dstate + first_state + n) * a.channels + c] = h[n / 4][n % 4];
     if (group == 0) a.sums[int64_t(k) * a.channels + c] = sum;
   }
+}
+
+// The value of lane `from` of every four neighbouring lanes, in all of them; that of the lane whose number differs in bit 0
+// or in bit 1.
+__device__ __forceinline__ float of_lane(float v, int from) {
+  const int i = __float_as_int(v);
+  switch (from) {
+    case 0: return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x00, 0xF, 0xF, true));
+    case 1: return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x55, 0xF, 0xF, true));
+    case 2: return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0xAA, 0xF, 0xF, true));
+    default: return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0xFF, 0xF, 0xF, true));
+  }
+}
+__device__ __forceinline__ float other_of_pair(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float other_pair(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));
+}
+
+// Dense sequences walked whole by four lanes a channel, N states each.  Of four rows each of the lanes loads one, forms its
+// step size and its gate, and writes its y; the step sizes go round as lane exchanges within the products that take them.
+// Values and the next 16 rows of B and C are loaded a tile ahead: a SIMD may have one wave only (4 x 2048 x 4096 x 16: 109
+// ns a row for one wave a SIMD, 72 a wave for four).
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 2) quad_kernel(ScanKernelArgs a) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr int kStates = 4 * N, kGroups = kRows / 4;
+  constexpr int kPer = (kRows * kStates + kThreads - 1) / kThreads;   // values of B, and of C, that a thread stages
+  __shared__ __attribute__((aligned(16))) float Bs[2][kRows][kStates], Cs[2][kRows][kStates];
+  const int lane = int(threadIdx.x) % kWave, q = lane % 4, first_state = q * N;
+  const int32_t c = int32_t(blockIdx.y) * (kThreads / 4) + int32_t(threadIdx.x) / 4;
+  const bool live = c < a.channels;
+  const int32_t cc = min(c, a.channels - 1);   // lanes past the last channel compute it too and store nothing
+  const int32_t s = int32_t(blockIdx.x), length = int32_t(a.seq.length.d);
+  const int64_t base = int64_t(s) * length;
+  float A2[N], h[N] = {};
+  load_states<N>(a.A + int64_t(cc) * a.dstate, 1, first_state, a.dstate, A2);
+  if (a.h0 != nullptr) load_states<N>(a.h0 + (int64_t(s) * a.channels + cc) * a.dstate, 1, first_state, a.dstate, h);
+#pragma unroll
+  for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
+  const float bias = a.delta_bias != nullptr ? a.delta_bias[cc] : 0.f, skip = a.D != nullptr ? a.D[cc] : 0.f;
+  const bool has_z = a.z != nullptr;
+  const uint32_t pitch = uint32_t(a.channels) * sizeof(T), bytes = uint32_t(length) * pitch;
+  const uint32_t at_lane = uint32_t(q) * pitch + uint32_t(cc) * sizeof(T);
+  const Rsrc ru = make_rsrc(static_cast<const T*>(a.u) + base * a.channels, bytes);
+  const Rsrc rd = make_rsrc(static_cast<const T*>(a.delta) + base * a.channels, bytes);
+  const Rsrc rz = make_rsrc(static_cast<const T*>(has_z ? a.z : a.u) + base * a.channels, bytes);
+  const Rsrc ry = make_rsrc(static_cast<T*>(a.y) + base * a.channels, bytes);
+  const uint32_t row_bytes = uint32_t(a.dstate) * sizeof(T), bc_bytes = uint32_t(length) * row_bytes;
+  const Rsrc rB = make_rsrc(static_cast<const T*>(a.B) + base * a.dstate, bc_bytes);
+  const Rsrc rC = make_rsrc(static_cast<const T*>(a.C) + base * a.dstate, bc_bytes);
+
+  // what a lane needs of a tile of rows, loaded a tile ahead (rows past the sequence load as zero)
+  struct Tile { T u[kGroups], delta[kGroups], z[kGroups]; };
+  const auto load_values = [&](int32_t tile) {
+    Tile t;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const uint32_t at = at_lane + uint32_t(tile + 4 * g) * pitch;
+      t.u[g] = load_element<T>(ru, at, 0);
+      t.delta[g] = load_element<T>(rd, at, 0);
+      t.z[g] = load_element<T>(rz, at, 0);
+    }
+    return t;
+  };
+  T staged_b[kPer], staged_c[kPer];
+  const auto load_tile = [&](int32_t tile) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
+      const uint32_t at = n < a.dstate ? uint32_t(tile + r) * row_bytes + uint32_t(n) * sizeof(T) : kOutOfRange;
+      staged_b[i] = load_element<T>(rB, at, 0);
+      staged_c[i] = load_element<T>(rC, at, 0);
+    }
+  };
+  const auto put_tile = [&](int buffer) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = int(threadIdx.x) + i * kThreads, r = e / kStates, n = e % kStates;
+      if (r < kRows) {
+        Bs[buffer][r][n] = to_f32(staged_b[i]);
+        Cs[buffer][r][n] = to_f32(staged_c[i]);
+      }
+    }
+  };
+  // a row of B and C, the lane's states
+  struct Row { float b[N], c[N]; };
+  const auto read_row = [&](int buffer, int r) __attribute__((always_inline)) {
+    Row t;
+    __builtin_memcpy(t.b, __builtin_assume_aligned(&Bs[buffer][r][first_state], N == 2 ? 8 : 16), sizeof(t.b));
+    __builtin_memcpy(t.c, __builtin_assume_aligned(&Cs[buffer][r][first_state], N == 2 ? 8 : 16), sizeof(t.c));
+    return t;
+  };
+  // one token: d its step size, dv that times u; returns the lane's part of C . h
+  const auto token = [&](float d, float dv, const Row& t) __attribute__((always_inline)) {
+    float out = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], dv * t.b[n]);
+      out = n == 0 ? t.c[0] * h[0] : fmaf(t.c[n], h[n], out);
+    }
+    return out;
+  };
+  struct Step { float d, dv, v, gate; };   // of the lane's row
+  const auto prepare = [&](const Tile& t, int g) __attribute__((always_inline)) {
+    Step p;
+    p.v = to_f32(t.u[g]);
+    const float raw = to_f32(t.delta[g]) + bias, soft = softplus<EXACT>(raw), open = silu<EXACT>(to_f32(t.z[g]));
+    p.d = a.softplus ? soft : raw;
+    p.dv = p.d * p.v;
+    p.gate = has_z ? open : 1.f;
+    return p;
+  };
+  // y of four rows: lane q gets row q's sum over the four lanes
+  const auto finish = [&](const float (&out)[4], const Step& p, int32_t row0) __attribute__((always_inline)) {
+    const bool odd = q & 1, high = q & 2;
+    const float low_rows = (odd ? out[1] : out[0]) + other_of_pair(odd ? out[0] : out[1]);
+    const float high_rows = (odd ? out[3] : out[2]) + other_of_pair(odd ? out[2] : out[3]);
+    const float read = (high ? high_rows : low_rows) + other_pair(high ? low_rows : high_rows);
+    store_element(ry, live ? at_lane + uint32_t(row0) * pitch : kOutOfRange, 0, from_f32<T>(fmaf(skip, p.v, read) * p.gate));
+  };
+
+  load_tile(0);
+  Tile ahead = load_values(0);
+  put_tile(0);
+  int buffer = 0;
+  for (int32_t tile = 0; tile < length; tile += kRows, buffer ^= 1) {
+    __syncthreads();   // the tile is in LDS, and the buffer of the one before is free
+    const bool more = tile + kRows < length;
+    const Tile now = ahead;
+    if (more) {
+      load_tile(tile + kRows);
+      ahead = load_values(tile + kRows);
+    }
+    if (tile + kRows <= length) {
+      Step p = prepare(now, 0);
+      Row t = read_row(buffer, 0);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const Step next_p = prepare(now, g + 1 < kGroups ? g + 1 : g);
+        float out[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const Row next = read_row(buffer, 4 * g + r + 1 < kRows ? 4 * g + r + 1 : 0);
+          out[r] = token(of_lane(p.d, r), of_lane(p.dv, r), t);
+          t = next;
+        }
+        finish(out, p, tile + 4 * g);
+        p = next_p;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int32_t row0 = tile + 4 * g;
+        if (row0 >= length) break;
+        const Step p = prepare(now, g);
+        float out[4] = {};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (row0 + r < length) out[r] = token(of_lane(p.d, r), of_lane(p.dv, r), read_row(buffer, 4 * g + r));
+        finish(out, p, row0);
+      }
+    }
+    if (more) put_tile(buffer ^ 1);
+  }
+  if (!live || a.h_final == nullptr) return;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (first_state + n < a.dstate)
+      a.h_final[(int64_t(s) * a.channels + c) * a.dstate + first_state + n] = h[n];
 }
 
 constexpr int kCarried = 16;
@@ -465,6 +641,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(float* __restrict__ stat
 // ---- host ----
 
 struct Plan {
+  bool quad;   // quad_kernel: sequences are the chunks
   int32_t chunk, per_sequence, chunks;
   size_t sums, resets, bytes;   // byte offsets behind the states, and the total
 };
@@ -473,15 +650,32 @@ constexpr int64_t kSimds = 1024;   // of a whole chip; the workspace's size does
 
 constexpr int state_groups(int32_t dstate) { return dstate <= 16 ? 1 : dstate <= 32 ? 2 : 4; }
 
-// How long a chunk is.  Where the sequences and channels alone give every SIMD a wave they are walked whole, in one pass.
-// Otherwise the walk is made twice, in as many chunks as fill the three waves that a SIMD holds a whole number of times; a
+// Microseconds by both ways, for up to 8, 16, 32 and 64 states.  quad_kernel: a row takes `row` and `wave` more for every
+// wave that a SIMD holds.  Chunks: kLaunches for three kernels, and `work` for a row of 16 x 1024 channels.  Measured, quad
+// and chunks: 2048 x 4096 x 16 states with 2 sequences 219 and 144, with 4 223 and 257, with 8 344 and 467; 1 x 128 x 4096
+// 17 and 28, 1 x 512 x 8192 58 and 64, 1001 x 1024 110 and 34; 2 x 2048 x 4096 with 8 states 164 and 94, with 32 332 and
+// 304, with 64 531 and 537.
+struct Costs { double row, wave, work; };
+constexpr Costs kCosts[] = {{0.036, 0.046, 0.080}, {0.050, 0.058, 0.115}, {0.076, 0.088, 0.28}, {0.100, 0.165, 0.52}};
+constexpr double kLaunches = 25.;
+
+bool quads_win(int64_t length, int64_t chains, int32_t channels, int32_t dstate) {
+  const Costs& c = kCosts[dstate <= 8 ? 0 : dstate <= 16 ? 1 : dstate <= 32 ? 2 : 3];
+  const int64_t waves = chains * ((int64_t(channels) + 15) / 16);
+  const double quad = double(length) * (c.row + c.wave * double((waves + kSimds - 1) / kSimds));
+  return quad <= kLaunches + double(length) * double(waves) / kSimds * c.work;
+}
+
+// Which way, and how long a chunk is: as many chunks as fill the three waves that a SIMD holds a whole number of times; a
 // chunk has 16 to 256 rows (carried states are traffic, and the sum of d is kept precise).
 bool make_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed, Plan* p) {
   const int64_t length = packed ? tokens : tokens / sequences, chains = packed ? 1 : sequences;
-  const int64_t waves = chains * ((int64_t(channels) + kWave - 1) / kWave) * state_groups(dstate);
-  const bool reach = length * channels < (int64_t(1) << 29);   // a chunk's rows are addressed in 32 bits
+  // a sequence's rows are addressed in 32 bits
+  p->quad = !packed && length > 0 && length * std::max(channels, dstate) < int64_t(1) << 29 &&
+            quads_win(length, chains, channels, dstate);
   int64_t chunk = std::max<int64_t>(length, 1);
-  if (waves < kSimds || !reach) {
+  if (!p->quad) {
+    const int64_t waves = chains * ((int64_t(channels) + kWave - 1) / kWave) * state_groups(dstate);
     const int64_t least = (length + 255) / 256, rounds = (least * waves + 3 * kSimds - 1) / (3 * kSimds);
     const int64_t number = std::max(least, rounds * 3 * kSimds / waves);
     chunk = number > 0 ? (length + number - 1) / number : 1;
@@ -522,8 +716,22 @@ hipError_t launch_states(const ScanKernelArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <typename T, int N>
+hipError_t launch_quad(const ScanKernelArgs& a, hipStream_t stream) {
+  quad_kernel<T, N><<<dim3(a.seq.sequences, (a.channels + kThreads / 4 - 1) / (kThreads / 4)), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T>
-hipError_t launch_scan(const ScanKernelArgs& a, hipStream_t stream) {
+hipError_t launch_scan(const ScanKernelArgs& a, bool quad, hipStream_t stream) {
+  if (quad) {
+    if (a.dstate <= 8) return launch_quad<T, 2>(a, stream);
+    switch (state_groups(a.dstate)) {
+      case 1: return launch_quad<T, 4>(a, stream);
+      case 2: return launch_quad<T, 8>(a, stream);
+      default: return launch_quad<T, 16>(a, stream);
+    }
+  }
   if (a.dstate <= 8) return launch_states<T, 8, 1>(a, stream);
   switch (state_groups(a.dstate)) {
     case 1: return launch_states<T, 16, 1>(a, stream);
@@ -584,9 +792,9 @@ hipError_t launch_selective_scan(const SelectiveArgs& s, hipStream_t stream) {
   a.chunks = p.chunks;
   a.softplus = s.softplus;
   switch (s.dtype) {
-    case SSDQ_DTYPE_F32: return launch_scan<float>(a, stream);
-    case SSDQ_DTYPE_F16: return launch_scan<_Float16>(a, stream);
-    default: return launch_scan<__bf16>(a, stream);
+    case SSDQ_DTYPE_F32: return launch_scan<float>(a, p.quad, stream);
+    case SSDQ_DTYPE_F16: return launch_scan<_Float16>(a, p.quad, stream);
+    default: return launch_scan<__bf16>(a, p.quad, stream);
   }
 }
 

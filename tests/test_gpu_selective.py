@@ -94,7 +94,8 @@ class Scan:
 @pytest.mark.parametrize("batch,length,channels,n", [
     (1, 1, 1, 1), (1, 1, 64, 16), (3, 2, 65, 16), (2, 15, 33, 13), (1, 16, 256, 8), (2, 17, 300, 16), (1, 255, 70, 16),
     (1, 256, 64, 5), (3, 257, 64, 16), (1, 700, 130, 16), (2, 1025, 40, 16), (1, 300, 96, 32), (1, 290, 50, 64), (2, 530, 20, 41),
-    (70, 9, 129, 16)])
+    (70, 9, 129, 16), (2, 37, 70, 33), (1, 50, 130, 64), (3, 61, 40, 20), (1, 100, 33, 7), (1, 64, 65, 16), (2, 97, 17, 2),
+    (16, 171, 1025, 9), (8, 400, 20, 64)])
 def test_dense(dtype, batch, length, channels, n):
     Scan(length, dtype, batch, batch * length, channels, n).check()
 
