@@ -687,9 +687,9 @@ ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale,
  *   state_out : (sequences, width - 1, channels) of dtype or NULL, written: the inputs of each sequence's last width - 1
  *               tokens, oldest first (of state where it has fewer); it must not be state
  * width 2, 3 or 4; sequences, channels >= 1; tokens >= 0, dense a multiple of sequences (else SSDQ_ERROR_INVALID_VALUE);
- * tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20 and ceil(channels / 256) * (sequences + tokens / 16 + 1) < 2^25
- * (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of order
- * give unspecified results but no access outside the tensors.  No output overlaps an input.
+ * tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20 and ceil(channels / 256) * (sequences + tokens / 16 + 1) <
+ * 2^25 (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of
+ * order give unspecified results but no access outside the tensors.  No output overlaps an input.
  */
 ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, const float* bias, const void* state,
                              const int32_t* offsets, void* out, void* state_out, int32_t sequences, int64_t tokens,
@@ -730,9 +730,9 @@ size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int
  * sequences >= 1, tokens >= 0, channels >= 1, 1 <= dstate <= 64; dense tokens a multiple of sequences (else
  * SSDQ_ERROR_INVALID_VALUE); tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20, a workspace below 2^40 bytes and
  * fewer than 2^23 pieces that the kernels walk the sequences in: 16 to 256 tokens of a sequence each, or a whole one
- * (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With
- * tokens == 0 the (tokens, ...) pointers are not looked at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence and
- * channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
+ * (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With tokens == 0 the (tokens, ...) pointers are not
+ * looked at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence
+ * and channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
  * products of it over 256 neighbouring tokens stay finite.  The result does not depend on timing: calls with the same
  * arguments give the same bits.
  */

@@ -103,7 +103,8 @@ __device__ __forceinline__ Taps<T> state_row(const ConvKernelArgs& a, int64_t s,
 
 template <typename T, int W, bool PAST>
 __global__ void __launch_bounds__(kThreads) causal_conv_kernel(ConvKernelArgs a) {
-  const uint32_t unit = uint32_t(__builtin_amdgcn_readfirstlane(int(blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave)));
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const uint32_t unit = blockIdx.x * uint32_t(kThreads / kWave) + uint32_t(wave);
   const uint32_t item = fdiv(unit, a.blocks);
   if (item >= a.items) return;
   const int c = int(unit - item * a.blocks.d) * kWaveChannels + int(threadIdx.x % kWave) * V;
@@ -145,7 +146,8 @@ __global__ void __launch_bounds__(kThreads) causal_conv_kernel(ConvKernelArgs a)
 #pragma unroll
       for (int k = 0; k + 1 < W; ++k) window[k] = x_of[r + k];
       if (first + r < last)
-        store_taps<PAST>(out + int64_t(first + r) * a.channels + c, count, convolve<T, W>(window, x_of[r + W - 1], w, b, a.silu));
+        store_taps<PAST>(out + int64_t(first + r) * a.channels + c, count,
+                         convolve<T, W>(window, x_of[r + W - 1], w, b, a.silu));
     }
     return;
   }
@@ -239,11 +241,10 @@ hipError_t launch_step(void* state, const void* x, const float* weight, const fl
   T* st = static_cast<T*>(state);
   const T* in = static_cast<const T*>(x);
   T* o = static_cast<T*>(out);
-  switch (width) {
-    case 2: causal_conv_step_kernel<T, 2><<<grid, kThreads, 0, stream>>>(st, in, weight, bias, o, units, packs, channels, silu); break;
-    case 3: causal_conv_step_kernel<T, 3><<<grid, kThreads, 0, stream>>>(st, in, weight, bias, o, units, packs, channels, silu); break;
-    default: causal_conv_step_kernel<T, 4><<<grid, kThreads, 0, stream>>>(st, in, weight, bias, o, units, packs, channels, silu);
-  }
+  const auto kernel = width == 2   ? causal_conv_step_kernel<T, 2>
+                      : width == 3 ? causal_conv_step_kernel<T, 3>
+                                   : causal_conv_step_kernel<T, 4>;
+  kernel<<<grid, kThreads, 0, stream>>>(st, in, weight, bias, o, units, packs, channels, silu);
   return hipGetLastError();
 }
 

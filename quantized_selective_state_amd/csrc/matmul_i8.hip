@@ -5,9 +5,9 @@
 // channels of one token and stores them together.
 //
 // Three kernels: few tokens are bound by the weights' bytes and streamed (1 x 4096 x 18560 15 us, 5.0 TB/s); many tokens
-// by the matrix units, whose clock the card's power limits on codes that are not zeros (32768 x 4096 x 18560 2.05 ms, 2.4
-// POP/s; out of registers alone random codes reach 3.4 to 4.0, zeros 4.8); inner sizes that no 16 divides by their unaligned
-// loads (777 x 1531 x 1000 15 us).
+// by the matrix units and LDS together, which the tiles need for equally many cycles, at a clock that power limits (32768
+// x 4096 x 18560 2.05 ms, 2.4 POP/s: matrix units at work in 58% of the cycles, at 1.9 GHz; out of registers alone random
+// codes reach 3.4 to 4.0, zeros 4.8); inner sizes that no 16 divides by their unaligned loads (777 x 1531 x 1000 14 us).
 #include <algorithm>
 
 #include "block_internal.h"
@@ -368,8 +368,9 @@ struct Store {
 };
 
 // WM x WN waves, kStages slabs in LDS.  Between two barriers every wave reads a slab's operands and multiplies them.  The
-// largest tiles read the fewest bytes of LDS per product: 256 x 256 in 8 waves has matrix units and LDS busy for about as
-// long, 64 x 64 is bound by LDS and by what a compute unit can load (256 x 8192 x 4096 17 to 21 us, 0.9 POP/s).  With
+// largest tiles read the fewest bytes of LDS per product: a slab of 256 x 256 in 8 waves takes the matrix units and LDS
+// (reads and arriving loads) 2048 cycles each; 64 x 64 is bound by LDS and by what a compute unit can load (256 x 8192 x
+// 4096 16.5 to 20 us, 1 POP/s).  With
 // kSplit 2 there are twice the waves, and the halves of them walk half of the inner axis each: two waves on every SIMD for
 // tiles that are too few to give a compute unit a second one.
 template <typename T, int TM, int TN, int WM, int WN, int kStages, int kSplit>
@@ -430,20 +431,25 @@ __global__ void __launch_bounds__(WM * WN * kSplit * kWave) tile_kernel(TileArgs
 }
 
 // Inner sizes of any number of codes: rows may start at any byte, so the pieces pass through registers, those of the next
-// slabs while the current one is multiplied (loads of 16 bytes at any address; the aligned words that hold them, shifted,
-// take longer: 777 x 1531 x 1000 18.2 us against 15.3).  A row's last slab is loaded code by code.  Square tiles, 4 waves,
-// of 128 once there is one for every compute unit (8192 x 4097 x 8192 501 us, 862 with 64), else of 64.
-template <typename T, int kSide>
-__global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restrict__ out) {
+// slabs while the current one is multiplied (loads of 16 bytes at any address, which take five times as long as aligned
+// ones and bound the kernel; the aligned words that hold them, shifted, take longer still: 777 x 1531 x 1000 18.2 us
+// against 14.8).  A row's last slab is loaded code by code.  Square tiles, 4 waves, of 128 once there is one for every
+// compute unit (8192 x 4097 x 8192 501 us, 862 with 64), else of 64; those no more than compute units in two halves of
+// the inner axis as above (777 x 1531 x 1000 14.8 and 13.8 us so, 64 x 8190 x 4096 46.5 and 37.2, 300 x 100 x 700 9.7 and
+// 9.8).
+template <typename T, int kSide, int kSplit>
+__global__ void __launch_bounds__(256 * kSplit) ragged_kernel(TileArgs args, T* __restrict__ out) {
   constexpr int kThreads = 256, kPieces = 2 * kSide * kSlab / 16 / kThreads, F = kSide / 32;
   constexpr int kSets = kSide == 64 ? 2 : 1;   // slabs in registers
   typedef Store<T, F, F> Put;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2][2 * kSide * kSlab];
+  __shared__ __attribute__((aligned(16))) int8_t lds[kSplit][2][2 * kSide * kSlab];
   __shared__ __attribute__((aligned(16))) int8_t results[4][Put::kRoom];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  __shared__ v4i sums[kSplit > 1 ? 4 : 1][kSplit > 1 ? F * F : 1][kWave];
+  const int lane = threadIdx.x % kWave, of_block = __builtin_amdgcn_readfirstlane(int(threadIdx.x / kWave));
+  const int group = of_block / 4, wave = of_block % 4, thread = threadIdx.x % kThreads;
   const Walk<kSide, kSide> walk(args);
-  const int wm = (wave % 2) * (kSide / 2), wn = (wave / 2) * (kSide / 2), piece = threadIdx.x % 8;
-  const int32_t slabs = (args.k + kSlab - 1) / kSlab;
+  const int wm = (wave % 2) * (kSide / 2), wn = (wave / 2) * (kSide / 2), piece = thread % 8;
+  const int32_t slabs = ((args.k + kSlab - 1) / kSlab + kSplit - 1) / kSplit;   // (the last may be past k: zeros)
   for (uint32_t t = blockIdx.x / 8; t < walk.run; t += walk.stride) {
     int64_t m0;
     int32_t n0;
@@ -452,11 +458,12 @@ __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restric
     v4i pieces[kSets][kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int r = int(threadIdx.x) / 8 + i * (kThreads / 8);   // the tokens' rows, then the channels'
+      const int r = thread / 8 + i * (kThreads / 8);   // the tokens' rows, then the channels'
       row[i] = r < kSide ? args.a + min(m0 + r, args.m - 1) * args.k
                          : args.b + int64_t(min(n0 + r - kSide, args.n - 1)) * args.k;
     }
-    const auto load = [&](int32_t slab, int set) __attribute__((always_inline)) {
+    const auto load = [&](int32_t of_group, int set) __attribute__((always_inline)) {
+      const int32_t slab = group * slabs + of_group;
       if ((slab + 1) * kSlab <= args.k) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) __builtin_memcpy(&pieces[set][i], row[i] + slab * kSlab + piece * 16, 16);
@@ -467,10 +474,10 @@ __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restric
     };
     v4i acc[F][F] = {};
     const auto multiply = [&](int32_t slab, int set) __attribute__((always_inline)) {
-      int8_t* rows = lds[slab & 1];
+      int8_t* rows = lds[group][slab & 1];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int r = int(threadIdx.x) / 8 + i * (kThreads / 8);
+        const int r = thread / 8 + i * (kThreads / 8);
         *reinterpret_cast<v4i*>(rows + r * kSlab + place_of_piece(r, piece) * 16) = pieces[set][i];
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -487,7 +494,23 @@ __global__ void __launch_bounds__(256) ragged_kernel(TileArgs args, T* __restric
       multiply(slab, 0);
       if (kSets > 1 && slab + 1 < slabs) multiply(slab + 1, kSets - 1);
     }
-    Put::run(acc, args, out, results[wave], lane, m0 + wm, n0 + wn);
+    if constexpr (kSplit > 1) {
+      if (group == 1) {
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int i = 0; i < F; ++i) sums[wave][j * F + i][lane] = acc[j][i];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      barrier();
+      if (group == 0) {
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int i = 0; i < F; ++i) acc[j][i] += sums[wave][j * F + i][lane];
+      }
+    }
+    if (group == 0) Put::run(acc, args, out, results[wave], lane, m0 + wm, n0 + wn);
     barrier();   // the next tile's first slab goes over one that other waves may still read
   }
 }
@@ -534,15 +557,19 @@ int choose(const MatmulArgs& a) {
 template <typename T>
 hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   const Epilogue ep = {a.a_scale, a.b_scale, a.bias, a.per_row};
+  const int64_t tiles = (a.m + 63) / 64 * ((int64_t(a.n) + 63) / 64);   // of the smallest size
   if (a.k % 16 != 0) {
     if (a.m <= 16 && a.n <= 1 << 24) return launch_stream<T, 1, true>(a, ep, stream);
     uint32_t blocks;
     if ((a.m + 127) / 128 * ((int64_t(a.n) + 127) / 128) >= compute_units()) {
       const TileArgs args = tile_args<128, 128>(a, ep, 2, &blocks);
-      ragged_kernel<T, 128><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
-    } else {
+      ragged_kernel<T, 128, 1><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+    } else if (tiles > compute_units()) {
       const TileArgs args = tile_args<64, 64>(a, ep, 3, &blocks);
-      ragged_kernel<T, 64><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+      ragged_kernel<T, 64, 1><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
+    } else {
+      const TileArgs args = tile_args<64, 64>(a, ep, 1, &blocks);
+      ragged_kernel<T, 64, 2><<<dim3(blocks), 512, 0, stream>>>(args, static_cast<T*>(a.out));
     }
     return hipGetLastError();
   }
@@ -559,7 +586,6 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   }
   // no more tiles than compute units: two halves of the inner axis in each (256 x 4096 x 4096 12.9 us and 11.2 so;
   // 64 x 4096 x 18560, 290 tiles, 24.0 and 24.5)
-  const int64_t tiles = (a.m + 63) / 64 * ((int64_t(a.n) + 63) / 64);
   if (tiles <= compute_units()) return launch_tiles<T, 64, 64, 2, 2, 4, 2>(a, ep, 1, stream);
   return launch_tiles<T, 64, 64, 2, 2, 4>(a, ep, kCandidates[3].per_unit, stream);
 }
