@@ -689,7 +689,7 @@ ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale,
  * width 2, 3 or 4; sequences, channels >= 1; tokens >= 0, dense a multiple of sequences (else SSDQ_ERROR_INVALID_VALUE);
  * tokens < 2^31 - 2^16, sequences < 2^24, channels <= 2^20 and ceil(channels / 256) * (sequences + tokens / 16 + 1) <
  * 2^25 (else SSDQ_ERROR_UNSUPPORTED).  With tokens == 0 x and out are not looked at.  Offsets out of range or out of
- * order give unspecified results but no access outside the tensors.  No output overlaps an input.
+ * order give unspecified results but no access outside the tensors.  No output overlaps an input (out on x is refused).
  */
 ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, const float* bias, const void* state,
                              const int32_t* offsets, void* out, void* state_out, int32_t sequences, int64_t tokens,

@@ -139,7 +139,8 @@ ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, 
   if (!ok_ptr(weight) || !ok_opt(bias) || !ok_opt(state) || !ok_opt(offsets) || !ok_opt(state_out))
     return SSDQ_ERROR_INVALID_VALUE;
   if (tokens > 0 && (!ok_ptr(x) || !ok_ptr(out))) return SSDQ_ERROR_INVALID_VALUE;
-  if (state != nullptr && state == state_out) return SSDQ_ERROR_INVALID_VALUE;
+  // neighbouring waves read the rows ahead of their own
+  if ((tokens > 0 && x == out) || (state != nullptr && state == state_out)) return SSDQ_ERROR_INVALID_VALUE;
   const ConvArgs a = {dtype, x, weight, bias, state, offsets, out, state_out, sequences, tokens, channels, width,
                       silu != 0};
   return launched(launch_causal_conv(a, stream));

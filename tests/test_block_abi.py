@@ -67,13 +67,13 @@ def test_matmul_refusals(over, status):
     (dict(tokens=-1), INVALID), (dict(channels=0), INVALID), (dict(sequences=3), INVALID), (dict(x=None), INVALID),
     (dict(x=ODD), INVALID), (dict(weight=None), INVALID), (dict(bias=ODD), INVALID), (dict(state=ODD), INVALID),
     (dict(offsets=ODD), INVALID), (dict(out=None), INVALID), (dict(state_out=ODD), INVALID),
-    (dict(state_out=A), INVALID), (dict(tokens=1 << 31, sequences=1), UNSUPPORTED),
+    (dict(state_out=A), INVALID), (dict(out=A), INVALID), (dict(tokens=1 << 31, sequences=1), UNSUPPORTED),
     (dict(channels=(1 << 20) + 1), UNSUPPORTED), (dict(sequences=1 << 24, tokens=1 << 24), UNSUPPORTED),
     (dict(channels=1 << 20, tokens=1 << 30, sequences=1), UNSUPPORTED),
     (dict(channels=64, tokens=(1 << 29) - 32, sequences=1), UNSUPPORTED),   # 2^25 - 2 runs of 16 rows, a state, one more
     (dict(channels=64, tokens=(1 << 29) - 48, sequences=1, x=None), INVALID)])
 def test_conv_refusals(over, status):
-    a = dict(dtype=1, x=A, weight=A, bias=A, state=A, offsets=None, out=A, state_out=2 * A, sequences=2, tokens=8,
+    a = dict(dtype=1, x=A, weight=A, bias=A, state=A, offsets=None, out=3 * A, state_out=2 * A, sequences=2, tokens=8,
              channels=64, width=4, silu=1)
     a.update(over)
     assert ssdq.lib.ssdq_causal_conv(*a.values(), None) == status
