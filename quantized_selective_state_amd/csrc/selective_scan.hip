@@ -11,8 +11,8 @@
 // staged as binary32 in LDS.
 //
 // Bound by the vector units, not by memory: a token, channel and state costs an exp2 (a third of the rate of an fma), two
-// products, an fma into the state and one into y.  With 16 states, bf16: 4 x 2048 x 4096 223 us (its bytes would take 54; in
-// chunks 257), 16 x 2048 x 8192 1071 us (4.0e12 tokens x channels x states a second).  16384 x 5120 fp16, in chunks, 584 us.
+// products, an fma into the state and one into y.  With 16 states, bf16: 4 x 2048 x 4096 219 us (its bytes would take 54; in
+// chunks 255), 16 x 2048 x 8192 1050 us (4.1e12 tokens x channels x states a second).  16384 x 5120 fp16, in chunks, 577 us.
 // 4 x 2048 x 4096 with 64 states 535 us (in chunks 1255).
 #include "block_internal.h"
 #include "gated_types.h"
@@ -26,21 +26,13 @@ constexpr int kRows = 16;            // rows of B and C in LDS at a time
 constexpr int kGroup = 4;            // rows whose values are loaded together, one group ahead
 constexpr float kLog2e = 1.44269502e+00f;
 
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|); log(1 + e) = e P(e) with a polynomial fitted to it on [0, 1] (within
-// 2.3 half places of itself in binary32), so that also small step sizes keep their relative precision.  -inf gives 0.
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|).  With w the rounded 1 + e, log(1 + e) is log(w) and about what the
+// rounding left, e - (w - 1): wrong by no more than 2^-24 of itself, so that also small step sizes keep their relative
+// precision.  -inf gives 0.
 template <bool EXACT>
 __device__ __forceinline__ float softplus(float v) {
-  const float e = exp_f32<EXACT>(fmaxf(-fabsf(v), -104.f));
-  float p = 0.0051058256f;
-  p = fmaf(p, e, -0.028991956f);
-  p = fmaf(p, e, 0.077380739f);
-  p = fmaf(p, e, -0.135905996f);
-  p = fmaf(p, e, 0.190713093f);
-  p = fmaf(p, e, -0.248339459f);
-  p = fmaf(p, e, 0.333179355f);
-  p = fmaf(p, e, -0.499994367f);
-  p = fmaf(p, e, 0.99999994f);
-  return fmaf(p, e, v < 0.f ? 0.f : v);   // (a NaN stays one)
+  const float e = exp_f32<EXACT>(-fabsf(v)), w = 1.f + e, left = e - (w - 1.f);
+  return fmaf(__builtin_amdgcn_logf(w), 6.93147182e-01f, left) + fmaxf(v, 0.f);   // (a NaN stays one: e is one)
 }
 template <bool EXACT>
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + exp_f32<EXACT>(-z)); }
@@ -104,7 +96,7 @@ __device__ __forceinline__ Span chunk_rows(const ScanKernelArgs& a, int32_t k) {
 // channels of the lanes, an outer product of 4 states of B and d u, added to 4 registers of each lane.  That takes an fma
 // and the read of B in every lane off the vector units (a row of 64 channels x 16 states, in cycles of a wave on its own:
 // 318 against 365 with fma, with y 398 against 445; the instruction's sums are binary32 like an fma's).  Vector units are
-// at work in 87 and 88% of the cycles (16384 x 5120 fp16: 262 us without y, 355 with it).
+// at work in 87 and 88% of the cycles (16384 x 5120 fp16: 258 us without y, 347 with it).
 template <typename T, int N, int G, bool OUTPUT>
 __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKernelArgs a) {
   constexpr bool EXACT = sizeof(T) == 4;

@@ -143,10 +143,11 @@ def test_sequences_without_tokens_keep_their_state():
     assert torch.equal(final, h0)
 
 
+@pytest.mark.parametrize("length", [600, 118])                               # in chunks, and whole
 @pytest.mark.parametrize("dtype", TYPES)
-def test_extreme_steps(dtype):
+def test_extreme_steps(dtype, length):
     """Step sizes from the far ends of softplus: states that forget at once, and ones that never do."""
-    d = Scan(8, dtype, 1, 600, 64, 16)
+    d = Scan(8, dtype, 1, length, 64, 16)
     d.delta.view(-1, 64)[:, :20] = 40.0
     d.delta.view(-1, 64)[:, 20:40] = -30.0
     d.delta.view(-1, 64)[100:110, 40:] = 1000.0
@@ -169,24 +170,27 @@ def test_softplus_of_every_size():
     assert off.max() <= 8 * ref.E                                            # what ref.scan assumes of d
 
 
+@pytest.mark.parametrize("length", [600, 118])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_what_is_not_finite_stays(dtype):
-    d = Scan(11, dtype, 3, 3 * 600, 80, 16)
+def test_what_is_not_finite_stays(dtype, length):
+    d = Scan(11, dtype, 3, 3 * length, 80, 16)
     clean, clean_final = d.run()
-    d.u[0, 300, 7], d.delta[0, 300, 9], d.z[1, 5, 3] = float("nan"), float("nan"), float("nan")
-    d.B[2, 400, 2] = float("inf")
+    half, later = length // 2, length * 2 // 3
+    d.u[0, half, 7], d.delta[0, half, 9], d.z[1, 5, 3] = float("nan"), float("nan"), float("nan")
+    d.B[2, later, 2] = float("inf")
     d.h0[1, 11, 4] = float("nan")
     y, final = d.run()
     bad = torch.zeros_like(y, dtype=torch.bool)
-    bad[0, 300:, 7] = bad[0, 300:, 9] = bad[1, 5, 3] = bad[1, :, 11] = bad[2, 400:] = True
+    bad[0, half:, 7] = bad[0, half:, 9] = bad[1, 5, 3] = bad[1, :, 11] = bad[2, later:] = True
     assert not torch.isfinite(y[bad]).any() and torch.equal(y[~bad], clean[~bad])
     assert torch.isnan(final[0, 7]).all() and torch.isnan(final[0, 9]).all() and torch.equal(final[0, 10], clean_final[0, 10])
     assert torch.isnan(final[1, 11, 4]) and torch.equal(final[1, 11, 5:], clean_final[1, 11, 5:])
 
 
-def test_same_bits_every_time_and_any_workspace():
-    d = Scan(12, "bf16", 2, 2 * 3000, 300, 16)
-    need = lib().selective_scan_workspace_size(2, 6000, 300, 16)
+@pytest.mark.parametrize("sequences,length", [(2, 3000), (90, 70)])
+def test_same_bits_every_time_and_any_workspace(sequences, length):
+    d = Scan(12, "bf16", sequences, sequences * length, 300, 16)
+    need = lib().selective_scan_workspace_size(sequences, sequences * length, 300, 16)
     y, final = d.run(workspace=torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV))
     for _ in range(3):
         again, final2 = d.run()
