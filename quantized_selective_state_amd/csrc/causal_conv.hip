@@ -4,8 +4,8 @@
 // HBM-bound: one read and one write per element (4 x 2048 x 4096 bf16 29 us, 4.6 TB/s; 16384 x 5120 fp16 73 us, 4.6
 // TB/s).  A lane holds 4 neighbouring channels of a run of 16 rows and the width - 1 rows before it, all loaded before the
 // first is used, so a row is read once and (width - 1) / 16 times more, from cache (rows loaded one by one: 136 us at
-// 16384 x 5120).  Runs are cut at multiples of their rows in the whole tensor, whatever the sequences are; those that a
-// sequence begins or ends within are walked row by row.  The weights of a wave's channels are loaded once per run.
+// 16384 x 5120; with a branch at every row's end 111).  Runs are cut at multiples of their rows in the whole tensor,
+// whatever the sequences are; those that a sequence begins or ends within decide row by row.
 #include "block_internal.h"
 #include "gated_types.h"
 #include "sequences.h"
@@ -17,6 +17,7 @@ constexpr int V = 4;
 constexpr int kRun = 16;       // rows of a wave
 constexpr int kThreads = 256;
 constexpr int kWaveChannels = kWave * V;
+constexpr int kNoLoads = 0x0F70;   // s_waitcnt: no memory operation under way, whatever LDS has
 
 struct ConvKernelArgs {
   Sequences seq;
@@ -107,9 +108,11 @@ __global__ void __launch_bounds__(kThreads) causal_conv_kernel(ConvKernelArgs a)
   const uint32_t unit = blockIdx.x * uint32_t(kThreads / kWave) + uint32_t(wave);
   const uint32_t item = fdiv(unit, a.blocks);
   if (item >= a.items) return;
-  const int c = int(unit - item * a.blocks.d) * kWaveChannels + int(threadIdx.x % kWave) * V;
+  int c = int(unit - item * a.blocks.d) * kWaveChannels + int(threadIdx.x % kWave) * V;
+  if (c >= a.channels) return;
+  // a last lane with fewer channels moves back and writes some of its neighbour's too, the same values
+  if (a.channels >= V) c = min(c, a.channels - V);
   const int count = a.channels - c;
-  if (count <= 0) return;
   const T* x = static_cast<const T*>(a.x);
   if (item >= a.runs) {   // the inputs of a sequence's last W - 1 tokens
     const int64_t s = item - a.runs;
@@ -127,53 +130,61 @@ __global__ void __launch_bounds__(kThreads) causal_conv_kernel(ConvKernelArgs a)
   const int32_t first = int32_t(item) * kRun, last = min(first + kRun, a.seq.tokens);
   float w[V][W], b[V];
   load_weights<W>(a.weight, a.bias, c, count, w, b);
-  Taps<T> window[W - 1];
-  int32_t s = a.seq.at(first);
   T* out = static_cast<T*>(a.out);
-  const Span whole = a.seq.span(s);
-  if (whole.begin <= first && last <= whole.end) {
-    constexpr int R = kRun;
-    Taps<T> x_of[R + W - 1];
+  Taps<T> x_of[kRun + W - 1];
+  int32_t s = a.seq.at(first);
+  Span span = a.seq.span(s);
+  if (a.channels >= V && last - first == kRun && span.begin <= first && last <= span.end) {
+    // One sequence: straight through.  Behind a branch a wave would wait for its earlier stores too.
 #pragma unroll
-    for (int i = 0; i < R + W - 1; ++i) {
-      const int32_t source = first - (W - 1) + i;
-      if (source >= whole.begin) x_of[i] = load_taps(x + int64_t(min(source, last - 1)) * a.channels + c, count);
-      else x_of[i] = state_row<T, W>(a, s, source - whole.begin + W - 1, c, count);
+    for (int i = W - 1; i < kRun + W - 1; ++i) x_of[i] = load_taps(x + int64_t(first - (W - 1) + i) * a.channels + c, V);
+    if (span.begin <= first - (W - 1)) {
+#pragma unroll
+      for (int i = 0; i + 1 < W; ++i) x_of[i] = load_taps(x + int64_t(first - (W - 1) + i) * a.channels + c, V);
+    } else {
+#pragma unroll
+      for (int i = 0; i + 1 < W; ++i) {
+        const int32_t source = first - (W - 1) + i;
+        if (source >= span.begin) x_of[i] = load_taps(x + int64_t(source) * a.channels + c, V);
+        else x_of[i] = state_row<T, W>(a, s, source - span.begin + W - 1, c, V);
+      }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < kRun; ++r) {
       Taps<T> window[W - 1];
 #pragma unroll
       for (int k = 0; k + 1 < W; ++k) window[k] = x_of[r + k];
-      if (first + r < last)
-        store_taps<PAST>(out + int64_t(first + r) * a.channels + c, count,
-                         convolve<T, W>(window, x_of[r + W - 1], w, b, a.silu));
+      store_taps<PAST>(out + int64_t(first + r) * a.channels + c, V, convolve<T, W>(window, x_of[r + W - 1], w, b, a.silu));
     }
     return;
   }
-  for (int32_t row = first; row < last;) {
-    const Span span = s < a.seq.sequences ? a.seq.span(s) : Span{last, last};
-    if (span.end <= row) {   // without tokens, or done
-      ++s;
-      continue;
-    }
-    row = max(row, span.begin);
-    if (row >= last) break;
+#pragma unroll
+  for (int i = 0; i < kRun + W - 1; ++i)   // (rows of other sequences too, and the tensor's first and last ones again)
+    x_of[i] = load_taps(x + int64_t(min(max(first - (W - 1) + i, 0), last - 1)) * a.channels + c, count);
+  if (span.begin < first && first < span.end) {
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k) {
-      const int32_t source = row - (W - 1) + k;
-      window[k] = source >= span.begin ? load_taps(x + int64_t(source) * a.channels + c, count)
-                                       : state_row<T, W>(a, s, source - span.begin + W - 1, c, count);
+      const int32_t source = first - (W - 1) + k;
+      if (source < span.begin) x_of[k] = state_row<T, W>(a, s, source - span.begin + W - 1, c, count);
     }
-    const int32_t stop = min(span.end, last);
-    for (; row < stop; ++row) {
-      const Taps<T> now = load_taps(x + int64_t(row) * a.channels + c, count);
-      store_taps<PAST>(out + int64_t(row) * a.channels + c, count, convolve<T, W>(window, now, w, b, a.silu));
+  }
+  __builtin_amdgcn_s_waitcnt(kNoLoads);
 #pragma unroll
-      for (int k = 0; k + 2 < W; ++k) window[k] = window[k + 1];
-      window[W - 2] = now;
+  for (int r = 0; r < kRun; ++r) {
+    const int32_t row = first + r;
+    while (s < a.seq.sequences && span.end <= row)
+      if (++s < a.seq.sequences) span = a.seq.span(s);
+    if (row >= last || s >= a.seq.sequences) break;
+    if (row < span.begin) continue;
+    if (row == span.begin) {   // its state in the place of the rows ahead, which are done with
+#pragma unroll
+      for (int k = 0; k + 1 < W; ++k) x_of[r + k] = state_row<T, W>(a, s, k, c, count);
+      __builtin_amdgcn_s_waitcnt(kNoLoads);   // here, so that rows without a beginning wait for nothing
     }
-    ++s;
+    Taps<T> window[W - 1];
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) window[k] = x_of[r + k];
+    store_taps<PAST>(out + int64_t(row) * a.channels + c, count, convolve<T, W>(window, x_of[r + W - 1], w, b, a.silu));
   }
 }
 
