@@ -1,11 +1,12 @@
 // Short causal convolution along the tokens of every channel with SiLU, for prompts (dense or packed) and for single
 // tokens.
 //
-// HBM-bound: one read and one write per element (4 x 2048 x 4096 bf16 29 us, 4.6 TB/s; 16384 x 5120 fp16 73 us, 4.6
-// TB/s).  A lane holds 4 neighbouring channels of a run of 16 rows and the width - 1 rows before it, all loaded before the
+// HBM-bound: one read and one write per element (out of memory 4 x 2048 x 4096 bf16 30 us, 4.5 TB/s; 16384 x 5120 fp16 62
+// us, 5.4 TB/s, a copy of it 63; small ones by the latency of a wave, 9001 x 1536 bf16 21 us).  A lane holds 4 neighbouring channels of a run of 16 rows and the width - 1 rows before it, all loaded before the
 // first is used, so a row is read once and (width - 1) / 16 times more, from cache (rows loaded one by one: 136 us at
 // 16384 x 5120; with a branch at every row's end 111).  Runs are cut at multiples of their rows in the whole tensor,
-// whatever the sequences are; those that a sequence begins or ends within decide row by row.
+// whatever the sequences are; those that a sequence begins or ends within decide row by row (9001 x 1536 in 2 or 37 sequences
+// 26 and 27 us).
 #include "block_internal.h"
 #include "gated_types.h"
 #include "sequences.h"
@@ -229,8 +230,9 @@ hipError_t launch_conv(const ConvArgs& c, hipStream_t stream) {
   if (units == 0) return hipSuccess;
   constexpr int kWaves = kThreads / kWave;
   const dim3 grid(uint32_t((units + kWaves - 1) / kWaves));
-  // Stores pass the caches by once a call touches more than the 256 MiB of the Infinity Cache (16384 x 5120 fp16: 75 us
-  // against 113).
+  // Stores pass the caches by once a call touches more than the 256 MiB of the Infinity Cache (16384 x 8192 bf16: 92 us
+  // against 95, its input in the caches 79 against 94).  Below that it would gain up to 2 us, and what reads the output
+  // next would lose more.
   const bool past = c.tokens * c.channels * int64_t(2 * sizeof(T)) > int64_t(256) << 20;
   switch (c.width * 2 + past) {
     case 4: causal_conv_kernel<T, 2, false><<<grid, kThreads, 0, stream>>>(a); break;

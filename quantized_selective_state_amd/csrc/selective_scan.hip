@@ -96,7 +96,7 @@ __device__ __forceinline__ Span chunk_rows(const ScanKernelArgs& a, int32_t k) {
 // channels of the lanes, an outer product of 4 states of B and d u, added to 4 registers of each lane.  That takes an fma
 // and the read of B in every lane off the vector units (a row of 64 channels x 16 states, in cycles of a wave on its own:
 // 318 against 365 with fma, with y 398 against 445; the instruction's sums are binary32 like an fma's).  Vector units are
-// at work in 87 and 88% of the cycles (16384 x 5120 fp16: 258 us without y, 347 with it).
+// at work in 84 and 86% of the cycles (16384 x 5120 fp16: 258 us without y, 347 with it).
 template <typename T, int N, int G, bool OUTPUT>
 __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKernelArgs a) {
   constexpr bool EXACT = sizeof(T) == 4;
