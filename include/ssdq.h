@@ -674,6 +674,25 @@ ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale,
                            int32_t n, hipStream_t stream);
 
 /*
+ * The kernel that ssdq_matmul_i8 takes for these sizes on the current device (host; informational: the sums are exact in
+ * all of them); -1 for sizes without work, invalid or unsupported ones.
+ */
+typedef enum {
+  SSDQ_MATMUL_STREAM_16 = 0,            /* weights streamed, up to 16 tokens */
+  SSDQ_MATMUL_STREAM_32 = 1,            /* the same, up to 32 */
+  SSDQ_MATMUL_TILES_256X256 = 2,        /* tiles of tokens x output channels */
+  SSDQ_MATMUL_TILES_128X128 = 3,
+  SSDQ_MATMUL_TILES_128X64 = 4,
+  SSDQ_MATMUL_TILES_64X64 = 5,
+  SSDQ_MATMUL_TILES_64X64_HALVES = 6,   /* in two halves of the inner axis */
+  SSDQ_MATMUL_ODD_STREAM_16 = 7,        /* inner sizes that no 16 divides, the same kinds */
+  SSDQ_MATMUL_ODD_128X128 = 8,
+  SSDQ_MATMUL_ODD_64X64 = 9,
+  SSDQ_MATMUL_ODD_64X64_HALVES = 10,
+} ssdq_matmul_plan;
+int32_t ssdq_matmul_i8_plan(int64_t m, int32_t k, int32_t n);
+
+/*
  * Short causal convolution along the tokens of every channel, ahead of the selective scan (the convolution of the
  * Mamba block; ssdq_frontend holds the Mamba-2 block's, fused with its quantizer):
  *
@@ -708,6 +727,10 @@ ssdq_status ssdq_causal_conv_step(int32_t dtype, void* state, const void* x, con
  * unsupported sizes, else at least 256). */
 size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate,
                                           int32_t packed);
+
+/* How ssdq_selective_scan walks sequences of these sizes (host; informational, results differ in binary32 rounding
+ * only): 0 whole, else in chunks of so many tokens; -1 on invalid or unsupported sizes. */
+int32_t ssdq_selective_scan_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, int32_t packed);
 
 /*
  * Selective state space scan with a decay for every channel and state and a step size for every channel (the recurrence
@@ -753,6 +776,10 @@ ssdq_status ssdq_selective_step(int32_t dtype, float* state, const void* u, cons
                                 const void* B, const void* C, const float* D, const void* z, const float* delta_bias,
                                 void* y, int32_t batch, int32_t channels, int32_t dstate, int32_t softplus,
                                 hipStream_t stream);
+
+/* How many sequences a lane of ssdq_selective_step takes at these sizes, 4 or 1 (host; informational, the results do not
+ * depend on it); -1 on invalid or unsupported sizes. */
+int32_t ssdq_selective_step_plan(int32_t batch, int32_t channels, int32_t dstate);
 
 #ifdef __cplusplus
 }

@@ -809,6 +809,16 @@ for _name, _types in {
     getattr(lib, _name).restype = ctypes.c_int
 lib.ssdq_selective_scan_workspace_size.argtypes = [_i32, _i64, _i32, _i32, _i32]
 lib.ssdq_selective_scan_workspace_size.restype = _sz
+lib.ssdq_matmul_i8_plan.argtypes = [_i64, _i32, _i32]
+lib.ssdq_matmul_i8_plan.restype = _i32
+lib.ssdq_selective_scan_plan.argtypes = [_i32, _i64, _i32, _i32, _i32]
+lib.ssdq_selective_scan_plan.restype = _i32
+lib.ssdq_selective_step_plan.argtypes = [_i32, _i32, _i32]
+lib.ssdq_selective_step_plan.restype = _i32
+
+# ssdq_matmul_plan
+MATMUL_I8_PLANS = ("stream 16", "stream 32", "tiles 256x256", "tiles 128x128", "tiles 128x64", "tiles 64x64",
+                   "tiles 64x64 halves", "odd stream 16", "odd 128x128", "odd 64x64", "odd 64x64 halves")
 
 
 def _inference_only(where: str, *tensors: torch.Tensor | None) -> None:
@@ -983,6 +993,15 @@ def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
     return out
 
 
+def matmul_i8_plan(m: int, k: int, n: int) -> str | None:
+    """The kernel that matmul_i8 takes for (m, k) by (n, k) on the current device, one of MATMUL_I8_PLANS
+    (ssdq_matmul_i8_plan); None where there is nothing to do or the sizes are not taken."""
+    if not (0 < m < 2 ** 63 and 0 < k <= _INT32_MAX and 0 < n <= _INT32_MAX):
+        return None
+    plan = lib.ssdq_matmul_i8_plan(m, k, n)
+    return None if plan < 0 else MATMUL_I8_PLANS[plan]
+
+
 # ---------------------------------------------------------------------------------------------
 # causal convolution and selective scan
 
@@ -1069,6 +1088,22 @@ def selective_scan_workspace_size(sequences: int, tokens: int, channels: int, ds
     if not all(0 <= n <= _INT32_MAX for n in (sequences, tokens, channels, dstate)):
         return 0
     return int(lib.ssdq_selective_scan_workspace_size(sequences, tokens, channels, dstate, int(packed)))
+
+
+def selective_scan_plan(sequences: int, tokens: int, channels: int, dstate: int, packed: bool = False) -> int:
+    """How selective_scan walks its sequences: 0 whole, else in chunks of so many tokens (ssdq_selective_scan_plan; -1:
+    sizes that it does not take)."""
+    if not all(0 <= n <= _INT32_MAX for n in (sequences, tokens, channels, dstate)):
+        return -1
+    return int(lib.ssdq_selective_scan_plan(sequences, tokens, channels, dstate, int(packed)))
+
+
+def selective_step_plan(batch: int, channels: int, dstate: int) -> int:
+    """How many sequences a lane of selective_step takes, 4 or 1 (ssdq_selective_step_plan; -1: sizes that it does not
+    take)."""
+    if not all(0 <= n <= _INT32_MAX for n in (batch, channels, dstate)):
+        return -1
+    return int(lib.ssdq_selective_step_plan(batch, channels, dstate))
 
 
 def _parameters(A, D, delta_bias, channels, dev) -> int:

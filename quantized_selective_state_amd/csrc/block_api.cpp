@@ -46,6 +46,16 @@ ssdq_status check_selective(int32_t sequences, int64_t tokens, int32_t channels,
   return SSDQ_SUCCESS;
 }
 
+bool ok_matmul(int64_t m, int32_t k, int32_t n) {
+  // a grid's threads in 32 bits, at 256 for each 128 x 128 of out
+  return k <= 131071 && m < kMostRows && ((m + 127) / 128) * ((int64_t(n) + 127) / 128) < (int64_t(1) << 24);
+}
+
+bool ok_selective_step(int32_t batch, int32_t channels, int32_t dstate) {
+  // a grid's threads in 32 bits, at up to 256 for each 16 channels
+  return dstate <= 64 && (int64_t(channels) + 15) / 16 * batch < int64_t(1) << 24;
+}
+
 }  // namespace
 
 extern "C" {
@@ -118,14 +128,16 @@ ssdq_status ssdq_matmul_i8(int32_t dtype, const int8_t* a, const float* a_scale,
                            const int8_t* b, const float* b_scale, const float* bias, void* out, int64_t m, int32_t k,
                            int32_t n, hipStream_t stream) {
   if (!ok_dtype(dtype) || m < 0 || k <= 0 || n <= 0) return SSDQ_ERROR_INVALID_VALUE;
-  // a grid's threads in 32 bits, at 256 for each 128 x 128 of out
-  if (k > 131071 || m >= kMostRows || ((m + 127) / 128) * ((int64_t(n) + 127) / 128) >= (int64_t(1) << 24))
-    return SSDQ_ERROR_UNSUPPORTED;
+  if (!ok_matmul(m, k, n)) return SSDQ_ERROR_UNSUPPORTED;
   if (m == 0) return SSDQ_SUCCESS;
   if (!ok_ptr(a) || !ok_ptr(a_scale) || !ok_ptr(b) || !ok_ptr(b_scale) || !ok_opt(bias) || !ok_ptr(out))
     return SSDQ_ERROR_INVALID_VALUE;
   const MatmulArgs args = {dtype, a, a_scale, a_scale_per_row != 0, b, b_scale, bias, out, m, k, n};
   return launched(launch_matmul_i8(args, stream));
+}
+
+int32_t ssdq_matmul_i8_plan(int64_t m, int32_t k, int32_t n) {
+  return m > 0 && k > 0 && n > 0 && ok_matmul(m, k, n) ? matmul_i8_plan(m, k, n) : -1;
 }
 
 ssdq_status ssdq_causal_conv(int32_t dtype, const void* x, const float* weight, const float* bias, const void* state,
@@ -161,6 +173,11 @@ size_t ssdq_selective_scan_workspace_size(int32_t sequences, int64_t tokens, int
   return selective_workspace_bytes(sequences, tokens, channels, dstate, packed != 0);
 }
 
+int32_t ssdq_selective_scan_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, int32_t packed) {
+  if (check_selective(sequences, tokens, channels, dstate, packed != 0) != SSDQ_SUCCESS) return -1;
+  return selective_scan_plan(sequences, tokens, channels, dstate, packed != 0);
+}
+
 ssdq_status ssdq_selective_scan(int32_t dtype, const void* u, const void* delta, const float* A, const void* B,
                                 const void* C, const float* D, const void* z, const float* delta_bias, const float* h0,
                                 const int32_t* offsets, void* y, float* h_final, int32_t sequences, int64_t tokens,
@@ -187,13 +204,17 @@ ssdq_status ssdq_selective_step(int32_t dtype, float* state, const void* u, cons
                                 void* y, int32_t batch, int32_t channels, int32_t dstate, int32_t softplus,
                                 hipStream_t stream) {
   if (!ok_dtype(dtype) || batch <= 0 || channels <= 0 || dstate <= 0) return SSDQ_ERROR_INVALID_VALUE;
-  // a grid's threads in 32 bits, at up to 256 for each 16 channels
-  if (dstate > 64 || (int64_t(channels) + 15) / 16 * batch >= int64_t(1) << 24) return SSDQ_ERROR_UNSUPPORTED;
+  if (!ok_selective_step(batch, channels, dstate)) return SSDQ_ERROR_UNSUPPORTED;
   if (!ok_ptr(state) || !ok_ptr(u) || !ok_ptr(delta) || !ok_ptr(A) || !ok_ptr(B) || !ok_ptr(C) || !ok_opt(D) ||
       !ok_opt(z) || !ok_opt(delta_bias) || !ok_ptr(y))
     return SSDQ_ERROR_INVALID_VALUE;
   return launched(launch_selective_step(dtype, state, u, delta, A, B, C, D, z, delta_bias, y, batch, channels, dstate,
                                         softplus != 0, stream));
+}
+
+int32_t ssdq_selective_step_plan(int32_t batch, int32_t channels, int32_t dstate) {
+  if (batch <= 0 || channels <= 0 || dstate <= 0 || !ok_selective_step(batch, channels, dstate)) return -1;
+  return selective_step_plan(batch, channels, dstate);
 }
 
 }  // extern "C"

@@ -41,6 +41,7 @@ struct MatmulArgs {
   int32_t k, n;
 };
 hipError_t launch_matmul_i8(const MatmulArgs& a, hipStream_t stream);
+int32_t matmul_i8_plan(int64_t m, int32_t k, int32_t n);   // of valid sizes, m > 0
 
 struct ConvArgs {
   int32_t dtype;
@@ -83,6 +84,8 @@ struct SelectiveArgs {
 };
 // 0: sizes that the kernels do not take
 size_t selective_workspace_bytes(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed);
+int32_t selective_scan_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed);   // of such
+int32_t selective_step_plan(int32_t batch, int32_t channels, int32_t dstate);   // of valid sizes
 hipError_t launch_selective_scan(const SelectiveArgs& a, hipStream_t stream);
 hipError_t launch_selective_step(int32_t dtype, float* state, const void* u, const void* delta, const float* A,
                                  const void* B, const void* C, const float* D, const void* z, const float* delta_bias,

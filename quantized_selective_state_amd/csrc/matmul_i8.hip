@@ -535,15 +535,16 @@ hipError_t launch_tiles(const MatmulArgs& a, const Epilogue& ep, int per_unit, h
 
 // Which tiles: the fewest microseconds by rounds x slabs x the time of a slab, where a round is as many tiles as the device
 // holds at once and the times are those measured with all compute units at work.
-struct Candidate { int tm, tn, per_unit; float slab_us; };
-constexpr Candidate kCandidates[] = {{256, 256, 1, 1.80f}, {128, 128, 2, 1.06f}, {128, 64, 2, 0.68f}, {64, 64, 2, 0.50f}};
+struct Candidate { int32_t plan; int tm, tn, per_unit; float slab_us; };
+constexpr Candidate kCandidates[] = {{SSDQ_MATMUL_TILES_256X256, 256, 256, 1, 1.80f}, {SSDQ_MATMUL_TILES_128X128, 128, 128, 2, 1.06f},
+                                     {SSDQ_MATMUL_TILES_128X64, 128, 64, 2, 0.68f}, {SSDQ_MATMUL_TILES_64X64, 64, 64, 2, 0.50f}};
 
-int choose(const MatmulArgs& a) {
+int32_t choose(int64_t m, int32_t n) {
   int best = 0;
   double least = 0.;
   for (int i = 0; i < 4; ++i) {
     const Candidate& c = kCandidates[i];
-    const int64_t tiles = (a.m + c.tm - 1) / c.tm * ((int64_t(a.n) + c.tn - 1) / c.tn);
+    const int64_t tiles = (m + c.tm - 1) / c.tm * ((int64_t(n) + c.tn - 1) / c.tn);
     const int64_t slots = int64_t(compute_units()) * c.per_unit;
     const double time = double((tiles + slots - 1) / slots) * c.slab_us;
     if (i == 0 || time < least) {
@@ -551,46 +552,54 @@ int choose(const MatmulArgs& a) {
       least = time;
     }
   }
-  return best;
+  return kCandidates[best].plan;
+}
+
+template <typename T, int kSide, int kSplit>
+hipError_t launch_ragged(const MatmulArgs& a, const Epilogue& ep, int per_unit, hipStream_t stream) {
+  uint32_t blocks;
+  const TileArgs args = tile_args<kSide, kSide>(a, ep, per_unit, &blocks);
+  ragged_kernel<T, kSide, kSplit><<<dim3(blocks), 256 * kSplit, 0, stream>>>(args, static_cast<T*>(a.out));
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   const Epilogue ep = {a.a_scale, a.b_scale, a.bias, a.per_row};
-  const int64_t tiles = (a.m + 63) / 64 * ((int64_t(a.n) + 63) / 64);   // of the smallest size
-  if (a.k % 16 != 0) {
-    if (a.m <= 16 && a.n <= 1 << 24) return launch_stream<T, 1, true>(a, ep, stream);
-    uint32_t blocks;
-    if ((a.m + 127) / 128 * ((int64_t(a.n) + 127) / 128) >= compute_units()) {
-      const TileArgs args = tile_args<128, 128>(a, ep, 2, &blocks);
-      ragged_kernel<T, 128, 1><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
-    } else if (tiles > compute_units()) {
-      const TileArgs args = tile_args<64, 64>(a, ep, 3, &blocks);
-      ragged_kernel<T, 64, 1><<<dim3(blocks), 256, 0, stream>>>(args, static_cast<T*>(a.out));
-    } else {
-      const TileArgs args = tile_args<64, 64>(a, ep, 1, &blocks);
-      ragged_kernel<T, 64, 2><<<dim3(blocks), 512, 0, stream>>>(args, static_cast<T*>(a.out));
-    }
-    return hipGetLastError();
+  switch (matmul_i8_plan(a.m, a.k, a.n)) {
+    case SSDQ_MATMUL_STREAM_16: return launch_stream<T, 1>(a, ep, stream);
+    case SSDQ_MATMUL_STREAM_32: return launch_stream<T, 2>(a, ep, stream);
+    case SSDQ_MATMUL_TILES_256X256: return launch_tiles<T, 256, 256, 2, 4, 2>(a, ep, kCandidates[0].per_unit, stream);
+    case SSDQ_MATMUL_TILES_128X128: return launch_tiles<T, 128, 128, 2, 2, 2>(a, ep, kCandidates[1].per_unit, stream);
+    case SSDQ_MATMUL_TILES_128X64: return launch_tiles<T, 128, 64, 2, 2, 3>(a, ep, kCandidates[2].per_unit, stream);
+    case SSDQ_MATMUL_TILES_64X64: return launch_tiles<T, 64, 64, 2, 2, 4>(a, ep, kCandidates[3].per_unit, stream);
+    case SSDQ_MATMUL_TILES_64X64_HALVES: return launch_tiles<T, 64, 64, 2, 2, 4, 2>(a, ep, 1, stream);
+    case SSDQ_MATMUL_ODD_STREAM_16: return launch_stream<T, 1, true>(a, ep, stream);
+    case SSDQ_MATMUL_ODD_128X128: return launch_ragged<T, 128, 1>(a, ep, 2, stream);
+    case SSDQ_MATMUL_ODD_64X64: return launch_ragged<T, 64, 1>(a, ep, 3, stream);
+    default: return launch_ragged<T, 64, 2>(a, ep, 1, stream);
   }
-  // Few tokens: up to 8 the tokens' bytes are nothing beside the weights'; up to 32 where tiles of 64 channels would leave
-  // half of the compute units idle (16 x 8192 x 4096: 11.0 us against 20.5; 16 x 4096 x 18560: 23.2 against 20.9).
-  const bool narrow = (int64_t(a.n) + 63) / 64 * 2 <= compute_units();
-  if ((a.m <= 8 && a.n <= 1 << 24) || (a.m <= 16 && narrow)) return launch_stream<T, 1>(a, ep, stream);
-  if (a.m <= 32 && narrow) return launch_stream<T, 2>(a, ep, stream);
-  switch (choose(a)) {
-    case 0: return launch_tiles<T, 256, 256, 2, 4, 2>(a, ep, kCandidates[0].per_unit, stream);
-    case 1: return launch_tiles<T, 128, 128, 2, 2, 2>(a, ep, kCandidates[1].per_unit, stream);
-    case 2: return launch_tiles<T, 128, 64, 2, 2, 3>(a, ep, kCandidates[2].per_unit, stream);
-    default: break;
-  }
-  // no more tiles than compute units: two halves of the inner axis in each (256 x 4096 x 4096 12.9 us and 11.2 so;
-  // 64 x 4096 x 18560, 290 tiles, 24.0 and 24.5)
-  if (tiles <= compute_units()) return launch_tiles<T, 64, 64, 2, 2, 4, 2>(a, ep, 1, stream);
-  return launch_tiles<T, 64, 64, 2, 2, 4>(a, ep, kCandidates[3].per_unit, stream);
 }
 
 }  // namespace
+
+int32_t matmul_i8_plan(int64_t m, int32_t k, int32_t n) {
+  const int64_t tiles = (m + 63) / 64 * ((int64_t(n) + 63) / 64);   // of the smallest size
+  if (k % 16 != 0) {
+    if (m <= 16 && n <= 1 << 24) return SSDQ_MATMUL_ODD_STREAM_16;
+    if ((m + 127) / 128 * ((int64_t(n) + 127) / 128) >= compute_units()) return SSDQ_MATMUL_ODD_128X128;
+    return tiles > compute_units() ? SSDQ_MATMUL_ODD_64X64 : SSDQ_MATMUL_ODD_64X64_HALVES;
+  }
+  // Few tokens: up to 8 the tokens' bytes are nothing beside the weights'; up to 32 where tiles of 64 channels would leave
+  // half of the compute units idle (16 x 8192 x 4096: 11.0 us against 20.5; 16 x 4096 x 18560: 23.2 against 20.9).
+  const bool narrow = (int64_t(n) + 63) / 64 * 2 <= compute_units();
+  if ((m <= 8 && n <= 1 << 24) || (m <= 16 && narrow)) return SSDQ_MATMUL_STREAM_16;
+  if (m <= 32 && narrow) return SSDQ_MATMUL_STREAM_32;
+  const int32_t best = choose(m, n);
+  // no more tiles than compute units: two halves of the inner axis in each (256 x 4096 x 4096 12.9 us and 11.2 so;
+  // 64 x 4096 x 18560, 290 tiles, 24.0 and 24.5)
+  return best == SSDQ_MATMUL_TILES_64X64 && tiles <= compute_units() ? SSDQ_MATMUL_TILES_64X64_HALVES : best;
+}
 
 hipError_t launch_matmul_i8(const MatmulArgs& a, hipStream_t stream) {
   switch (a.dtype) {

@@ -734,15 +734,19 @@ hipError_t launch_scan(const ScanKernelArgs& a, bool quad, hipStream_t stream) {
   }
 }
 
+int32_t step_lanes(int32_t dstate) {   // of a channel, with four states each
+  int32_t lanes = 1;
+  while (lanes * 4 < dstate) lanes *= 2;
+  return lanes;
+}
+int32_t step_channel_blocks(int32_t channels, int32_t lanes) { return (channels + kThreads / lanes - 1) / (kThreads / lanes); }
+
 template <typename T>
 hipError_t launch_step(float* state, const void* u, const void* delta, const float* A, const void* B, const void* C,
                        const float* D, const void* z, const float* delta_bias, void* y, int32_t batch, int32_t channels,
                        int32_t dstate, bool softplus, hipStream_t stream) {
-  int32_t lanes = 1;
-  while (lanes * 4 < dstate) lanes *= 2;
-  const int32_t channel_blocks = (channels + kThreads / lanes - 1) / (kThreads / lanes);
-  // four sequences a lane once they leave a block for every compute unit
-  const bool many = int64_t(channel_blocks) * (batch / 4) >= 256;
+  const int32_t lanes = step_lanes(dstate), channel_blocks = step_channel_blocks(channels, lanes);
+  const bool many = selective_step_plan(batch, channels, dstate) == 4;
   const int64_t blocks = int64_t(channel_blocks) * (many ? (batch + 3) / 4 : batch);
   const dim3 grid = dim3(uint32_t(blocks));
   const T *in = static_cast<const T*>(u), *steps = static_cast<const T*>(delta), *gate = static_cast<const T*>(z);
@@ -758,6 +762,17 @@ hipError_t launch_step(float* state, const void* u, const void* delta, const flo
 size_t selective_workspace_bytes(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed) {
   Plan p;
   return make_plan(sequences, tokens, channels, dstate, packed, &p) ? p.bytes : 0;
+}
+
+int32_t selective_scan_plan(int32_t sequences, int64_t tokens, int32_t channels, int32_t dstate, bool packed) {
+  Plan p;
+  if (!make_plan(sequences, tokens, channels, dstate, packed, &p)) return -1;
+  return p.quad ? 0 : p.chunk;
+}
+
+// four sequences a lane once they leave a block for every compute unit
+int32_t selective_step_plan(int32_t batch, int32_t channels, int32_t dstate) {
+  return int64_t(step_channel_blocks(channels, step_lanes(dstate))) * (batch / 4) >= 256 ? 4 : 1;
 }
 
 hipError_t launch_selective_scan(const SelectiveArgs& s, hipStream_t stream) {
