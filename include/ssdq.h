@@ -619,7 +619,8 @@ ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, cons
  *                  n / static_scale, within [-127, 127] (NaN gives 0); scale is NULL then
  * -128 is never produced.  A row whose sum of squares is not finite in binary32 (a NaN or an infinity in it, or
  * magnitudes near 2^64) is NaN: out is NaN throughout, the scale is NaN and the codes 0, so that the fault is not hidden;
- * with a static scale its codes are 0.  So is a row of zeros with eps 0.  (With groups: out is NaN in that group, scale
+ * with a static scale its codes are 0.  So is a row of zeros with eps 0.  A row whose squares underflow is none of these: its
+ * n is that of the formula, whatever eps.  (With groups: out is NaN in that group, scale
  * and codes over the row; under a static scale the codes are 0 in that group.)
  *   dtype    : ssdq_dtype of x, gate and out     x, gate, out : (rows, channels)
  *   residual_dtype : ssdq_dtype of residual and residual_out: dtype, or SSDQ_DTYPE_F32

@@ -5,10 +5,17 @@
 // max |n| is max |v w| times it.  So the sum of squares and the largest |v w| are reduced together, the row stays in
 // registers between, and a block has one barrier per row (none where a row fits one wave).
 //
+// Squares below 2^-149 are lost.  That is nothing beside an eps of 2^-64 or more; with a smaller one (kSmall) a group's
+// values are first scaled by a power of two to a largest magnitude near 1, which changes no other digit and takes one
+// reduction more.
+//
 // HBM-bound: every tensor once (32768 x 4096 bf16: norm 82 us, 6.5 TB/s; to codes 73, with a residual in bf16 to codes 172,
 // 5.5 TB/s; 32768 x 8192 fp16 gated to codes 256, 5.2 TB/s; rows as codes 70 and back 61 at 32768 x 4096).  A lane's 16
 // bytes are neighbours and a lane holds up to four such pieces, so that a row has some waves and a compute unit many
 // rows: their loads cover each other's latency, and no row is loaded ahead by its own block.
+#include <algorithm>
+#include <cmath>
+
 #include "block_internal.h"
 #include "gated_types.h"
 
@@ -84,6 +91,7 @@ struct NormKernelArgs {
   int32_t lanes;                    // threads of a group, a power of two
   int32_t per_block;                // rows of a block
   float eps, inverse_size;
+  int32_t most_shift;               // kSmall: of the scaling, so that eps stays finite under it
 };
 
 // sum and most over the `lanes` (at most 64) neighbouring lanes of a group, in all of them
@@ -94,14 +102,21 @@ __device__ __forceinline__ void reduce_lanes(float& sum, uint32_t& most, int lan
   }
 }
 
-__device__ __forceinline__ float root(float sum, const NormKernelArgs& a) {
-  return sum < __builtin_inff() ? 1.f / sqrtf(fmaf(sum, a.inverse_size, a.eps)) : __builtin_nanf("");
+__device__ __forceinline__ float root(float sum, float eps, const NormKernelArgs& a) {
+  return sum < __builtin_inff() ? 1.f / sqrtf(fmaf(sum, a.inverse_size, eps)) : __builtin_nanf("");
 }
 
-template <typename T, typename R, int SOURCE, bool NORM, int OUT, int SLOTS, bool PAST>
+// kSmall: 2^shift for a group with this largest magnitude, 1 where that is 1 or more (or not finite)
+__device__ __forceinline__ float scaling(uint32_t most, const NormKernelArgs& a) {
+  const int shift = min(max(127 - int(most >> 23), 0), a.most_shift);
+  return __uint_as_float(uint32_t(127 + shift) << 23);
+}
+
+template <typename T, typename R, int SOURCE, bool NORM, int OUT, int SLOTS, bool PAST, bool kSmall>
 __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
   __shared__ float sums[2][kMostThreads];       // of a wave, or of a group with fewer lanes; two rows in turn
   __shared__ uint32_t mosts[2][kMostThreads];
+  __shared__ uint32_t tops[2][kSmall ? kMostThreads : 1];
   const int sub = int(threadIdx.x) / a.lanes, lane = int(threadIdx.x) % a.lanes;
   const int in_block = sub / a.groups, group = sub % a.groups;
   const int unit = a.lanes < kWave ? a.lanes : kWave;            // threads that share one entry of sums
@@ -123,7 +138,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
     const int64_t row = row0 + in_block;
     const bool live = in_block < a.per_block && row < a.rows;
     const int64_t at = row * a.channels + start;
-    float v[SLOTS][V], sum = 0.f;
+    float v[SLOTS][V], sum = 0.f, eps = a.eps;
     uint32_t most = 0;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
@@ -138,6 +153,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
         if constexpr (SOURCE == kResidual)
           store_some<false>(static_cast<R*>(a.residual_out) + at + c, count, rounded<R>(v[s]));
       }
+      if constexpr (kSmall) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) most = max(most, __float_as_uint(fabsf(v[s][i])));
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if constexpr (NORM) {
@@ -147,11 +167,39 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
         if constexpr (OUT == kDynamic) most = max(most, __float_as_uint(fabsf(v[s][i])));
       }
     }
+    const auto scale_of = [&](int g) {   // kSmall: of the row's group g, once tops has its largest magnitudes
+      uint32_t top = 0;
+      for (int k = 0; k < per_group; ++k) top = max(top, tops[parity][kSmall ? first + g * per_group + k : 0]);
+      return scaling(top, a);
+    };
+    if constexpr (kSmall) {
+      reduce_lanes(sum, most, a.lanes);
+      float up;
+      if (per_group == 1) {
+        up = scaling(most, a);
+      } else {
+        tops[parity][entry] = most;
+        __syncthreads();
+        up = scale_of(group);
+      }
+      most = 0;
+      eps = a.eps * up * up;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[s][i] *= up;
+          sum = fmaf(v[s][i], v[s][i], sum);
+          v[s][i] *= w[s][i];
+          if constexpr (OUT == kDynamic) most = max(most, __float_as_uint(fabsf(v[s][i])));
+        }
+      }
+    }
     reduce_lanes(sum, most, a.lanes);
     float r = 1.f;
     if (per_group == 1) {   // a group's lanes have its sums
       if constexpr (NORM) {
-        r = root(sum, a);
+        r = root(sum, eps, a);
         most = __float_as_uint(fabsf(__uint_as_float(most) * r));
       }
       if (OUT == kDynamic && a.groups > 1) {
@@ -174,7 +222,12 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(NormKernelArgs a) {
         }
         if constexpr (NORM) {
           if (OUT != kDynamic && g != group) continue;
-          const float its = root(total, a);
+          float its_eps = eps;
+          if constexpr (kSmall) {
+            const float up = scale_of(g);
+            its_eps = a.eps * up * up;
+          }
+          const float its = root(total, its_eps, a);
           if (g == group) r = its;
           top = __float_as_uint(fabsf(__uint_as_float(top) * its));
         }
@@ -248,6 +301,7 @@ int32_t power_of_two(int32_t n) {
 // and 44).
 // The residual stays an ordinary store (fp32 residual to codes, 32768 x 4096: 275 us, 285 with all stores).
 constexpr int64_t kInfinityCache = int64_t(256) << 20;
+constexpr float kSmallEps = 5.42101086e-20f;   // 2^-64
 
 template <typename T, typename R, int SOURCE, bool NORM, int OUT, bool PAST>
 hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
@@ -266,6 +320,8 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   a.size = n.channels / n.groups;
   a.eps = n.eps;
   a.inverse_size = 1.f / float(a.size);
+  const bool small = NORM && a.eps < kSmallEps;
+  if (small) a.most_shift = a.eps > 0.f ? std::min(126, (59 - std::ilogb(a.eps)) / 2) : 126;
   const int32_t packs = (a.size + V - 1) / V;
   // Up to four packs a lane, so that a compute unit has several rows (the limits on sizes keep all groups within
   // kMostThreads); one where there is not a row for every compute unit.
@@ -278,9 +334,10 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   const int64_t most = int64_t(compute_units()) * (2048 / block);
   const dim3 grid(uint32_t(items < most ? items : most));
   const int32_t slots = (packs + a.lanes - 1) / a.lanes;
-  if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1, PAST><<<grid, block, 0, stream>>>(a);
-  else if (slots <= 2) norm_kernel<T, R, SOURCE, NORM, OUT, 2, PAST><<<grid, block, 0, stream>>>(a);
-  else norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST><<<grid, block, 0, stream>>>(a);
+  if (small) norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST, NORM><<<grid, block, 0, stream>>>(a);
+  else if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1, PAST, false><<<grid, block, 0, stream>>>(a);
+  else if (slots <= 2) norm_kernel<T, R, SOURCE, NORM, OUT, 2, PAST, false><<<grid, block, 0, stream>>>(a);
+  else norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST, false><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
