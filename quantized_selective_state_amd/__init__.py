@@ -14,6 +14,7 @@ import functools
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssdq.so")
@@ -575,15 +576,26 @@ def _int32(n: int, what: str) -> None:
         raise ValueError(f"{what} must be below 2^31, got {n}")
 
 
+def _refuse_gradients(where: str, why: str, tensors) -> None:
+    """The calls are no autograd nodes: where torch would record one, or carry a forward-mode tangent on (which
+    torch.no_grad() does not stop), a result without it would drop gradients."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(where + why)
+    if getattr(forward_ad, "_current_level", 0) >= 0:    # (without torch's private number: look at every tensor)
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(where + why + " (forward mode: a tensor has a tangent; its primal has none)")
+
+
+_RECORDS_NONE = (" records no gradient, but one of its tensors requires it: call it under torch.no_grad(), on detached tensors "
+                 "or within a torch.autograd.Function (whose backward calls gated_scan_backward)")
+_HAS_NONE = " has no gradient, but one of its tensors requires it: call it under torch.no_grad() or on detached tensors"
+
+
 def _no_gradient_lost(where: str, *tensors: torch.Tensor | None) -> None:
-    """The calls are no autograd nodes: where torch would record one, a result without it would drop gradients."""
-    if not torch.is_grad_enabled():
-        return
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise ValueError(f"{where} records no gradient, but one of its tensors requires it: call it under "
-                             "torch.no_grad(), on detached tensors or within a torch.autograd.Function (whose backward "
-                             "calls gated_scan_backward)")
+    _refuse_gradients(where, _RECORDS_NONE, tensors)
 
 
 def _at(t: torch.Tensor | None) -> int | None:
@@ -822,13 +834,7 @@ MATMUL_I8_PLANS = ("stream 16", "stream 32", "tiles 256x256", "tiles 128x128", "
 
 
 def _inference_only(where: str, *tensors: torch.Tensor | None) -> None:
-    """None of the calls has a gradient: where torch would record one, a result without it would drop gradients."""
-    if not torch.is_grad_enabled():
-        return
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise ValueError(f"{where} has no gradient, but one of its tensors requires it: call it under "
-                             "torch.no_grad() or on detached tensors")
+    _refuse_gradients(where, _HAS_NONE, tensors)
 
 
 # ---------------------------------------------------------------------------------------------
