@@ -173,8 +173,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_kernel(ConvKernelArgs a)
 #pragma unroll
   for (int r = 0; r < kRun; ++r) {
     const int32_t row = first + r;
-    while (s < a.seq.sequences && span.end <= row)
-      if (++s < a.seq.sequences) span = a.seq.span(s);
+    if (s < a.seq.sequences && span.end <= row) a.seq.advance(row, s, span);
     if (row >= last || s >= a.seq.sequences) break;
     if (row < span.begin) continue;
     if (row == span.begin) {   // its state in the place of the rows ahead, which are done with
