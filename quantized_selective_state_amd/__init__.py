@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import types
 
 import torch
 from torch.autograd import forward_ad
@@ -576,17 +577,15 @@ def _int32(n: int, what: str) -> None:
         raise ValueError(f"{what} must be below 2^31, got {n}")
 
 
-def _refuse_gradients(where: str, why: str, tensors) -> None:
-    """The calls are no autograd nodes: where torch would record one, or carry a forward-mode tangent on (which
-    torch.no_grad() does not stop), a result without it would drop gradients."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(where + why)
-    if getattr(forward_ad, "_current_level", 0) >= 0:    # (without torch's private number: look at every tensor)
-        for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError(where + why + " (forward mode: a tensor has a tangent; its primal has none)")
+# Whether a forward-mode level is open, by torch's private number of it (without that: as if one were).
+_forward = forward_ad if hasattr(forward_ad, "_current_level") else types.SimpleNamespace(_current_level=0)
+
+
+def _refuse_tangents(message: str, tensors) -> None:
+    """A forward-mode tangent goes on under torch.no_grad() too, and a result without one would drop it."""
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{message} (forward mode: a tensor has a tangent; its primal has none)")
 
 
 _RECORDS_NONE = (" records no gradient, but one of its tensors requires it: call it under torch.no_grad(), on detached tensors "
@@ -595,7 +594,13 @@ _HAS_NONE = " has no gradient, but one of its tensors requires it: call it under
 
 
 def _no_gradient_lost(where: str, *tensors: torch.Tensor | None) -> None:
-    _refuse_gradients(where, _RECORDS_NONE, tensors)
+    """The calls are no autograd nodes: where torch would record one, a result without it would drop gradients."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(where + _RECORDS_NONE)
+    if _forward._current_level >= 0:
+        _refuse_tangents(where + _RECORDS_NONE, tensors)
 
 
 def _at(t: torch.Tensor | None) -> int | None:
@@ -834,7 +839,13 @@ MATMUL_I8_PLANS = ("stream 16", "stream 32", "tiles 256x256", "tiles 128x128", "
 
 
 def _inference_only(where: str, *tensors: torch.Tensor | None) -> None:
-    _refuse_gradients(where, _HAS_NONE, tensors)
+    """None of the calls has a gradient: where torch would record one, a result without it would drop gradients."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(where + _HAS_NONE)
+    if _forward._current_level >= 0:
+        _refuse_tangents(where + _HAS_NONE, tensors)
 
 
 # ---------------------------------------------------------------------------------------------
