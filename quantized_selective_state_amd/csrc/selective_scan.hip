@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, OUTPUT ? 3 : 4) chunk_kernel(ScanKer
 #pragma unroll 1
       for (int r = 0; r < kGroup && row0 + r < rows.end; ++r) {   // where sequences begin or end
         const int32_t row = row0 + r;
-        if (s < a.seq.sequences && span.end <= row) {
+        if (OUTPUT && s < a.seq.sequences && span.end <= row) {   // (else all rows from `from` on are of one)
           a.seq.advance(row, s, span);
           inside = false;
         }

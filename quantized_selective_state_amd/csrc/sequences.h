@@ -36,15 +36,12 @@ struct Sequences {
     return low;
   }
   // From sequence s, whose span ends at or before `row`, on to the first that ends behind it (`sequences` if none does).
-  // The next ones are tried; the end of a long run of empty ones is searched for.  With offsets in order the last
-  // sequence that begins at or before `row` is the wanted one, or no row from `row` on is in any.
+  // The next one is tried; the end of a run of empty ones is searched for.  With offsets in order the last sequence that
+  // begins at or before `row` is the wanted one, or no row from `row` on is in any.
   __device__ __forceinline__ void advance(int32_t row, int32_t& s, Span& now) const {
-#pragma unroll 1
-    for (int tries = 0; tries < 4; ++tries) {
-      if (++s >= sequences) return;
-      now = span(s);
-      if (now.end > row) return;
-    }
+    if (++s >= sequences) return;
+    now = span(s);
+    if (now.end > row) return;
     s = at(row);
     now = span(s);
     if (now.end <= row) s = sequences;
