@@ -7,7 +7,7 @@
 //
 // Squares below 2^-149 are lost.  That is nothing beside an eps of 2^-64 or more; with a smaller one (kSmall) a group's
 // values are first scaled by a power of two to a largest magnitude near 1, which changes no other digit and takes one
-// reduction more.
+// reduction more (32768 x 4096 with eps 0, fp32: norm 238 us and 244 so, to codes 124 and 129).
 //
 // HBM-bound: every tensor once (32768 x 4096 bf16: norm 82 us, 6.5 TB/s; to codes 73, with a residual in bf16 to codes 172,
 // 5.5 TB/s; 32768 x 8192 fp16 gated to codes 256, 5.2 TB/s; rows as codes 70 and back 61 at 32768 x 4096).  A lane's 16
@@ -320,7 +320,9 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   a.size = n.channels / n.groups;
   a.eps = n.eps;
   a.inverse_size = 1.f / float(a.size);
-  const bool small = NORM && a.eps < kSmallEps;
+  // (numbers of binary16, down to 2^-24, have squares that do not underflow)
+  constexpr bool kUnderflows = NORM && !(__is_same(T, _Float16) && (SOURCE == kPlain || (SOURCE == kResidual && __is_same(R, T))));
+  const bool small = kUnderflows && a.eps < kSmallEps;
   if (small) a.most_shift = a.eps > 0.f ? std::min(126, (59 - std::ilogb(a.eps)) / 2) : 126;
   const int32_t packs = (a.size + V - 1) / V;
   // Up to four packs a lane, so that a compute unit has several rows (the limits on sizes keep all groups within
@@ -334,7 +336,7 @@ hipError_t launch_slots(const NormArgs& n, hipStream_t stream) {
   const int64_t most = int64_t(compute_units()) * (2048 / block);
   const dim3 grid(uint32_t(items < most ? items : most));
   const int32_t slots = (packs + a.lanes - 1) / a.lanes;
-  if (small) norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST, NORM><<<grid, block, 0, stream>>>(a);
+  if (small) norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST, kUnderflows><<<grid, block, 0, stream>>>(a);
   else if (slots <= 1) norm_kernel<T, R, SOURCE, NORM, OUT, 1, PAST, false><<<grid, block, 0, stream>>>(a);
   else if (slots <= 2) norm_kernel<T, R, SOURCE, NORM, OUT, 2, PAST, false><<<grid, block, 0, stream>>>(a);
   else norm_kernel<T, R, SOURCE, NORM, OUT, 4, PAST, false><<<grid, block, 0, stream>>>(a);
