@@ -615,7 +615,7 @@ ssdq_status ssdq_gated_step(int32_t dtype, int32_t gate_kind, float* state, cons
  *   out          : (rows, channels) of dtype = n, rounded to nearest even
  *   codes, scale : (rows, channels) int8 and (rows) fp32: the row's scale is m * (1/127) with m = max |n[r,:]| (0, with
  *                  zero codes, when m < 127 * 2^-126), a code the integer nearest to n / scale, ties to even
- *   codes, static_scale : static_scale [1] fp32, device, positive and normal; a code is the integer nearest to
+ *   codes, static_scale : static_scale [1] fp32, device, from 2^-126 to 2^115; a code is the integer nearest to
  *                  n / static_scale, within [-127, 127] (NaN gives 0); scale is NULL then
  * -128 is never produced.  A row whose sum of squares is not finite in binary32 (a NaN or an infinity in it, or
  * magnitudes near 2^64) is NaN: out is NaN throughout, the scale is NaN and the codes 0, so that the fault is not hidden;

@@ -96,3 +96,19 @@ def test_many_rows_past_the_caches():
     some = torch.arange(0, 40000, 611, device=DEV)
     n, _, bound = ref.norm(host(x[some]), host(w), eps=0.0)
     close(out[some], n, bound, torch.float32, "norm")
+
+
+@pytest.mark.parametrize("power", [-126, -100, 0, 100, 114])
+def test_static_scales_of_every_size(power):
+    """From the smallest scale that is allowed to the largest."""
+    s = lib()
+    x, w = draw(1, (40, 1000), torch.float32), draw(2, (1000,), torch.float32)
+    w = (w.double() * 2.0 ** (power + 5)).float()                            # quotients around 32, some beyond 127
+    scale = torch.tensor([1.1 * 2.0 ** power], dtype=torch.float64).float().to(DEV)
+    n, _, bound = ref.norm(host(x), host(w))
+    codes, _, _ = s.rms_norm_i8(x, w, scale=scale)
+    quotient = n / host(scale)
+    # (at the lower end products and n are subnormal: off by 2^-149 each, 2^-23 of the scale)
+    off = np.abs(codes.cpu().numpy() - np.clip(quotient, -127, 127))
+    assert np.all(off <= 0.5 + 2.0 ** -20 + np.minimum(np.abs(quotient), 128) * (np.max(bound / np.abs(n)) + 2 * ref.E))
+    assert np.abs(codes.cpu().numpy()).max() == 127 and (np.abs(quotient) < 60).any()
