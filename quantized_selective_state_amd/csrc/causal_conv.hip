@@ -83,7 +83,7 @@ __device__ __forceinline__ void load_weights(const float* __restrict__ weight, c
 // the output of one row: the window holds the W - 1 rows before `now`, oldest first
 template <typename T, int W>
 __device__ __forceinline__ Taps<T> convolve(const Taps<T> (&window)[W - 1], const Taps<T>& now, const float (&w)[V][W],
-                                            const float (&b)[V], bool silu) {
+                                            const float (&b)[V], bool activate) {
   Taps<T> r;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ Taps<T> convolve(const Taps<T> (&window)[W - 1], cons
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k) a = fmaf(w[i][k], to_f32(window[k].e[i]), a);
     a = fmaf(w[i][W - 1], to_f32(now.e[i]), a);
-    if (silu) a *= __builtin_amdgcn_rcpf(1.f + exp_f32<__is_same(T, float)>(-a));
+    if (activate) a = silu<__is_same(T, float)>(a);
     r.e[i] = from_f32<T>(a);
   }
   return r;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(T* __restric
                                                                     const float* __restrict__ weight,
                                                                     const float* __restrict__ bias, T* __restrict__ out,
                                                                     uint32_t units, FastDiv packs, int32_t channels,
-                                                                    bool silu) {
+                                                                    bool activate) {
   const uint32_t unit = blockIdx.x * kThreads + threadIdx.x;
   if (unit >= units) return;
   const uint32_t s = fdiv(unit, packs);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) causal_conv_step_kernel(T* __restric
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k) window[k] = load_taps(rows + int64_t(k) * channels, count);
   const Taps<T> now = load_taps(x + int64_t(s) * channels + c, count);
-  store_taps(out + int64_t(s) * channels + c, count, convolve<T, W>(window, now, w, b, silu));
+  store_taps(out + int64_t(s) * channels + c, count, convolve<T, W>(window, now, w, b, activate));
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k) store_taps(rows + int64_t(k) * channels, count, k + 2 < W ? window[k + 1] : now);
 }

@@ -35,6 +35,11 @@ __device__ __forceinline__ float exp_f32(float x) {
   return fabsf(hi) < 128.f ? fmaf(e, lo * kLn2, e) : e;
 }
 
+// v / (1 + exp(-v)), by the hardware's reciprocal as it is: with EXACT within 4 * 2^-24 of itself (3.5 measured), else as
+// exp_f32 and two more.
+template <bool EXACT>
+__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + exp_f32<EXACT>(-v)); }
+
 // A logit's two sigmoids, a and 1 - a, as one number: the smaller of them (which keeps its relative precision), with
 // the logit's sign.
 template <bool EXACT>

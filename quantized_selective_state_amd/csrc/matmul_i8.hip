@@ -50,7 +50,6 @@ __device__ __forceinline__ v4i load_codes(const int8_t* __restrict__ row, int32_
 // tokens.  kAny: rows may start at any byte (1 x 8190 x 4096 19 us; by tiles 63).
 constexpr int kLine = 128, kLinesAhead = 4;
 constexpr int kStreamWaves = 16;              // at most
-constexpr uint32_t kNowhere = 0x80000000u;    // an offset that no buffer reaches: loads as zero
 
 __device__ __forceinline__ v4i load_piece(Rsrc r, uint32_t offset) { return __builtin_bit_cast(v4i, buf_load16(r, offset)); }
 
@@ -79,7 +78,7 @@ __global__ void __launch_bounds__(kStreamWaves* kWave)
       const bool some = line < lines;
       line += turn;
       if (line >= lines) line -= lines;
-      const uint32_t at = some ? uint32_t(line) * kLine + (lane / 16) * 32 : kNowhere;
+      const uint32_t at = some ? uint32_t(line) * kLine + (lane / 16) * 32 : kOutOfRange;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool in = at + h * 16 < uint32_t(k);
@@ -89,9 +88,9 @@ __global__ void __launch_bounds__(kStreamWaves* kWave)
 #pragma unroll
           for (int i = 0; i < MT; ++i) fa[l][i][h] = load_codes(a + int64_t(min(16 * i + lane % 16, m - 1)) * k, from, k);
         } else {
-          fb[l][h] = load_piece(rb, in ? row_at[0] + at + h * 16 : kNowhere);
+          fb[l][h] = load_piece(rb, in ? row_at[0] + at + h * 16 : kOutOfRange);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_piece(ra, in ? row_at[i] + at + h * 16 : kNowhere);
+          for (int i = 0; i < MT; ++i) fa[l][i][h] = load_piece(ra, in ? row_at[i] + at + h * 16 : kOutOfRange);
         }
       }
     }
@@ -221,7 +220,7 @@ struct Loader {
   __device__ __forceinline__ void operator()(int8_t* stage) {
     int8_t* to = stage + wave * 1024;
     const uint32_t at = uint32_t(slab) * kSlab + piece;
-    const uint32_t from = at < uint32_t(a.k) ? row_at + at : kNowhere, step = uint32_t(kWaves * kRows) * uint32_t(a.k);
+    const uint32_t from = at < uint32_t(a.k) ? row_at + at : kOutOfRange, step = uint32_t(kWaves * kRows) * uint32_t(a.k);
 #pragma unroll
     for (int i = 0; i < LA; ++i) load_to_lds(ra, to + i * kWaves * 1024, from + i * step);
 #pragma unroll

@@ -74,9 +74,6 @@ __device__ __forceinline__ Eight<T> rounded(const float (&v)[V]) {
   return r;
 }
 
-template <bool EXACT>
-__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + exp_f32<EXACT>(-v)); }
-
 struct NormKernelArgs {
   const void* x;
   const void* other;        // residual or gate
