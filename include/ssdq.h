@@ -756,7 +756,8 @@ int32_t ssdq_selective_scan_plan(int32_t sequences, int64_t tokens, int32_t chan
  * fewer than 2^23 pieces that the kernels walk the sequences in: 16 to 256 tokens of a sequence each, or a whole one
  * (else SSDQ_ERROR_UNSUPPORTED; the workspace's size is 0 then).  With tokens == 0 the (tokens, ...) pointers are not
  * looked at.  No output overlaps an input or another output.  A NaN or an infinity in u, delta or h0 stays in its sequence
- * and channel, one in B or C in its sequence, one in z in its element.  exp(d A) above 1 (A above 0) is allowed as long as
+ * and channel, one in B or C in its sequence, one in z in its element; behind an infinity (or where d u overflows) y may be a
+ * NaN where the formula has an infinity.  exp(d A) above 1 (A above 0) is allowed as long as
  * products of it over 256 neighbouring tokens stay finite.  The result does not depend on timing: calls with the same
  * arguments give the same bits.
  */

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(WM * WN * kSplit * kWave) tile_kernel(TileArgs
 // Inner sizes of any number of codes: rows may start at any byte, so the pieces pass through registers, those of the next
 // slabs while the current one is multiplied (loads of 16 bytes at any address, which take five times as long as aligned
 // ones and bound the kernel; the aligned words that hold them, shifted, take longer still: 777 x 1531 x 1000 18.2 us
-// against 14.8).  A row's last slab is loaded code by code.  Square tiles, 4 waves, of 128 once there is one for every
+// against 15.3).  A row's last slab is loaded code by code.  Square tiles, 4 waves, of 128 once there is one for every
 // compute unit (8192 x 4097 x 8192 501 us, 862 with 64), else of 64; those no more than compute units in two halves of
 // the inner axis as above (777 x 1531 x 1000 14.8 and 13.8 us so, 64 x 8190 x 4096 46.5 and 37.2, 300 x 100 x 700 9.7 and
 // 9.8).
@@ -533,7 +533,9 @@ hipError_t launch_tiles(const MatmulArgs& a, const Epilogue& ep, int per_unit, h
 }
 
 // Which tiles: the fewest microseconds by rounds x slabs x the time of a slab, where a round is as many tiles as the device
-// holds at once and the times are those measured with all compute units at work.
+// holds at once with 16-bit output and the times are those measured with all compute units at work.  (With fp32 output a
+// block of 128 x 64 tiles has 82944 bytes of LDS, of which a compute unit holds one and not two; its rounds count as if it
+// held two: 1024 x 4096 x 4096 34 to 37 us, with fp16 output 23.5; 128 x 4096 x 18560 32 to 33 and 21.8.)
 struct Candidate { int32_t plan; int tm, tn, per_unit; float slab_us; };
 constexpr Candidate kCandidates[] = {{SSDQ_MATMUL_TILES_256X256, 256, 256, 1, 1.80f}, {SSDQ_MATMUL_TILES_128X128, 128, 128, 2, 1.06f},
                                      {SSDQ_MATMUL_TILES_128X64, 128, 64, 2, 0.68f}, {SSDQ_MATMUL_TILES_64X64, 64, 64, 2, 0.50f}};

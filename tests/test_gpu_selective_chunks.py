@@ -164,3 +164,21 @@ def test_rows_past_32_bit_offsets(packed):
                                                         None, host(h0[s:s + 1].index_select(1, pick)), 1, None)
         close(y[rows].index_select(1, pick), want, wrong, torch.bfloat16, f"y {s}")
         close(final[s:s + 1].index_select(1, pick), want_final, wrong_final, torch.float32, f"h_final {s}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 5, 13, 20, 41])
+def test_an_infinity_stays_in_its_channel_with_any_number_of_states(n):
+    """Whole and in chunks; numbers of states that the kernels fill up."""
+    for sequences, tokens, channels in ((2, 2002, 2200), (60, 600, 1100)):
+        d = Wide(n, "f32", sequences, tokens, channels, n)
+        y, final = d.run()
+        half = tokens // sequences // 2
+        d.u[1, half, 3] = float("inf")
+        got, got_final = d.run()
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        bad[1, half:, 3] = True
+        assert not torch.isfinite(got[bad]).any() and torch.equal(got[~bad], y[~bad])
+        assert not torch.isfinite(got_final[1, 3]).any()
+        got_final[1, 3] = final[1, 3]
+        assert torch.equal(got_final, final)
